@@ -62,7 +62,8 @@ typedef enum {
   JOLT_ERR_UNSUPPORTED = 9        /* valid request outside what the library implements */
 } jolt_status;
 
-typedef enum { JOLT_BF16 = 0, JOLT_F32 = 1 } jolt_dtype;
+/* JOLT_F16: page sets and their rows only (the codec's caches are BF16 or F32). */
+typedef enum { JOLT_BF16 = 0, JOLT_F32 = 1, JOLT_F16 = 2 } jolt_dtype;
 
 typedef enum { JOLT_ENC_AUTO = 0, JOLT_ENC_EXACT = 1, JOLT_ENC_SKETCH = 2 } jolt_encoder;
 
@@ -188,6 +189,118 @@ JOLT_API jolt_status jolt_decode(jolt_stream_t stream, void* K_out, void* V_out,
  */
 JOLT_API jolt_status jolt_attention(jolt_stream_t stream, const void* Q, int32_t q_heads, int32_t n_queries,
                                     float scale, float* out, void* cuda_stream);
+
+/* ---------------------------------------------------------------- the growing cache
+ * The codec compresses a cache that is complete; these entry points serve the part of a context
+ * that still grows: query and key rows normed and rotated, keys and values appended to a paged
+ * cache, and attention of new tokens over it, optionally joined with the attention over another
+ * part of the context (for instance the compressed part, jolt_attention_lse). They have no
+ * counterpart in the method's pages.
+ *
+ * A page set is two device tensors [num_pages][heads][page_size][head_dim], keys and values, owned
+ * by the caller. A sequence's token p is row p % page_size of the page page_table[s][p / page_size].
+ * A batch is a list of sequences, each with a chunk of new tokens (1 while generating, many in a
+ * prompt): tokens q_start[s] .. q_start[s + 1] - 1 of the batch's rows are the last ones of the
+ * kv_len[s] tokens that the sequence has in its pages. Rows behind q_start[num_seqs] belong to no
+ * sequence (a padded batch) and their outputs are left as they were.
+ *
+ * The batch's arrays live on the device, nothing is read back and no call waits for the device, so
+ * every call but jolt_pages_create and jolt_pages_status can be captured in a CUDA graph and
+ * replayed with new array contents. Calls on one page set may overlap on several CUDA streams
+ * where their data allows it; scratch is taken per call from the library's memory pool.
+ *
+ * What the host cannot check is checked on the device and reported by jolt_pages_status: a sequence
+ * whose bounds do not fit (offsets that fall or leave [0, total_q], more than max_q tokens, kv_len
+ * outside [0, max_pages * page_size]) is skipped, a table entry that is no page of the set is never
+ * followed (its keys count as zeros in attention and are not written by append). Entries behind
+ * the pages of kv_len tokens are not read and may hold anything, and so may the rows of the last
+ * page behind kv_len; the rows before kv_len have to be finite.
+ * Supported: head_dim 128, page_size a multiple of 16, BF16 and F16.
+ */
+typedef struct jolt_pages_s* jolt_pages_t;
+
+typedef struct {
+  int32_t num_pages, heads, page_size, head_dim;
+  jolt_dtype dtype;
+} jolt_page_shape;
+
+typedef struct {
+  int32_t num_seqs;            /* sequences */
+  int32_t total_q;             /* rows of the batch's tensors, padded rows included */
+  int32_t max_q;               /* the longest chunk that may occur */
+  int32_t max_pages;           /* columns of page_table */
+  const int32_t* q_start;      /* device [num_seqs + 1] */
+  const int32_t* kv_len;       /* device [num_seqs], the chunk's tokens included */
+  const int32_t* page_table;   /* device [num_seqs][max_pages] */
+} jolt_batch;
+
+/*
+ * jolt_pages_create - describe a page set to the library. K_pages, V_pages: device, 16-byte
+ *   aligned. The device that is current becomes the set's; calls on it need that device current.
+ *   Not to be captured. Errors: INVALID_ARG, OOM, CUDA, UNSUPPORTED (dtype, page_size).
+ */
+JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pages, void* V_pages,
+                                       void* cuda_stream, jolt_pages_t* out);
+
+/* Synchronise `cuda_stream`, report what the device found wrong in the batches of the set's calls
+ * since the last report (INVALID_ARG with a message, TIMEOUT) and clear it. */
+JOLT_API jolt_status jolt_pages_status(jolt_pages_t pages, void* cuda_stream);
+
+/* Release the description (the tensors stay the caller's) after the set's calls have finished. */
+JOLT_API void jolt_pages_destroy(jolt_pages_t pages);
+
+/*
+ * jolt_qk_norm_rope - norms of queries and keys for each head with the position rotation, in one
+ *   pass: y = w * x / sqrt(mean(x^2) + eps) over the 128 features of a row (left out where the
+ *   weight is NULL), then for i < rope_dim / 2, a = position * inv_freq[i] (float64):
+ *   (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a), j = i + rope_dim / 2, or pairs
+ *   (2 i, 2 i + 1) when interleaved. float32 inside, rounded once.
+ * Q, K: device [tokens][heads][128] of `dtype`, element strides as given (multiples of 8; rows
+ *   contiguous and 16-byte aligned); K may be NULL with k_heads 0. Q_out, K_out: the same, or the
+ *   inputs themselves. q_weight, k_weight: device [128] of `dtype`, or NULL. positions: device int32
+ *   [tokens]; inv_freq: device float32 [rope_dim / 2], rope_dim a multiple of 16 up to 128; both
+ *   NULL for no rotation.
+ */
+JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const void* Q, int64_t q_token_stride,
+                                       int64_t q_head_stride, int32_t q_heads, const void* q_weight, void* Q_out,
+                                       int64_t qo_token_stride, int64_t qo_head_stride, const void* K,
+                                       int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads,
+                                       const void* k_weight, void* K_out, int64_t ko_token_stride,
+                                       int64_t ko_head_stride, float eps, const int32_t* positions,
+                                       const float* inv_freq, int32_t rope_dim, int32_t interleaved,
+                                       void* cuda_stream);
+
+/*
+ * jolt_paged_append - write the keys and values of a batch's new tokens to their places in the
+ *   pages, the keys normed (k_weight, or NULL) and rotated (inv_freq, or NULL) on the way as in
+ *   jolt_qk_norm_rope. K, V: device [total_q][heads][128] of the set's dtype, element strides as
+ *   there. positions: the rotation's positions [total_q], or NULL for the token's index in its
+ *   sequence's pages. A token before the cache's begin (kv_len smaller than the chunk) is dropped.
+ *   Two tokens of one batch must not share a place.
+ */
+JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* batch, const void* K,
+                                       int64_t k_token_stride, int64_t k_head_stride, const void* V,
+                                       int64_t v_token_stride, int64_t v_head_stride, const void* k_weight, float eps,
+                                       const int32_t* positions, const float* inv_freq, int32_t rope_dim,
+                                       int32_t interleaved, void* cuda_stream);
+
+/*
+ * jolt_paged_attention - attention of a batch's new tokens over the pages, grouped-query as in
+ *   jolt_attention: for token i of a chunk of n and query head j reading KV head j / (q_heads / heads),
+ *       out = sum_t e^(s_t) V[t] / sum_t e^(s_t),  s_t = scale * Q . K[t],
+ *   over t <= kv_len - n + i (causal) or all t < kv_len (causal = 0). The chunk's own keys have to be
+ *   appended before. prefix_out, prefix_lse: the attention of the same queries over another part of
+ *   the context and the log of its sum of exponentials (both or neither): joined as a term
+ *   e^(prefix_lse) of value prefix_out. A row without keys gets out = 0 and lse = -inf.
+ * Q: device [total_q][q_heads][128] of the set's dtype, element strides as above. out: device
+ *   [total_q][q_heads][128] of that dtype; lse: device float32 [total_q][q_heads], the log of the
+ *   sum of exponentials, prefix included, or NULL. prefix_out, prefix_lse: device float32
+ *   [total_q][q_heads][128] and [total_q][q_heads], or NULL. All four contiguous, 16-byte aligned.
+ */
+JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* batch, const void* Q,
+                                          int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads, float scale,
+                                          int32_t causal, const float* prefix_out, const float* prefix_lse, void* out,
+                                          float* lse, void* cuda_stream);
 
 /*
  * jolt_rel_frob_error - ||ref - approx||_F / ||ref||_F over n elements (the error measure the

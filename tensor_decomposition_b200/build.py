@@ -29,11 +29,11 @@ def nvcc() -> str:
 
 
 def sources():
-    return [os.path.join(CSRC, "jolt_api.cpp")] + sorted(glob.glob(os.path.join(CSRC, "kernels", "*.cu")))
+    return [os.path.join(CSRC, "jolt_api.cpp"), os.path.join(CSRC, "paged_api.cpp")] + sorted(glob.glob(os.path.join(CSRC, "kernels", "*.cu")))
 
 
 def headers():
-    return glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    return glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "kernels", "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def _flags(src: str):

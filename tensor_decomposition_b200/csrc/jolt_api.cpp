@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "jolt_internal.h"
+#include "paged.h"
 #include "kernels/gemm_tc.h"
 
 using namespace jolt;
@@ -217,6 +218,29 @@ cudaError_t pool_malloc(T** ptr, size_t bytes, cudaStream_t s) {
   return pool_malloc(reinterpret_cast<void**>(ptr), bytes, s);
 }
 }  // namespace
+
+// Services of this file for the other host files (paged.h).
+namespace jolt {
+jolt_status host_fail(jolt_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+void host_clear_error() { g_err.clear(); }
+cudaError_t host_pool_malloc(void** ptr, size_t bytes, cudaStream_t s) { return pool_malloc(ptr, bytes, s); }
+cudaError_t host_dev_malloc(void** ptr, size_t bytes) { return dev_malloc(ptr, bytes); }
+void* host_prof_begin(const char* name, cudaStream_t s) {
+  {
+    std::lock_guard<std::mutex> g(g_prof_mu);
+    if (!g_prof_on) return nullptr;
+  }
+  return new (std::nothrow) Prof(name, s);
+}
+void host_prof_end(void* token) { delete static_cast<Prof*>(token); }
+}  // namespace jolt
 
 // ============================================================================ objects
 struct jolt_plan_s {

@@ -1,0 +1,295 @@
+// Host side of the growing cache (include/jolt.h): page sets, argument checks and launches.
+#include <mutex>
+#include <new>
+#include <vector>
+
+#include "paged.h"
+
+using namespace jolt;
+
+struct jolt_pages_s {
+  jolt_page_shape shape{};
+  void *K = nullptr, *V = nullptr;
+  int device = 0;
+  int32_t* d_status = nullptr;
+};
+
+namespace {
+
+// Status words of page sets: slabs of them per device, allocated once and handed out again, so that
+// creating and destroying a set allocates and frees nothing (a destructor may run while another
+// thread captures a graph, where freeing is an error).
+constexpr int kSlab = 1024;
+constexpr int kDevices = 64;
+std::mutex g_slot_mu;
+std::vector<int32_t*> g_free_slots[kDevices];
+
+cudaError_t take_slot(int dev, int32_t** out) {
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> g(g_slot_mu);
+  auto& fr = g_free_slots[dev];
+  if (fr.empty()) {
+    void* p = nullptr;
+    const cudaError_t e = host_dev_malloc(&p, kSlab * sizeof(int32_t));
+    if (e != cudaSuccess) return e;
+    try {
+      fr.reserve(fr.capacity() + kSlab);   // also what giving slots back needs
+    } catch (...) {
+      cudaFree(p);
+      return cudaErrorMemoryAllocation;
+    }
+    for (int i = kSlab - 1; i >= 0; --i) fr.push_back(static_cast<int32_t*>(p) + i);
+  }
+  *out = fr.back();
+  fr.pop_back();
+  return cudaSuccess;
+}
+void give_slot(int dev, int32_t* p) {
+  std::lock_guard<std::mutex> g(g_slot_mu);
+  g_free_slots[dev].push_back(p);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+struct ProfScope {
+  ProfScope(const char* name, cudaStream_t s) : token(host_prof_begin(name, s)) {}
+  ~ProfScope() {
+    if (token) host_prof_end(token);
+  }
+  void* token;
+};
+
+jolt_status cuda_fail(const char* what, cudaError_t e) {
+  return host_fail(e == cudaErrorMemoryAllocation ? JOLT_ERR_OOM : JOLT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// Strides of a rows tensor: rows of 128 contiguous elements on 16-byte boundaries.
+jolt_status check_rows(const char* what, const char* name, const void* p, int64_t ts, int64_t hs, int32_t heads) {
+  if (heads <= 0) return host_fail(JOLT_ERR_INVALID_ARG, "%s: %s has no heads", what, name);
+  if (!p) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null %s", what, name);
+  if (!aligned16(p) || ts % 8 || hs % 8)
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: %s rows must start on 16-byte boundaries (strides a multiple of 8)", what,
+                     name);
+  return JOLT_OK;
+}
+
+jolt_status check_rope(const char* what, const int32_t* positions, bool positions_needed, const float* inv_freq,
+                       int32_t rope_dim) {
+  if (!inv_freq) return JOLT_OK;
+  if (positions_needed && !positions) return host_fail(JOLT_ERR_INVALID_ARG, "%s: inv_freq without positions", what);
+  if (rope_dim <= 0 || rope_dim > kD || rope_dim % 16)
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: rope_dim %d is not a multiple of 16 in [16, %d]", what, rope_dim, kD);
+  return JOLT_OK;
+}
+
+jolt_status check_batch(const char* what, const jolt_pages_s* pg, const jolt_batch* b) {
+  if (!pg || !b) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null pages or batch", what);
+  if (b->num_seqs < 0 || b->total_q < 0 || b->max_q < 0 || b->max_pages < 0)
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: negative batch size", what);
+  if (b->num_seqs > 0 && (!b->q_start || !b->kv_len || (b->max_pages > 0 && !b->page_table)))
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: null q_start, kv_len or page_table", what);
+  if ((int64_t)b->max_pages * pg->shape.page_size > INT32_MAX - 1024)
+    return host_fail(JOLT_ERR_UNSUPPORTED, "%s: page tables of more than 2^31 tokens", what);
+  return JOLT_OK;
+}
+
+jolt_status check_device(const char* what, const jolt_pages_s* pg) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(what, e);
+  if (dev != pg->device)
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: the page set is on device %d, the current device is %d", what, pg->device,
+                     dev);
+  return JOLT_OK;
+}
+
+BatchView view_of(const jolt_pages_s* pg, const jolt_batch* b) {
+  BatchView v{};
+  v.num_seqs = b->num_seqs;
+  v.total_q = b->total_q;
+  v.max_q = b->max_q;
+  v.max_pages = b->max_pages;
+  v.q_start = b->q_start;
+  v.kv_len = b->kv_len;
+  v.page_table = b->page_table;
+  v.num_pages = pg->shape.num_pages;
+  v.heads = pg->shape.heads;
+  v.page_size = pg->shape.page_size;
+  v.status = pg->d_status;
+  return v;
+}
+
+RopeArgs rope_of(float eps, const int32_t* positions, const float* inv_freq, int32_t rope_dim, int32_t interleaved) {
+  RopeArgs r;
+  r.positions = positions;
+  r.inv_freq = inv_freq;
+  r.rope_dim = inv_freq ? rope_dim : 0;
+  r.interleaved = interleaved != 0;
+  r.eps = eps;
+  return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pages, void* V_pages, void* cuda_stream,
+                                       jolt_pages_t* out) {
+  host_clear_error();
+  if (!shape || !out) return host_fail(JOLT_ERR_INVALID_ARG, "jolt_pages_create: null shape or out");
+  *out = nullptr;
+  const jolt_page_shape& sh = *shape;
+  if (sh.num_pages <= 0 || sh.heads <= 0 || sh.page_size <= 0)
+    return host_fail(JOLT_ERR_INVALID_ARG, "jolt_pages_create: non-positive dimension");
+  if (sh.head_dim != kD)
+    return host_fail(JOLT_ERR_INVALID_ARG, "jolt_pages_create: head_dim %d unsupported (supported: 128)", sh.head_dim);
+  if (sh.dtype != JOLT_BF16 && sh.dtype != JOLT_F16)
+    return host_fail(JOLT_ERR_UNSUPPORTED, "jolt_pages_create: pages are bf16 or f16");
+  if (sh.page_size % 16 || sh.page_size > (1 << 24))
+    return host_fail(JOLT_ERR_UNSUPPORTED, "jolt_pages_create: page_size %d is not a multiple of 16 up to 2^24",
+                     sh.page_size);
+  if ((int64_t)sh.heads * sh.page_size * (2 * kD) >= (1ll << 40))
+    return host_fail(JOLT_ERR_UNSUPPORTED, "jolt_pages_create: a page of 2^40 bytes or more");
+  if (!K_pages || !V_pages) return host_fail(JOLT_ERR_INVALID_ARG, "jolt_pages_create: null pages");
+  if (!aligned16(K_pages) || !aligned16(V_pages))
+    return host_fail(JOLT_ERR_INVALID_ARG, "jolt_pages_create: pages must be 16-byte aligned");
+  jolt_pages_s* p = new (std::nothrow) jolt_pages_s();
+  if (!p) return host_fail(JOLT_ERR_OOM, "jolt_pages_create: host allocation");
+  p->shape = sh;
+  p->K = K_pages;
+  p->V = V_pages;
+  cudaError_t e = cudaGetDevice(&p->device);
+  if (e == cudaSuccess) e = take_slot(p->device, &p->d_status);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p->d_status, 0, sizeof(int32_t), (cudaStream_t)cuda_stream);
+  if (e != cudaSuccess) {
+    if (p->d_status) give_slot(p->device, p->d_status);
+    delete p;
+    return cuda_fail("jolt_pages_create", e);
+  }
+  *out = p;
+  return JOLT_OK;
+}
+
+JOLT_API void jolt_pages_destroy(jolt_pages_t p) {
+  if (!p) return;
+  give_slot(p->device, p->d_status);
+  delete p;
+}
+
+JOLT_API jolt_status jolt_pages_status(jolt_pages_t p, void* cuda_stream) {
+  host_clear_error();
+  if (!p) return host_fail(JOLT_ERR_INVALID_ARG, "jolt_pages_status: null pages");
+  if (jolt_status st = check_device("jolt_pages_status", p)) return st;
+  cudaStream_t s = (cudaStream_t)cuda_stream;
+  int32_t w = 0;
+  cudaError_t e = cudaMemcpyAsync(&w, p->d_status, sizeof(w), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p->d_status, 0, sizeof(w), s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_fail("jolt_pages_status", e);
+  if (w & PST_TIMEOUT) return host_fail(JOLT_ERR_TIMEOUT, "a bounded device wait of paged attention gave up");
+  if (w & PST_BAD_BATCH)
+    return host_fail(JOLT_ERR_INVALID_ARG, "a sequence's q_start or kv_len does not fit its batch (the sequence was skipped)");
+  if (w & PST_BAD_PAGE)
+    return host_fail(JOLT_ERR_INVALID_ARG, "a page table names a page outside the set (it was not followed)");
+  return JOLT_OK;
+}
+
+JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const void* Q, int64_t q_token_stride,
+                                       int64_t q_head_stride, int32_t q_heads, const void* q_weight, void* Q_out,
+                                       int64_t qo_token_stride, int64_t qo_head_stride, const void* K,
+                                       int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads,
+                                       const void* k_weight, void* K_out, int64_t ko_token_stride,
+                                       int64_t ko_head_stride, float eps, const int32_t* positions,
+                                       const float* inv_freq, int32_t rope_dim, int32_t interleaved,
+                                       void* cuda_stream) {
+  const char* what = "jolt_qk_norm_rope";
+  host_clear_error();
+  if (dtype != JOLT_BF16 && dtype != JOLT_F16) return host_fail(JOLT_ERR_UNSUPPORTED, "%s: rows are bf16 or f16", what);
+  if (tokens < 0 || k_heads < 0) return host_fail(JOLT_ERR_INVALID_ARG, "%s: negative size", what);
+  if (tokens == 0) return JOLT_OK;
+  jolt_status st = check_rows(what, "Q", Q, q_token_stride, q_head_stride, q_heads);
+  if (st == JOLT_OK) st = check_rows(what, "Q_out", Q_out, qo_token_stride, qo_head_stride, q_heads);
+  if (st == JOLT_OK && k_heads > 0) st = check_rows(what, "K", K, k_token_stride, k_head_stride, k_heads);
+  if (st == JOLT_OK && k_heads > 0) st = check_rows(what, "K_out", K_out, ko_token_stride, ko_head_stride, k_heads);
+  if (st == JOLT_OK) st = check_rope(what, positions, true, inv_freq, rope_dim);
+  if (st != JOLT_OK) return st;
+  if (!aligned16(q_weight) || !aligned16(k_weight))
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: weights must be 16-byte aligned", what);
+  RowsIn q, k;
+  RowsOut qo, ko;
+  q.p = Q; q.ts = q_token_stride; q.hs = q_head_stride; q.heads = q_heads; q.w = q_weight;
+  qo.p = Q_out; qo.ts = qo_token_stride; qo.hs = qo_head_stride;
+  if (k_heads > 0) {
+    k.p = K; k.ts = k_token_stride; k.hs = k_head_stride; k.heads = k_heads; k.w = k_weight;
+    ko.p = K_out; ko.ts = ko_token_stride; ko.hs = ko_head_stride;
+  }
+  cudaStream_t s = (cudaStream_t)cuda_stream;
+  ProfScope prof("qk_norm_rope", s);
+  const cudaError_t e = norm_rope(dtype, tokens, q, qo, k, ko, rope_of(eps, positions, inv_freq, rope_dim, interleaved), s);
+  return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
+}
+
+JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* batch, const void* K,
+                                       int64_t k_token_stride, int64_t k_head_stride, const void* V,
+                                       int64_t v_token_stride, int64_t v_head_stride, const void* k_weight, float eps,
+                                       const int32_t* positions, const float* inv_freq, int32_t rope_dim,
+                                       int32_t interleaved, void* cuda_stream) {
+  const char* what = "jolt_paged_append";
+  host_clear_error();
+  jolt_status st = check_batch(what, pages, batch);
+  if (st != JOLT_OK) return st;
+  const int H = pages->shape.heads;
+  if (batch->total_q == 0 || batch->num_seqs == 0) return JOLT_OK;
+  st = check_rows(what, "K", K, k_token_stride, k_head_stride, H);
+  if (st == JOLT_OK) st = check_rows(what, "V", V, v_token_stride, v_head_stride, H);
+  if (st == JOLT_OK) st = check_rope(what, positions, false, inv_freq, rope_dim);
+  if (st != JOLT_OK) return st;
+  if (!aligned16(k_weight)) return host_fail(JOLT_ERR_INVALID_ARG, "%s: the weight must be 16-byte aligned", what);
+  st = check_device(what, pages);
+  if (st != JOLT_OK) return st;
+  RowsIn k, v;
+  k.p = K; k.ts = k_token_stride; k.hs = k_head_stride; k.heads = H; k.w = k_weight;
+  v.p = V; v.ts = v_token_stride; v.hs = v_head_stride; v.heads = H;
+  cudaStream_t s = (cudaStream_t)cuda_stream;
+  ProfScope prof("paged_append", s);
+  const cudaError_t e = paged_append(pages->shape.dtype, view_of(pages, batch), k, v, pages->K, pages->V,
+                                     rope_of(eps, positions, inv_freq, rope_dim, interleaved), s);
+  return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
+}
+
+JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* batch, const void* Q,
+                                          int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads, float scale,
+                                          int32_t causal, const float* prefix_out, const float* prefix_lse, void* out,
+                                          float* lse, void* cuda_stream) {
+  const char* what = "jolt_paged_attention";
+  host_clear_error();
+  jolt_status st = check_batch(what, pages, batch);
+  if (st != JOLT_OK) return st;
+  if (q_heads <= 0 || q_heads % pages->shape.heads)
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: q_heads must be a positive multiple of the %d KV heads", what,
+                     pages->shape.heads);
+  if (!prefix_out != !prefix_lse)
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: prefix_out and prefix_lse come together", what);
+  if (batch->total_q == 0 || batch->num_seqs == 0) return JOLT_OK;
+  st = check_rows(what, "Q", Q, q_token_stride, q_head_stride, q_heads);
+  if (st != JOLT_OK) return st;
+  if (!out) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null out", what);
+  if (!aligned16(out) || !aligned16(prefix_out))
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: out and prefix_out must be 16-byte aligned", what);
+  st = check_device(what, pages);
+  if (st != JOLT_OK) return st;
+  PagedAttnArgs a{};
+  a.b = view_of(pages, batch);
+  a.dtype = pages->shape.dtype;
+  a.K = pages->K; a.V = pages->V;
+  a.Q = Q; a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.Hq = q_heads;
+  a.scale = scale; a.causal = causal != 0;
+  a.pre_out = prefix_out; a.pre_lse = prefix_lse;
+  a.out = out; a.lse = lse;
+  cudaStream_t s = (cudaStream_t)cuda_stream;
+  ProfScope prof("paged_attention", s);
+  const cudaError_t e = paged_attention(a, s);
+  return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
+}
+
+}  // extern "C"

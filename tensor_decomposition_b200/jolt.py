@@ -19,7 +19,7 @@ JOLT_OK = 0
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "BUDGET_INFEASIBLE", 3: "OOM", 4: "CUDA",
                 5: "NOT_CONVERGED", 6: "NONFINITE", 7: "TIMEOUT", 8: "CORRUPT_STREAM",
                 9: "UNSUPPORTED"}
-JOLT_BF16, JOLT_F32 = 0, 1
+JOLT_BF16, JOLT_F32, JOLT_F16 = 0, 1, 2
 JOLT_ENC_AUTO, JOLT_ENC_EXACT, JOLT_ENC_SKETCH = 0, 1, 2
 JOLT_EIG_TRIDIAG, JOLT_EIG_JACOBI = 0, 1
 JOLT_ROT_HAAR, JOLT_ROT_HADAMARD = 0, 1
@@ -32,7 +32,9 @@ EXPORTED = ["jolt_config_default", "jolt_plan", "jolt_plan_info", "jolt_encode",
             "jolt_stream_info", "jolt_stream_to_host", "jolt_stream_from_host", "jolt_export_debug", "jolt_stream_destroy",
             "jolt_plan_destroy", "jolt_last_error", "jolt_profile_enable", "jolt_profile_report",
             "jolt_launch_count", "jolt_alloc_count", "jolt_selftest_gemm_bf16", "jolt_selftest_gemm_bf16_layout",
-            "jolt_selftest_eig_dense", "jolt_selftest_eig_small", "jolt_attention"]
+            "jolt_selftest_eig_dense", "jolt_selftest_eig_small", "jolt_attention", "jolt_pages_create",
+            "jolt_pages_status", "jolt_pages_destroy", "jolt_qk_norm_rope", "jolt_paged_append",
+            "jolt_paged_attention"]
 
 
 class JoltError(RuntimeError):
@@ -55,11 +57,23 @@ class Config(ctypes.Structure):
                 ("eig_solver", ctypes.c_int32)]
 
 
+class PageShape(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class BatchDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_q", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m tensor_decomposition_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, u64, i32, st = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32, ctypes.c_int
+    i64, f32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "jolt_config_default": (None, [ctypes.POINTER(Config)]),
         "jolt_plan": (st, [ctypes.POINTER(Shape), u64, i32, ctypes.POINTER(Config), ctypes.POINTER(vp)]),
@@ -86,6 +100,13 @@ def _load():
         "jolt_selftest_eig_dense": (st, [i32, i32, i32, vp, vp, vp, vp]),
         "jolt_selftest_eig_small": (st, [i32, i32, vp, vp, vp, i32, vp]),
         "jolt_attention": (st, [vp, vp, i32, i32, ctypes.c_float, vp, vp]),
+        "jolt_pages_create": (st, [ctypes.POINTER(PageShape), vp, vp, vp, ctypes.POINTER(vp)]),
+        "jolt_pages_status": (st, [vp, vp]),
+        "jolt_pages_destroy": (None, [vp]),
+        "jolt_qk_norm_rope": (st, [i32, i32, vp, i64, i64, i32, vp, vp, i64, i64, vp, i64, i64, i32, vp, vp, i64, i64,
+                                   f32, vp, vp, i32, i32, vp]),
+        "jolt_paged_append": (st, [vp, vp, vp, i64, i64, vp, i64, i64, vp, f32, vp, vp, i32, i32, vp]),
+        "jolt_paged_attention": (st, [vp, vp, vp, i64, i64, i32, f32, i32, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -294,3 +315,162 @@ def jolt_attention(stream: Stream, Q, out, scale: float, cuda_stream=None):
         raise ValueError("Q and out must be [layers][q_heads][n][head_dim] of the same shape")
     _check(_lib.jolt_attention(stream.handle, _dptr(Q), int(Q.shape[1]), int(Q.shape[2]), float(scale), _dptr(out),
                                _stream_ptr(cuda_stream)))
+
+
+# ------------------------------------------------------------------ the growing cache
+class Pages:
+    """A page set (jolt_pages_create): keeps the page tensors alive."""
+
+    def __init__(self, handle, K_pages, V_pages):
+        self.handle, self.K, self.V = handle, K_pages, V_pages
+        self.heads, self.dtype, self.device = int(K_pages.shape[1]), K_pages.dtype, K_pages.get_device()
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            _lib.jolt_pages_destroy(self.handle)
+            self.handle = None
+
+
+class Batch:
+    """A batch description (jolt_batch): keeps its device arrays alive. Their contents may change
+    between calls, their places may not."""
+
+    def __init__(self, desc, keep):
+        self.desc, self._keep = desc, keep
+        self.ptr = ctypes.addressof(desc)
+        self.total_q, self.device = desc.total_q, keep[0].get_device()
+
+
+def _row_dtype(t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return JOLT_BF16
+    if t.dtype == torch.float16:
+        return JOLT_F16
+    raise ValueError(f"unsupported dtype {t.dtype} (bf16 or f16)")
+
+
+def _here(device):
+    """The tensors' device has to be the current one, as for every entry point."""
+    import torch
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on device {device}, the current device is {torch.cuda.current_device()}")
+
+
+def _rows(t, name, tokens, heads, dtype, device):
+    """(pointer, token stride, head stride) of a [tokens][heads][128] tensor with contiguous rows."""
+    if t.shape != (tokens, heads, 128) or t.dtype != dtype:
+        raise ValueError(f"{name} must be [{tokens}][{heads}][128] {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), s[0] if tokens > 1 else 0, s[1] if heads > 1 else 0
+
+
+def _array(t, name, shape, dtype, device):
+    """Pointer of a contiguous array of the shape, or None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)} on device {device}")
+    return t.data_ptr()
+
+
+def _rope(positions, inv_freq, tokens, device):
+    """(positions pointer, inv_freq pointer, rope_dim)."""
+    import torch
+    if inv_freq is None:
+        return None, None, 0
+    n = inv_freq.numel()
+    return (_array(positions, "positions", (tokens,), torch.int32, device),
+            _array(inv_freq, "inv_freq", (n,), torch.float32, device), 2 * n)
+
+
+def jolt_pages_create(K_pages, V_pages, cuda_stream=None) -> Pages:
+    """K_pages, V_pages: contiguous bf16 or f16 CUDA tensors [num_pages][heads][page_size][128]."""
+    if K_pages.dim() != 4 or V_pages.shape != K_pages.shape or V_pages.dtype != K_pages.dtype:
+        raise ValueError("K_pages and V_pages must be [num_pages][heads][page_size][head_dim] of the same shape and type")
+    k, v = _dptr(K_pages), _dptr(V_pages)
+    _here(K_pages.get_device())
+    if V_pages.get_device() != K_pages.get_device():
+        raise ValueError("K_pages and V_pages must be on one device")
+    sh = PageShape(*K_pages.shape, _row_dtype(K_pages))
+    h = ctypes.c_void_p()
+    _check(_lib.jolt_pages_create(ctypes.byref(sh), k, v, _stream_ptr(cuda_stream), ctypes.byref(h)))
+    return Pages(h, K_pages, V_pages)
+
+
+def jolt_pages_status(pages: Pages, cuda_stream=None):
+    _check(_lib.jolt_pages_status(pages.handle, _stream_ptr(cuda_stream)))
+
+
+def jolt_batch(q_start, kv_len, page_table, total_q: int, max_q: int) -> Batch:
+    """q_start [num_seqs + 1], kv_len [num_seqs], page_table [num_seqs][max_pages]: int32 CUDA tensors.
+    total_q: rows of the batch's tensors; max_q: the longest chunk that may occur."""
+    import torch
+    n, dev = int(kv_len.numel()), kv_len.get_device()
+    if kv_len.dim() != 1 or page_table.dim() != 2 or dev < 0:
+        raise ValueError("kv_len must be a CUDA tensor [num_seqs] and page_table [num_seqs][max_pages]")
+    d = BatchDesc(n, int(total_q), int(max_q), int(page_table.shape[1]),
+                  _array(q_start, "q_start", (n + 1,), torch.int32, dev),
+                  _array(kv_len, "kv_len", (n,), torch.int32, dev),
+                  _array(page_table, "page_table", (n, page_table.shape[1]), torch.int32, dev))
+    return Batch(d, (q_start, kv_len, page_table))
+
+
+def jolt_qk_norm_rope(Q, Q_out, K=None, K_out=None, positions=None, inv_freq=None, q_weight=None, k_weight=None,
+                      eps=1e-6, interleaved=False, cuda_stream=None):
+    """Q, Q_out: [tokens][q_heads][128], K, K_out: [tokens][k_heads][128] (bf16 or f16 CUDA tensors with
+    contiguous rows, any token and head strides that are multiples of 8); an output may be its input."""
+    if Q.dim() != 3:
+        raise ValueError("Q must be [tokens][q_heads][128]")
+    t, dev, n, hq = Q.dtype, Q.get_device(), Q.shape[0], Q.shape[1]
+    _here(dev)
+    dt = _row_dtype(Q)
+    q, qo = _rows(Q, "Q", n, hq, t, dev), _rows(Q_out, "Q_out", n, hq, t, dev)
+    if K is None:
+        hk, k, ko = 0, (None, 0, 0), (None, 0, 0)
+    else:
+        hk = K.shape[1]
+        k, ko = _rows(K, "K", n, hk, t, dev), _rows(K_out, "K_out", n, hk, t, dev)
+    if inv_freq is not None and positions is None:
+        raise ValueError("inv_freq without positions")
+    pos, fr, rd = _rope(positions, inv_freq, n, dev)
+    _check(_lib.jolt_qk_norm_rope(dt, n, *q, hq, _array(q_weight, "q_weight", (128,), t, dev), *qo, *k, hk,
+                                  _array(k_weight, "k_weight", (128,), t, dev), *ko, eps, pos, fr, rd,
+                                  1 if interleaved else 0, _stream_ptr(cuda_stream)))
+
+
+def jolt_paged_append(pages: Pages, batch: Batch, K, V, positions=None, inv_freq=None, k_weight=None, eps=1e-6,
+                      interleaved=False, cuda_stream=None):
+    """K, V: [total_q][heads][128] of the pages' type, contiguous rows, strides multiples of 8."""
+    n, h, t, dev = batch.total_q, pages.heads, pages.dtype, pages.device
+    _here(dev)
+    if batch.device != dev:
+        raise ValueError("the batch's arrays must be on the pages' device")
+    pos, fr, rd = _rope(positions, inv_freq, n, dev)
+    _check(_lib.jolt_paged_append(pages.handle, batch.ptr, *_rows(K, "K", n, h, t, dev), *_rows(V, "V", n, h, t, dev),
+                                  _array(k_weight, "k_weight", (128,), t, dev), eps, pos, fr, rd,
+                                  1 if interleaved else 0, _stream_ptr(cuda_stream)))
+
+
+def jolt_paged_attention(pages: Pages, batch: Batch, Q, out, scale: float, causal=True, lse=None, prefix_out=None,
+                         prefix_lse=None, cuda_stream=None):
+    """Q: [total_q][q_heads][128] of the pages' type with contiguous rows; out: contiguous, same shape and
+    type; lse, prefix_lse: float32 [total_q][q_heads]; prefix_out: float32 [total_q][q_heads][128]."""
+    import torch
+    n, t, dev = batch.total_q, pages.dtype, pages.device
+    if Q.dim() != 3:
+        raise ValueError("Q must be [total_q][q_heads][128]")
+    _here(dev)
+    if batch.device != dev:
+        raise ValueError("the batch's arrays must be on the pages' device")
+    hq = Q.shape[1]
+    _check(_lib.jolt_paged_attention(pages.handle, batch.ptr, *_rows(Q, "Q", n, hq, t, dev), hq, scale,
+                                     1 if causal else 0,
+                                     _array(prefix_out, "prefix_out", (n, hq, 128), torch.float32, dev),
+                                     _array(prefix_lse, "prefix_lse", (n, hq), torch.float32, dev),
+                                     _array(out, "out", (n, hq, 128), t, dev),
+                                     _array(lse, "lse", (n, hq), torch.float32, dev), _stream_ptr(cuda_stream)))

@@ -4,7 +4,7 @@
 // with a part (out0, lse0) attended elsewhere, which counts as one more key of score lse0 and
 // value out0. One warp a query row, lane i features 4 i .. 4 i + 3, one key at a time with a
 // running maximum and sum.
-#include "../paged.h"
+#include "paged_attention.cuh"
 
 namespace jolt {
 namespace {
@@ -73,8 +73,35 @@ __global__ void __launch_bounds__(128) k_paged_attention(const PagedAttnArgs a) 
 
 }  // namespace
 
-cudaError_t paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
-  if (a.b.total_q <= 0 || a.b.num_seqs <= 0) return cudaSuccess;
+namespace {
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+size_t o_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * kD * sizeof(float)); }
+size_t ml_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * sizeof(float2)); }
+}  // namespace
+
+// Rows of a chunk that read one KV head: up to 16 run in the kernel for few rows.
+AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
+  AttnPlan p;
+  const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size;
+  p.decode = (int64_t)a.b.max_q * (a.Hq / a.b.heads) <= 16;
+  if (!p.decode) return p;
+  const int64_t units = std::max<int64_t>(1, (tokens + 63) / 64) * a.b.heads * a.b.num_seqs;
+  p.grid = (int)std::min<int64_t>(2 * (int64_t)sms, units);
+  p.rows = 16;
+  p.bytes = o_bytes(p) + ml_bytes(p) + up256(p.grid * sizeof(pattn::Split));
+  return p;
+}
+
+cudaError_t paged_attention(const PagedAttnArgs& a, const AttnPlan& p, void* scratch, cudaStream_t s) {
+  if (p.decode) {
+    pattn::Workspace w;
+    char* at = static_cast<char*>(scratch);
+    w.o = reinterpret_cast<float*>(at);
+    w.ml = reinterpret_cast<float2*>(at + o_bytes(p));
+    w.list = reinterpret_cast<pattn::Split*>(at + o_bytes(p) + ml_bytes(p));
+    w.rows = p.rows;
+    return attn_decode(a, p, w, s);
+  }
   const dim3 grid(a.b.total_q, (a.Hq + 3) / 4);
   if (a.dtype == JOLT_BF16) k_paged_attention<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
   else k_paged_attention<__half><<<grid, 128, 0, s>>>(a);

@@ -1,0 +1,146 @@
+// Shared device code of the paged attention kernels: how a batch's work is divided, the join with a
+// prefix, and the workspace that carries an item's parts from one kernel to the next.
+#pragma once
+
+#include <algorithm>
+
+#include "../paged.h"
+
+namespace jolt {
+namespace pattn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^x by the special function unit (2 units in the last place; exp2(-inf) = 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The work of a call is a line of units: the sequences in order, in each its items (the rows of one
+// KV head that are attended together), in each item its blocks of keys. CTA c of G takes the units
+// [c W / G, (c + 1) W / G), so that all CTAs end together whatever the lengths are. An item that falls
+// into several CTAs leaves a part in each: its running maximum, sum and unscaled output, in slot 0 when
+// the item began before the CTA's range and slot 1 otherwise. Where an item begins in a CTA and
+// does not end there (one at most per CTA), the CTA lists it for the combining kernel.
+struct Split {
+  int32_t s, h, m;     // sequence, KV head, block of rows; s < 0: none
+  int32_t c_last;      // CTA that holds its last unit (the first one is the list's index)
+  int32_t slot;        // slot of its first part
+};
+struct Workspace {
+  float* o;            // [G][2][rows][128]
+  float2* ml;          // [G][2][rows]: maximum (in units of log 2), sum
+  Split* list;         // [G]
+  int32_t rows;
+};
+
+// CTA whose range holds unit u.
+__device__ __forceinline__ int owner_of(int64_t u, int64_t W, int G) { return (int)(((u + 1) * G - 1) / W); }
+
+struct Start {
+  int64_t W, lo, hi;   // all units, this CTA's range
+  int64_t base;        // first unit of the sequence that holds lo
+  int32_t s, G;        // that sequence; CTAs that have work
+};
+
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sm, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) sm[warp] = v;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int64_t x = sm[w];
+    before += w < warp ? x : 0;
+    total += x;
+  }
+  __syncthreads();
+  return v + before;   // inclusive
+}
+
+// This CTA's share of the line: work(s) is the units of sequence s; a CTA takes min_units at least.
+// Called by all NT threads (NT a multiple of 32).
+template <int NT, class F>
+__device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units) {
+  __shared__ int64_t sm[NT / 32];
+  __shared__ int64_t base_s;
+  __shared__ int seq_s;
+  Start r{};
+  const int tid = threadIdx.x;
+  int64_t mine = tid < num_seqs ? work(tid) : 0, sum = mine;
+  for (int s = tid + NT; s < num_seqs; s += NT) sum += work(s);
+  int64_t total, base = 0;
+  int64_t incl = block_scan<NT>(sum, sm, total);
+  r.W = total;
+  const int64_t most = (total + min_units - 1) / min_units;
+  r.G = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
+  if ((int)blockIdx.x >= r.G) return r;
+  r.lo = (int64_t)blockIdx.x * total / r.G;
+  r.hi = (int64_t)(blockIdx.x + 1) * total / r.G;
+  if (num_seqs <= NT) {   // the scan just made is the one over sequences
+    if (incl > r.lo && incl - mine <= r.lo) {
+      base_s = incl - mine;
+      seq_s = tid;
+    }
+    __syncthreads();
+  } else {
+    for (int s0 = 0; s0 < num_seqs; s0 += NT) {
+      const int64_t v = s0 + tid < num_seqs ? work(s0 + tid) : 0;
+      incl = base + block_scan<NT>(v, sm, total);
+      if (incl > r.lo && incl - v <= r.lo) {
+        base_s = incl - v;
+        seq_s = s0 + tid;
+      }
+      base += total;
+      if (base > r.lo) break;   // uniform
+    }
+    __syncthreads();
+  }
+  r.base = base_s;
+  r.s = seq_s;
+  return r;
+}
+
+// Four output features of one row, from the unscaled sum o, maximum m (units of log 2) and sum l:
+// joined with the prefix, scaled, rounded and stored; lane 0 stores the log-sum-exp.
+template <typename T>
+__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, int64_t row, int lane, float4 o, float m, float l) {
+  if (a.pre_lse) {
+    const float p = a.pre_lse[row] * kLog2e, mx = fmaxf(m, p);
+    if (mx != -INFINITY) {
+      const float4 x = *reinterpret_cast<const float4*>(a.pre_out + row * kD + 4 * lane);
+      const float f = ex2(m - mx), w = ex2(p - mx);
+      l = fmaf(l, f, w);
+      o.x = p == -INFINITY ? o.x * f : fmaf(o.x, f, w * x.x);
+      o.y = p == -INFINITY ? o.y * f : fmaf(o.y, f, w * x.y);
+      o.z = p == -INFINITY ? o.z * f : fmaf(o.z, f, w * x.z);
+      o.w = p == -INFINITY ? o.w * f : fmaf(o.w, f, w * x.w);
+      m = mx;
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  T y[4] = {(T)(o.x * inv), (T)(o.y * inv), (T)(o.z * inv), (T)(o.w * inv)};
+  *reinterpret_cast<uint2*>(reinterpret_cast<T*>(a.out) + row * kD + 4 * lane) = *reinterpret_cast<const uint2*>(y);
+  if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// Wait for the kernels before this one in the stream (a launch that was let start early).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Let the next kernel of the stream be placed now; it waits for this one's end by itself.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace pattn
+
+cudaError_t attn_decode(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s);
+
+}  // namespace jolt

@@ -91,7 +91,13 @@ struct PagedAttnArgs {
   void* out;                        // [total_q][Hq][128] of dtype
   float* lse;                       // [total_q][Hq], or null
 };
-cudaError_t paged_attention(const PagedAttnArgs& a, cudaStream_t s);
+// How a call is run: which kernel, its CTAs, the rows of an item's block and the scratch it needs.
+struct AttnPlan {
+  int32_t decode = 0, grid = 0, rows = 0;
+  size_t bytes = 0;
+};
+AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms);
+cudaError_t paged_attention(const PagedAttnArgs& a, const AttnPlan& p, void* scratch, cudaStream_t s);
 
 // Host services of jolt_api.cpp.
 jolt_status host_fail(jolt_status st, const char* fmt, ...);

@@ -1,4 +1,5 @@
 // Host side of the growing cache (include/jolt.h): page sets, argument checks and launches.
+#include <atomic>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -47,6 +48,18 @@ cudaError_t take_slot(int dev, int32_t** out) {
 void give_slot(int dev, int32_t* p) {
   std::lock_guard<std::mutex> g(g_slot_mu);
   g_free_slots[dev].push_back(p);
+}
+
+cudaError_t sm_count(int dev, int* out) {
+  static std::atomic<int> n[kDevices];
+  int v = n[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    const cudaError_t e = cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    n[dev].store(v, std::memory_order_relaxed);
+  }
+  *out = v;
+  return cudaSuccess;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -288,7 +301,17 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   a.out = out; a.lse = lse;
   cudaStream_t s = (cudaStream_t)cuda_stream;
   ProfScope prof("paged_attention", s);
-  const cudaError_t e = paged_attention(a, s);
+  int sms = 0;
+  cudaError_t e = sm_count(pages->device, &sms);
+  if (e != cudaSuccess) return cuda_fail(what, e);
+  const AttnPlan p = paged_attention_plan(a, sms);
+  void* scratch = nullptr;
+  if (p.bytes) e = host_pool_malloc(&scratch, p.bytes, s);
+  if (e == cudaSuccess) {
+    e = paged_attention(a, p, scratch, s);
+    const cudaError_t e2 = scratch ? cudaFreeAsync(scratch, s) : cudaSuccess;
+    if (e == cudaSuccess) e = e2;
+  }
   return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
 }
 

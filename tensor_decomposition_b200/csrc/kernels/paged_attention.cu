@@ -2,111 +2,102 @@
 //     out = sum_j e^{s_j} v_j / sum_j e^{s_j},  s_j = scale q . k_j,
 // over the keys j a row may see (all of the sequence, or up to its own token), optionally joined
 // with a part (out0, lse0) attended elsewhere, which counts as one more key of score lse0 and
-// value out0. One warp a query row, lane i features 4 i .. 4 i + 3, one key at a time with a
-// running maximum and sum.
+// value out0. Two kernels do the work, one for few rows a KV head (paged_attention_decode.cu), bound
+// by HBM, one for many (paged_attention_chunk.cu), bound by the tensor pipe; both divide it into
+// equal shares a CTA, whatever the lengths are. This file chooses, and combines the parts of what a
+// share's end has cut.
 #include "paged_attention.cuh"
 
 namespace jolt {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ void get4(const T* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  const T* h = reinterpret_cast<const T*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = (float)h[i];
-}
+using namespace pattn;
 
+// The items that lie in several CTAs' shares: a warp a row, the parts weighted by their maxima.
 template <typename T>
-__global__ void __launch_bounds__(128) k_paged_attention(const PagedAttnArgs a) {
-  const int tok = blockIdx.x, lane = threadIdx.x & 31;
-  const int qh = blockIdx.y * 4 + (threadIdx.x >> 5);
-  __shared__ int seq_s;
-  if (threadIdx.x == 0) seq_s = -1;
-  __syncthreads();
-  for (int s = threadIdx.x; s < a.b.num_seqs; s += 128)
-    if (tok >= a.b.q_start[s] && tok < a.b.q_start[s + 1]) seq_s = s;
-  __syncthreads();
-  const int s = seq_s;
-  if (s < 0 || qh >= a.Hq) return;
-  const SeqView v = seq_view(a.b, s);
-  if (v.n == 0) return;
-  const int h = qh / (a.Hq / a.b.heads), i = tok - v.q0;
-  const int lim = a.causal ? v.len - v.n + i : v.len - 1;
-  float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  get4(reinterpret_cast<const T*>(a.Q) + tok * a.q_ts + qh * a.q_hs + 4 * lane, q);
-  float m = -INFINITY, l = 0.0f;
-  const int64_t row = (int64_t)tok * a.Hq + qh;
-  if (a.pre_lse) {
-    m = a.pre_lse[row];
-    if (m != -INFINITY) {
-      l = 1.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = a.pre_out[row * kD + 4 * lane + e];
+__global__ void __launch_bounds__(128) k_attn_combine(const PagedAttnArgs a, const Workspace ws) {
+  grid_wait();
+  const Split sp = ws.list[blockIdx.x];
+  if (sp.s < 0) return;
+  const int lane = threadIdx.x & 31, c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
+  const SeqView v = seq_view(a.b, sp.s);
+  const int g = a.Hq / a.b.heads, R = min(ws.rows, v.n * g - sp.m * ws.rows);
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < R; r += 4 * gridDim.y) {
+    float mx = -INFINITY;
+    for (int c = lane; c < parts; c += 32) {
+      const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
+      mx = fmaxf(mx, ws.ml[at].x);
     }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float ls = 0.0f;
+    if (mx != -INFINITY) {
+#pragma unroll 4
+      for (int c = 0; c < parts; ++c) {
+        const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
+        const float2 p = ws.ml[at];
+        const float4 x = *reinterpret_cast<const float4*>(ws.o + at * kD + 4 * lane);
+        const float f = ex2(p.x - mx);
+        ls = fmaf(p.y, f, ls);
+        y.x = fmaf(x.x, f, y.x);
+        y.y = fmaf(x.y, f, y.y);
+        y.z = fmaf(x.z, f, y.z);
+        y.w = fmaf(x.w, f, y.w);
+      }
+    }
+    const int rr = sp.m * ws.rows + r;
+    finish_row<T>(a, (int64_t)(v.q0 + rr / g) * a.Hq + sp.h * g + rr % g, lane, y, mx, ls);
   }
-  for (int j = 0; j <= lim; ++j) {
-    const int pg = page_of(a.b, s, j);
-    if (pg < 0) continue;
-    const int64_t off = (((int64_t)pg * a.b.heads + h) * a.b.page_size + j % a.b.page_size) * kD + 4 * lane;
-    float k[4];
-    get4(reinterpret_cast<const T*>(a.K) + off, k);
-    float d = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) d = fmaf(q[e], k[e], d);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
-    d *= a.scale;
-    const float mn = fmaxf(m, d), f = m == -INFINITY ? 0.0f : expf(m - mn), p = expf(d - mn);
-    get4(reinterpret_cast<const T*>(a.V) + off, k);
-    l = fmaf(l, f, p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = fmaf(o[e], f, p * k[e]);
-    m = mn;
-  }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  T* out = reinterpret_cast<T*>(a.out) + row * kD + 4 * lane;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] = (T)(o[e] * inv);
-  if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? m + logf(l) : -INFINITY;
 }
 
-}  // namespace
+template <typename T>
+cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid, std::min(16, (p.rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];   // placed while the parts are still computed; waits for them itself
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_attn_combine<T>, a, w);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
 
-namespace {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 size_t o_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * kD * sizeof(float)); }
 size_t ml_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * sizeof(float2)); }
+
 }  // namespace
 
-// Rows of a chunk that read one KV head: up to 16 run in the kernel for few rows.
+// Up to 16 rows of a chunk reading one KV head run in the kernel for few rows, whose MMAs hold 16.
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   AttnPlan p;
-  const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size;
-  p.decode = (int64_t)a.b.max_q * (a.Hq / a.b.heads) <= 16;
-  if (!p.decode) return p;
-  const int64_t units = std::max<int64_t>(1, (tokens + 63) / 64) * a.b.heads * a.b.num_seqs;
-  p.grid = (int)std::min<int64_t>(2 * (int64_t)sms, units);
-  p.rows = 16;
-  p.bytes = o_bytes(p) + ml_bytes(p) + up256(p.grid * sizeof(pattn::Split));
+  const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)a.b.max_q * (a.Hq / a.b.heads);
+  p.decode = rows <= 16;
+  p.rows = p.decode ? 16 : 256;
+  const int unit = p.decode ? 64 : 128;
+  const int64_t units = std::max<int64_t>(1, (tokens + unit - 1) / unit) * std::max<int64_t>(1, (rows + p.rows - 1) / p.rows) *
+                        a.b.heads * a.b.num_seqs;
+  p.grid = (int)std::min<int64_t>((p.decode ? 2 : 1) * (int64_t)sms, units);
+  p.bytes = o_bytes(p) + ml_bytes(p) + up256(p.grid * sizeof(Split));
   return p;
 }
 
 cudaError_t paged_attention(const PagedAttnArgs& a, const AttnPlan& p, void* scratch, cudaStream_t s) {
-  if (p.decode) {
-    pattn::Workspace w;
-    char* at = static_cast<char*>(scratch);
-    w.o = reinterpret_cast<float*>(at);
-    w.ml = reinterpret_cast<float2*>(at + o_bytes(p));
-    w.list = reinterpret_cast<pattn::Split*>(at + o_bytes(p) + ml_bytes(p));
-    w.rows = p.rows;
-    return attn_decode(a, p, w, s);
-  }
-  const dim3 grid(a.b.total_q, (a.Hq + 3) / 4);
-  if (a.dtype == JOLT_BF16) k_paged_attention<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
-  else k_paged_attention<__half><<<grid, 128, 0, s>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  Workspace w;
+  char* at = static_cast<char*>(scratch);
+  w.o = reinterpret_cast<float*>(at);
+  w.ml = reinterpret_cast<float2*>(at + o_bytes(p));
+  w.list = reinterpret_cast<Split*>(at + o_bytes(p) + ml_bytes(p));
+  w.rows = p.rows;
+  const cudaError_t e = p.decode ? attn_decode(a, p, w, s) : attn_chunk(a, p, w, s);
+  if (e != cudaSuccess) return e;
+  return a.dtype == JOLT_BF16 ? combine<__nv_bfloat16>(a, p, w, s) : combine<__half>(a, p, w, s);
 }
 
 }  // namespace jolt

@@ -141,6 +141,8 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 
 }  // namespace pattn
 
+// The two kernels.
 cudaError_t attn_decode(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s);
+cudaError_t attn_chunk(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s);
 
 }  // namespace jolt

@@ -1,0 +1,563 @@
+// Paged attention of many query rows (chunks of a prompt, whole prompts): the rows of a chunk that
+// read one KV head (token-major: row r is token r / g, query head h g + r % g) in blocks of 256.
+//
+// Two matrix products of 128 x 128 x 128 a tile of 128 keys and half block, and one exponential a
+// score: at 4 exponentials a cycle and sub-partition both take about 1000 cycles, so the tensor
+// pipe and the special function unit bound it alike. One persistent CTA an SM walks its share
+// of the units (128 keys of one item). Its warps: two softmax groups of four, one for each half
+// block (a thread a row); one that issues the MMAs (tcgen05, 128 x 128 accumulators in Tensor
+// Memory: scores and outputs of both halves fill its 512 columns); one that loads keys and values
+// by TMA, a box of up to 128 rows of a page at a time, into a ring of five 32 KB stages; two that gather
+// the query rows. While one half's scores are turned into weights, the tensor pipe works for the
+// other. Weights overwrite their scores in Tensor Memory and are the second product's A operand
+// from there, so only keys, values and queries pass through shared memory.
+// The weights are rounded to the type of the values (the tensor pipe takes no wider ones); their sum
+// is not. A maximum that grows by less than 8 (in units of log 2) is not followed: weights up to 2^8
+// are as exact, and most rescalings of the output fall away.
+#include "paged_attention.cuh"
+#include "sm100.cuh"
+
+namespace jolt {
+namespace {
+
+using namespace pattn;
+using namespace sm100;
+
+constexpr int kHalf = 128;                   // rows of a half block, keys of a tile
+constexpr int kBlockRows = 2 * kHalf;
+constexpr int kStages = 5;
+constexpr uint32_t kTileBytes = kHalf * kD * 2;
+constexpr uint32_t kHalfTile = kTileBytes / 2;   // 128 rows x 64 features
+constexpr int kThreads = 384;
+constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+constexpr float kFollow = 8.0f;
+
+struct Maps {
+  CUtensorMap K, V;
+};
+
+struct Bars {
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t tail;
+};
+
+__device__ __forceinline__ int blocks_of(const SeqView& v, int g) {
+  return (int)(((int64_t)v.n * g + kBlockRows - 1) / kBlockRows);
+}
+// Tiles of keys that block m of the sequence's rows sees (one at least, so that empty rows are written).
+__device__ __forceinline__ int tiles_of(const SeqView& v, int g, int m, bool causal) {
+  int seen = v.len;
+  if (causal) {
+    const int64_t last = min((int64_t)v.n * g, (int64_t)(m + 1) * kBlockRows) - 1;
+    seen = v.len - v.n + (int)(last / g) + 1;
+  }
+  return max(1, (seen + kHalf - 1) / kHalf);
+}
+
+// A part of an item: tiles t0 .. t1 - 1 of its T.
+struct Piece {
+  int s, h, m, M, t0, t1, T;
+  SeqView v;
+  int64_t left;     // units of the CTA's share from t0 on
+};
+__device__ __forceinline__ void enter(Piece& p, int g, bool causal) {
+  p.T = tiles_of(p.v, g, p.m, causal);
+  p.t1 = (int)min((int64_t)p.T, p.t0 + p.left);
+}
+// The next piece of the share; false behind the last.
+__device__ __forceinline__ bool next(Piece& p, const BatchView& b, int g, bool causal) {
+  p.left -= p.t1 - p.t0;
+  if (p.left <= 0) return false;
+  p.t0 = 0;
+  if (++p.m == p.M) {
+    p.m = 0;
+    if (++p.h == b.heads) {
+      p.h = 0;
+      do {
+        if (++p.s >= b.num_seqs) return false;
+        p.v = seq_view(b, p.s);
+        p.M = blocks_of(p.v, g);
+      } while (p.M == 0);
+    }
+  }
+  enter(p, g, causal);
+  return true;
+}
+
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(__half, float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc();
+template <>
+__device__ __forceinline__ constexpr uint32_t idesc<__nv_bfloat16>() {
+  return idesc_bf16_f32(kHalf, kHalf);
+}
+template <>
+__device__ __forceinline__ constexpr uint32_t idesc<__half>() {
+  return idesc_f16_f32(kHalf, kHalf);
+}
+
+// A bounded wait that also ends when another role of the CTA has given up. The clock is looked at
+// only every 64 polls.
+struct Waits {
+  volatile int* gave_up;
+  int32_t* status;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+      uint32_t done;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done)
+          : "r"(a), "r"(parity)
+          : "memory");
+      if (done) return true;
+      if ((it & 63) == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (*gave_up || now - t0 > kWaitLimitNs) {
+          *gave_up = 1;
+          atomicOr(status, PST_TIMEOUT);
+          return false;
+        }
+      }
+    }
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_chunk(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws, int box) {
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) Bars bar;
+  __shared__ uint32_t tmem_s;
+  __shared__ int gave_up;
+  __shared__ Piece first_s;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const BatchView& b = a.b;
+  const int g = a.Hq / b.heads;
+  const bool causal = a.causal;
+  grid_release();
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.kv_full[i], 1);
+      mbar_init(&bar.kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar.q_full[t], 32);
+      mbar_init(&bar.q_empty[t], 1);
+      mbar_init(&bar.s_full[t], 1);
+      mbar_init(&bar.p_full[t], 4);
+      mbar_init(&bar.o_full[t], 1);
+      mbar_init(&bar.o_empty[t], 4);
+    }
+    mbar_init(&bar.tail, 1);
+    gave_up = 0;
+    fence_barrier_init();
+  }
+  const Start st = find_start<kThreads>(
+      b.num_seqs,
+      [&](int s) {
+        const SeqView v = seq_view(b, s);
+        const int M = blocks_of(v, g);
+        int64_t n = 0;
+        for (int m = 0; m < M; ++m) n += tiles_of(v, g, m, causal);
+        return n * b.heads;
+      },
+      2);
+  if ((int)blockIdx.x >= st.G) {
+    if (tid == 0) ws.list[blockIdx.x].s = -1;
+    return;
+  }
+  if (warp == 8) {
+    tmem_alloc(&tmem_s, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    Piece p;
+    p.s = st.s;
+    p.v = seq_view(b, p.s);
+    p.M = blocks_of(p.v, g);
+    int64_t per = 0, at = st.lo - st.base;
+    for (int m = 0; m < p.M; ++m) per += tiles_of(p.v, g, m, causal);
+    p.h = (int)(at / per);
+    at %= per;
+    p.m = 0;
+    while (at >= tiles_of(p.v, g, p.m, causal)) at -= tiles_of(p.v, g, p.m++, causal);
+    p.t0 = (int)at;
+    p.left = st.hi - st.lo;
+    enter(p, g, causal);
+    first_s = p;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  const Waits wait{&gave_up, b.status};
+  Piece p = first_s;
+  uint8_t* Qs = sm;
+  uint8_t* ring = sm + 2 * kTileBytes;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) {
+      // ---------------------------------------------------------------- MMA issue
+      if (elect_one()) {
+        constexpr uint32_t id_qk = idesc<T>(), id_pv = idesc<T>() | (1u << 16);   // V: MN-major
+        uint32_t kv = 0, pieces[2] = {0, 0}, tiles[2] = {0, 0};
+        bool ok = true;
+        auto full = [&](uint32_t i) { return wait(&bar.kv_full[i % kStages], (i / kStages) & 1); };
+        auto qk = [&](int t, uint32_t i) {
+          const uint32_t A = smem_u32(Qs + t * kTileBytes), B = smem_u32(ring + (i % kStages) * kTileBytes);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = (k >> 2) * kHalfTile + (k & 3) * 32;
+            umma_bf16(tmem + t * kHalf, desc_kmajor_sw128(A + off), desc_kmajor_sw128(B + off), id_qk, k != 0);
+          }
+          umma_commit(&bar.s_full[t]);
+        };
+        do {
+          const int nt = p.t1 - p.t0;
+          const int two = (int64_t)p.v.n * g - (int64_t)p.m * kBlockRows > kHalf ? 2 : 1;
+          for (int t = 0; t < two && ok; ++t) ok = wait(&bar.q_full[t], pieces[t] & 1);
+          if (!ok || !(ok = full(kv))) break;
+          tc_fence_after();
+          for (int t = 0; t < two; ++t) qk(t, kv);
+          umma_commit(&bar.kv_empty[kv % kStages]);
+          if (nt == 1)
+            for (int t = 0; t < two; ++t) umma_commit(&bar.q_empty[t]);
+          for (int j = 0; j < nt && ok; ++j) {
+            const uint32_t iv = kv + 1, ik = kv + 2;   // V of this tile, K of the next
+            const bool more = j + 1 < nt;
+            for (int t = 0; t < two; ++t) {
+              if (t == 0 && !(ok = full(iv))) break;
+              if (!(ok = wait(&bar.p_full[t], tiles[t] & 1))) break;
+              if (j == 0 && !(ok = wait(&bar.o_empty[t], (pieces[t] & 1) ^ 1))) break;
+              tc_fence_after();
+              ++tiles[t];
+              const uint32_t B = smem_u32(ring + (iv % kStages) * kTileBytes);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, desc_mnmajor_sw128(B + k * 2048, kHalfTile, 1024),
+                        id_pv, (j | k) != 0);
+              if (more) {
+                if (t == 0 && !(ok = full(ik))) break;
+                tc_fence_after();
+                qk(t, ik);
+                if (j + 2 == nt) umma_commit(&bar.q_empty[t]);
+              } else {
+                umma_commit(&bar.o_full[t]);
+              }
+            }
+            if (!ok) break;
+            umma_commit(&bar.kv_empty[iv % kStages]);
+            if (more) umma_commit(&bar.kv_empty[ik % kStages]);
+            kv += 2;
+          }
+          for (int t = 0; t < two; ++t) ++pieces[t];
+        } while (ok && next(p, b, g, causal));
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- keys and values
+      uint32_t kv = 0, tails = 0;
+      const int per = kHalf / box;           // boxes of a tile: one lane each
+      prefetch_tensormap(&maps.K);
+      prefetch_tensormap(&maps.V);
+      bool ok = true;
+      do {
+        for (int j = p.t0; j < p.t1 && ok; ++j) {
+          const int key = j * kHalf + lane * box;     // this lane's box
+          int page = -1;
+          const bool mine = lane < per && key < p.v.len;
+          if (mine) page = page_of(b, p.s, key);
+          const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+          const bool whole = __all_sync(0xffffffffu, !mine || page >= 0);
+          const bool ends = (j + 1) * kHalf > p.v.len;
+          for (int kind = 0; kind < 2; ++kind, ++kv) {
+            const uint32_t s = kv % kStages;
+            ok = __all_sync(0xffffffffu, wait(&bar.kv_empty[s], ((kv / kStages) & 1) ^ 1));
+            if (!ok) break;
+            // A tile with rows that hold no keys: values there are zeroed, since a weight of zero
+            // does not hide what lies in the page (keys are hidden by the mask on their scores);
+            // rows of a bad page are zeroed for both. Such a tile lands on a barrier of its own first.
+            const bool fix = !whole || (kind == 1 && ends);
+            uint64_t* fb = fix ? &bar.tail : &bar.kv_full[s];
+            uint8_t* dst = ring + s * kTileBytes;
+            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(good) * box * kD * 2);
+            __syncwarp();
+            if (page >= 0) {
+              const CUtensorMap* map = kind ? &maps.V : &maps.K;
+              const int row = key % b.page_size;
+              tma_load_4d(dst + lane * box * 128, map, fb, 0, row, p.h, page);
+              tma_load_4d(dst + kHalfTile + lane * box * 128, map, fb, 64, row, p.h, page);
+            }
+            if (fix) {
+              ok = __all_sync(0xffffffffu, wait(&bar.tail, tails & 1));
+              ++tails;
+              if (!ok) break;
+              for (int r = lane; r < kHalf; r += 32) {
+                if (((good >> (r / box)) & 1) && j * kHalf + r < p.v.len) continue;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  *reinterpret_cast<uint4*>(dst + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(dst + kHalfTile + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                }
+              }
+              fence_async_shared();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar.kv_full[s]);
+            }
+          }
+        }
+      } while (ok && next(p, b, g, causal));
+      if (!ok) {   // copies in flight land before the CTA's memory is given up
+        const uint32_t n = min(kv, (uint32_t)kStages);
+        for (uint32_t i = kv - n; i < kv; ++i) mbar_wait(&bar.kv_full[i % kStages], (i / kStages) & 1, 1u << 20);
+      }
+    } else {
+      // ---------------------------------------------------------------- queries: a warp a half block
+      const int t = warp - 10, c16 = lane & 15, r2 = lane >> 4;
+      uint32_t pieces = 0;
+      bool ok = true;
+      do {
+        const int64_t R = (int64_t)p.v.n * g, r0 = (int64_t)p.m * kBlockRows + t * kHalf;
+        if (r0 >= R) continue;
+        ok = __all_sync(0xffffffffu, wait(&bar.q_empty[t], (pieces & 1) ^ 1));
+        if (!ok) break;
+        ++pieces;
+        const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g * a.q_hs + 8 * c16;
+        const uint32_t dst = smem_u32(Qs + t * kTileBytes + (c16 >> 3) * kHalfTile);
+#pragma unroll 4
+        for (int i = 0; i < kHalf / 2; ++i) {
+          const int rr = 2 * i + r2;
+          const int64_t r = r0 + rr;
+          const int rc = (int)min(r, R - 1), tok = rc / g;
+          const T* src = Q + (int64_t)tok * a.q_ts + (int64_t)(rc - tok * g) * a.q_hs;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4)),
+                       "l"(src), "r"(r < R ? 16u : 0u)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_shared();
+        mbar_arrive(&bar.q_full[t]);
+      } while (next(p, b, g, causal));
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax: a thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = warp >> 2, wq = warp & 3;
+    const uint32_t tS = tmem + t * kHalf + ((uint32_t)(32 * wq) << 16), tO = tS + 2 * kHalf;
+    const bool neg = a.scale < 0.0f;
+    const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // not 0: a masked score times 0 is no number
+    uint32_t tiles = 0, pieces = 0;
+    bool ok = true;
+    Split split;
+    split.s = -1;
+    int64_t at = st.lo;
+    do {
+      const int64_t R = (int64_t)p.v.n * g, r0 = (int64_t)p.m * kBlockRows + t * kHalf;
+      const bool began = p.t0 == 0, ends = p.t1 == p.T;
+      if (tid == 0 && began && !ends) {
+        split.s = p.s;
+        split.h = p.h;
+        split.m = p.m;
+        split.slot = 1;
+        split.c_last = owner_of(at + p.T - 1, st.W, st.G);
+      }
+      at += p.t1 - p.t0;
+      if (r0 >= R) continue;
+      const int64_t r = r0 + 32 * wq + lane;
+      const int rc = (int)min(r, R - 1), tok = rc / g;
+      const int lim = causal ? p.v.len - p.v.n + tok : p.v.len - 1;
+      const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);      // the least of the warp's rows
+      float m = -INFINITY, l = 0.0f;
+      for (int j = p.t0; j < p.t1; ++j) {
+        ok = __all_sync(0xffffffffu, wait(&bar.s_full[t], tiles & 1));
+        if (!ok) break;
+        ++tiles;
+        tc_fence_after();
+        float s[kHalf];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+        tmem_ld_wait();
+        if (neg) {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) s[i] = -s[i];
+        }
+        if (j * kHalf + kHalf - 1 > lim_warp) {
+          const int rel = lim - j * kHalf;
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) s[i] = i > rel ? -INFINITY : s[i];
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kHalf; i += 4)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[i + k]);
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2);
+        if (j == p.t0) {
+          m = mn;
+        } else if (__any_sync(0xffffffffu, mn - m > kFollow || (m == -INFINITY && mn > m))) {
+          const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+          m = mn;
+          l *= f;
+          // the scores being complete, so is every earlier product: the output is at rest
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(tO + 32 * c, o);
+          }
+        }
+        const float sub = m == -INFINITY ? 0.0f : -m;
+        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float x = ex2(fmaf(s[64 * c + 2 * i], scale2, sub)), y = ex2(fmaf(s[64 * c + 2 * i + 1], scale2, sub));
+            ls[i & 1] += x;
+            ls[2 + (i & 1)] += y;
+            w[i] = pack2(T(), x, y);
+          }
+          tmem_st32(tS + 32 * c, w);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[t]);
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, wait(&bar.o_full[t], pieces & 1));
+      if (!ok) break;
+      ++pieces;
+      tc_fence_after();
+      const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g + (rc - tok * g);
+      if (began && ends) {
+        float inv = 1.0f, w = 0.0f;
+        if (a.pre_lse) {
+          const float pl = a.pre_lse[row] * kLog2e, mn = fmaxf(m, pl);
+          if (mn != -INFINITY) {
+            inv = ex2(m - mn);
+            w = ex2(pl - mn);
+            l = fmaf(l, inv, w);
+            m = mn;
+          }
+        }
+        const float il = l > 0.0f ? 1.0f / l : 0.0f;
+        inv *= il;
+        w *= il;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_ld_wait();
+          if (r < R) {
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * inv;
+            if (w > 0.0f) {
+              const float4* pre = reinterpret_cast<const float4*>(a.pre_out + row * kD + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 x = pre[i];
+                y[4 * i] = fmaf(w, x.x, y[4 * i]);
+                y[4 * i + 1] = fmaf(w, x.y, y[4 * i + 1]);
+                y[4 * i + 2] = fmaf(w, x.z, y[4 * i + 2]);
+                y[4 * i + 3] = fmaf(w, x.w, y[4 * i + 3]);
+              }
+            }
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + row * kD + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack2(T(), y[8 * i], y[8 * i + 1]), pack2(T(), y[8 * i + 2], y[8 * i + 3]),
+                                  pack2(T(), y[8 * i + 4], y[8 * i + 5]), pack2(T(), y[8 * i + 6], y[8 * i + 7]));
+          }
+        }
+        if (a.lse && r < R) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      } else {
+        const int64_t slot = ((int64_t)blockIdx.x * 2 + (began ? 1 : 0)) * kBlockRows + t * kHalf + 32 * wq + lane;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_ld_wait();
+          if (r < R) {
+            uint4* dst = reinterpret_cast<uint4*>(ws.o + slot * kD + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (r < R) ws.ml[slot] = make_float2(m, l);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.o_empty[t]);
+    } while (next(p, b, g, causal));
+    if (tid == 0) ws.list[blockIdx.x] = split;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <typename T>
+cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
+  int box = kHalf;
+  while (a.b.page_size % box) box /= 2;      // 16 at least
+  Maps maps;
+  maps.K = *static_cast<const CUtensorMap*>(a.kmap);
+  maps.V = *static_cast<const CUtensorMap*>(a.vmap);
+  cudaError_t e = cudaFuncSetAttribute(k_attn_chunk<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  k_attn_chunk<T><<<p.grid, kThreads, kSmem, s>>>(a, maps, w, box);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_chunk(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s) {
+  return a.dtype == JOLT_BF16 ? launch<__nv_bfloat16>(a, p, w, s) : launch<__half>(a, p, w, s);
+}
+
+}  // namespace jolt

@@ -328,61 +328,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttn
   if (tid == 0) ws.list[blockIdx.x] = split;
 }
 
-// The items that lie in several CTAs' shares: a warp a row, the parts weighted by their maxima.
-template <typename T>
-__global__ void __launch_bounds__(128) k_attn_combine(const PagedAttnArgs a, const Workspace ws) {
-  grid_wait();
-  const Split sp = ws.list[blockIdx.x];
-  if (sp.s < 0) return;
-  const int lane = threadIdx.x & 31, c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
-  const SeqView v = seq_view(a.b, sp.s);
-  const int g = a.Hq / a.b.heads, R = min(ws.rows, v.n * g - sp.m * ws.rows);
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < R; r += 4 * gridDim.y) {
-    float mx = -INFINITY;
-    for (int c = lane; c < parts; c += 32) {
-      const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
-      mx = fmaxf(mx, ws.ml[at].x);
-    }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float ls = 0.0f;
-    if (mx != -INFINITY) {
-#pragma unroll 4
-      for (int c = 0; c < parts; ++c) {
-        const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
-        const float2 p = ws.ml[at];
-        const float4 x = *reinterpret_cast<const float4*>(ws.o + at * kD + 4 * lane);
-        const float f = ex2(p.x - mx);
-        ls = fmaf(p.y, f, ls);
-        y.x = fmaf(x.x, f, y.x);
-        y.y = fmaf(x.y, f, y.y);
-        y.z = fmaf(x.z, f, y.z);
-        y.w = fmaf(x.w, f, y.w);
-      }
-    }
-    const int rr = sp.m * ws.rows + r;
-    finish_row<T>(a, (int64_t)(v.q0 + rr / g) * a.Hq + sp.h * g + rr % g, lane, y, mx, ls);
-  }
-}
-
 template <typename T>
 cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_attn_decode<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   k_attn_decode<T><<<p.grid, kThreads, kSmem, s>>>(a, w);
-  note_launch();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, (p.rows + 3) / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_attn_combine<T>, a, w);
-  if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
 }

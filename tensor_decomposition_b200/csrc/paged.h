@@ -82,6 +82,7 @@ struct PagedAttnArgs {
   BatchView b;
   jolt_dtype dtype;
   const void *K, *V;           // pages [num_pages][heads][page_size][128]
+  const void *kmap, *vmap;     // their tensor maps (host CUtensorMap)
   const void* Q;
   int64_t q_ts, q_hs;          // element strides of Q
   int32_t Hq;

@@ -5,6 +5,7 @@
 #include <vector>
 
 #include "paged.h"
+#include "kernels/gemm_tc.h"
 
 using namespace jolt;
 
@@ -13,6 +14,7 @@ struct jolt_pages_s {
   void *K = nullptr, *V = nullptr;
   int device = 0;
   int32_t* d_status = nullptr;
+  CUtensorMap kmap, vmap;   // boxes of gcd(page_size, 128) rows x 64 features
 };
 
 namespace {
@@ -171,6 +173,15 @@ JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pag
   p->shape = sh;
   p->K = K_pages;
   p->V = V_pages;
+  const uint64_t row = 2 * kD, P = (uint64_t)sh.page_size;
+  const uint64_t dims[4] = {kD, P, (uint64_t)sh.heads, (uint64_t)sh.num_pages};
+  const uint64_t strides[3] = {row, row * P, row * P * sh.heads};
+  uint32_t box = 128;
+  while (P % box) box /= 2;
+  if (!tc_map_bf16_box(&p->kmap, K_pages, 4, dims, strides, box) || !tc_map_bf16_box(&p->vmap, V_pages, 4, dims, strides, box)) {
+    delete p;
+    return host_fail(JOLT_ERR_CUDA, "jolt_pages_create: tensor map rejected");
+  }
   cudaError_t e = cudaGetDevice(&p->device);
   if (e == cudaSuccess) e = take_slot(p->device, &p->d_status);
   if (e == cudaSuccess) e = cudaMemsetAsync(p->d_status, 0, sizeof(int32_t), (cudaStream_t)cuda_stream);
@@ -295,6 +306,7 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   a.b = view_of(pages, batch);
   a.dtype = pages->shape.dtype;
   a.K = pages->K; a.V = pages->V;
+  a.kmap = &pages->kmap; a.vmap = &pages->vmap;
   a.Q = Q; a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.Hq = q_heads;
   a.scale = scale; a.causal = causal != 0;
   a.pre_out = prefix_out; a.pre_lse = prefix_lse;

@@ -42,8 +42,8 @@ __device__ __forceinline__ int owner_of(int64_t u, int64_t W, int G) { return (i
 
 struct Start {
   int64_t W, lo, hi;   // all units, this CTA's range
-  int64_t base;        // first unit of the sequence that holds lo
-  int32_t s, G;        // that sequence; CTAs that have work
+  int64_t base, units; // the sequence that holds lo: its first unit, its number of them
+  int32_t s, G;        // its index; CTAs that have work
 };
 
 template <int NT>
@@ -73,7 +73,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sm, int64_t& t
 template <int NT, class F>
 __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units) {
   __shared__ int64_t sm[NT / 32];
-  __shared__ int64_t base_s;
+  __shared__ int64_t base_s, units_s;
   __shared__ int seq_s;
   Start r{};
   const int tid = threadIdx.x;
@@ -90,6 +90,7 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units)
   if (num_seqs <= NT) {   // the scan just made is the one over sequences
     if (incl > r.lo && incl - mine <= r.lo) {
       base_s = incl - mine;
+      units_s = mine;
       seq_s = tid;
     }
     __syncthreads();
@@ -99,6 +100,7 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units)
       incl = base + block_scan<NT>(v, sm, total);
       if (incl > r.lo && incl - v <= r.lo) {
         base_s = incl - v;
+        units_s = v;
         seq_s = s0 + tid;
       }
       base += total;
@@ -107,6 +109,7 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units)
     __syncthreads();
   }
   r.base = base_s;
+  r.units = units_s;
   r.s = seq_s;
   return r;
 }

@@ -7,7 +7,7 @@
 // of the units (128 keys of one item). Its warps: two softmax groups of four, one for each half
 // block (a thread a row); one that issues the MMAs (tcgen05, 128 x 128 accumulators in Tensor
 // Memory: scores and outputs of both halves fill its 512 columns); one that loads keys and values
-// by TMA, a box of up to 128 rows of a page at a time, into a ring of five 32 KB stages; two that gather
+// by TMA, a box of up to 128 rows of a page at a time, into a ring of five 32 KB stages; one that gathers
 // the query rows. While one half's scores are turned into weights, the tensor pipe works for the
 // other. Weights overwrite their scores in Tensor Memory and are the second product's A operand
 // from there, so only keys, values and queries pass through shared memory.
@@ -28,9 +28,12 @@ constexpr int kBlockRows = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr uint32_t kTileBytes = kHalf * kD * 2;
 constexpr uint32_t kHalfTile = kTileBytes / 2;   // 128 rows x 64 features
-constexpr int kThreads = 384;
+constexpr int kThreads = 384;                // 12 warps, the last one idle (registers move by groups of four)
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;   // 256 x 200 + 128 x 104 = the launch's 384 x 168
 constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+constexpr int kItem = 2;                     // what an item costs besides its tiles, in tiles
 constexpr float kFollow = 8.0f;
+constexpr int kPoly = 2;                     // of 8 pairs of exponentials, those made by a polynomial
 
 struct Maps {
   CUtensorMap K, V;
@@ -38,38 +41,37 @@ struct Maps {
 
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
   uint64_t tail;
 };
 
-__device__ __forceinline__ int blocks_of(const SeqView& v, int g) {
-  return (int)(((int64_t)v.n * g + kBlockRows - 1) / kBlockRows);
-}
+__device__ __forceinline__ int blocks_of(const SeqView& v, int g) { return (v.n * g + kBlockRows - 1) / kBlockRows; }
 // Tiles of keys that block m of the sequence's rows sees (one at least, so that empty rows are written).
 __device__ __forceinline__ int tiles_of(const SeqView& v, int g, int m, bool causal) {
   int seen = v.len;
-  if (causal) {
-    const int64_t last = min((int64_t)v.n * g, (int64_t)(m + 1) * kBlockRows) - 1;
-    seen = v.len - v.n + (int)(last / g) + 1;
-  }
+  if (causal) seen += (int)((uint32_t)(min(v.n * g, (m + 1) * kBlockRows) - 1) / (uint32_t)g) + 1 - v.n;
   return max(1, (seen + kHalf - 1) / kHalf);
 }
 
-// A part of an item: tiles t0 .. t1 - 1 of its T.
+// A part of an item: tiles t0 .. t1 - 1 of its T. On the line an item takes kItem units (its begin and
+// end: queries in, output out) and one for each tile after them.
 struct Piece {
   int s, h, m, M, t0, t1, T;
   SeqView v;
-  int64_t left;     // units of the CTA's share from t0 on
+  int64_t left;     // units of the CTA's share behind the piece
 };
-__device__ __forceinline__ void enter(Piece& p, int g, bool causal) {
+// The piece of an item from its unit u on; false if the share ends before the item's first tile.
+__device__ __forceinline__ bool enter(Piece& p, int u, int g, bool causal) {
   p.T = tiles_of(p.v, g, p.m, causal);
-  p.t1 = (int)min((int64_t)p.T, p.t0 + p.left);
+  const int take = (int)min((int64_t)(p.T + kItem - u), p.left);
+  p.left -= take;
+  p.t0 = max(u - kItem, 0);
+  p.t1 = u + take - kItem;
+  return p.t1 > p.t0;
 }
 // The next piece of the share; false behind the last.
 __device__ __forceinline__ bool next(Piece& p, const BatchView& b, int g, bool causal) {
-  p.left -= p.t1 - p.t0;
   if (p.left <= 0) return false;
-  p.t0 = 0;
   if (++p.m == p.M) {
     p.m = 0;
     if (++p.h == b.heads) {
@@ -81,8 +83,7 @@ __device__ __forceinline__ bool next(Piece& p, const BatchView& b, int g, bool c
       } while (p.M == 0);
     }
   }
-  enter(p, g, causal);
-  return true;
+  return enter(p, 0, g, causal);
 }
 
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
@@ -104,6 +105,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float x, float y) {
@@ -123,6 +132,91 @@ __device__ __forceinline__ constexpr uint32_t idesc<__nv_bfloat16>() {
 template <>
 __device__ __forceinline__ constexpr uint32_t idesc<__half>() {
   return idesc_f16_f32(kHalf, kHalf);
+}
+
+// Two float32 in one register pair, and its packed arithmetic.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x of a pair on the multiply-add units, for x <= 2^6: the nearest whole number taken off by adding and
+// subtracting 1.5 2^23 (its bits end up in the sum's last places), a polynomial of degree 5 for the
+// rest in [-1/2, 1/2] (least relative error with constant 1, 1.9e-7 evaluated in float32), the whole
+// number added to the exponent. Below 2^-126 the result is about 2^-126.
+__device__ __forceinline__ void ex2_poly(uint64_t x2, float& a, float& b) {
+  const float kRound = 12582912.0f;
+  float x, y;
+  unpair(x2, x, y);
+  x2 = pair_of(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
+  const uint64_t n = add2(x2, pair_of(kRound, kRound));
+  const uint64_t f = fma2(add2(n, pair_of(-kRound, -kRound)), pair_of(-1.0f, -1.0f), x2);
+  uint64_t q = fma2(f, pair_of(0.001326472731307149f, 0.001326472731307149f), pair_of(0.009671512991189957f, 0.009671512991189957f));
+  q = fma2(q, f, pair_of(0.05550733581185341f, 0.05550733581185341f));
+  q = fma2(q, f, pair_of(0.24022242426872253f, 0.24022242426872253f));
+  q = fma2(q, f, pair_of(0.6931470036506653f, 0.6931470036506653f));
+  q = fma2(q, f, pair_of(1.0f, 1.0f));
+  float n0, n1, q0, q1;
+  unpair(n, n0, n1);
+  unpair(q, q0, q1);
+  a = __int_as_float(__float_as_int(q0) + (__float_as_int(n0) << 23));
+  b = __int_as_float(__float_as_int(q1) + (__float_as_int(n1) << 23));
+}
+
+// One row's weights 2^(s scale2 + sub), rounded to the type, written over its scores (tS); their sum
+// goes to l unrounded. kP of 8 pairs are made by the polynomial, so that the special function unit
+// is not what the two softmax groups wait for. The first half is announced while the second is made.
+template <typename T, int kP>
+__device__ __forceinline__ void weights(const float (&s)[kHalf], float scale2, float sub, float& l, uint32_t tS,
+                                        uint64_t* lo, uint64_t* hi, int lane) {
+  const uint64_t sc = pair_of(scale2, scale2), sb = pair_of(sub, sub);
+  uint64_t sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint64_t x2 = fma2(pair_of(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sc, sb);
+      float x, y;
+      if ((i & 7) < kP) {
+        ex2_poly(x2, x, y);
+      } else {
+        unpair(x2, x, y);
+        x = ex2(x);
+        y = ex2(y);
+      }
+      sum[i & 1] = add2(sum[i & 1], pair_of(x, y));
+      w[i] = pack2(T(), x, y);
+    }
+    tmem_st16(tS + 16 * c, w);
+    if (c & 1) {
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c == 3 ? hi : lo);
+    }
+  }
+  float x, y;
+  unpair(add2(sum[0], sum[1]), x, y);
+  l += x + y;
 }
 
 // A bounded wait that also ends when another role of the CTA has given up. The clock is looked at
@@ -164,6 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_s;
   __shared__ int gave_up;
   __shared__ Piece first_s;
+  __shared__ bool any_s;
+  __shared__ int64_t range_s[3];   // all units, the end of this CTA's, CTAs with work
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchView& b = a.b;
@@ -179,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.q_full[t], 32);
       mbar_init(&bar.q_empty[t], 1);
       mbar_init(&bar.s_full[t], 1);
-      mbar_init(&bar.p_full[t], 4);
+      mbar_init(&bar.p_lo[t], 4);
+      mbar_init(&bar.p_hi[t], 4);
       mbar_init(&bar.o_full[t], 1);
       mbar_init(&bar.o_empty[t], 4);
     }
@@ -193,10 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const SeqView v = seq_view(b, s);
         const int M = blocks_of(v, g);
         int64_t n = 0;
-        for (int m = 0; m < M; ++m) n += tiles_of(v, g, m, causal);
+#pragma unroll 4
+        for (int m = 0; m < M; ++m) n += tiles_of(v, g, m, causal) + kItem;
         return n * b.heads;
       },
-      2);
+      kItem + 2);
   if ((int)blockIdx.x >= st.G) {
     if (tid == 0) ws.list[blockIdx.x].s = -1;
     return;
@@ -210,31 +308,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.s = st.s;
     p.v = seq_view(b, p.s);
     p.M = blocks_of(p.v, g);
-    int64_t per = 0, at = st.lo - st.base;
-    for (int m = 0; m < p.M; ++m) per += tiles_of(p.v, g, m, causal);
+    const int64_t per = st.units / b.heads;
+    int64_t at = st.lo - st.base;
     p.h = (int)(at / per);
     at %= per;
     p.m = 0;
-    while (at >= tiles_of(p.v, g, p.m, causal)) at -= tiles_of(p.v, g, p.m++, causal);
-    p.t0 = (int)at;
+    for (int n; at >= (n = tiles_of(p.v, g, p.m, causal) + kItem); at -= n) ++p.m;
     p.left = st.hi - st.lo;
-    enter(p, g, causal);
+    any_s = enter(p, (int)at, g, causal);   // a share can lie in an item's first units only
     first_s = p;
+    range_s[0] = st.W;
+    range_s[1] = st.hi;
+    range_s[2] = st.G;
+    ws.list[blockIdx.x].s = -1;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
   const Waits wait{&gave_up, b.status};
-  Piece p = first_s;
   uint8_t* Qs = sm;
   uint8_t* ring = sm + 2 * kTileBytes;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (!any_s) {
+    // nothing to do: on to the end
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {
       // ---------------------------------------------------------------- MMA issue
       if (elect_one()) {
+        Piece p = first_s;
         constexpr uint32_t id_qk = idesc<T>(), id_pv = idesc<T>() | (1u << 16);   // V: MN-major
         uint32_t kv = 0, pieces[2] = {0, 0}, tiles[2] = {0, 0};
         bool ok = true;
@@ -250,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         do {
           const int nt = p.t1 - p.t0;
-          const int two = (int64_t)p.v.n * g - (int64_t)p.m * kBlockRows > kHalf ? 2 : 1;
+          const int two = p.v.n * g - p.m * kBlockRows > kHalf ? 2 : 1;
           for (int t = 0; t < two && ok; ++t) ok = wait(&bar.q_full[t], pieces[t] & 1);
           if (!ok || !(ok = full(kv))) break;
           tc_fence_after();
@@ -263,15 +366,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = j + 1 < nt;
             for (int t = 0; t < two; ++t) {
               if (t == 0 && !(ok = full(iv))) break;
-              if (!(ok = wait(&bar.p_full[t], tiles[t] & 1))) break;
+              if (!(ok = wait(&bar.p_lo[t], tiles[t] & 1))) break;
               if (j == 0 && !(ok = wait(&bar.o_empty[t], (pieces[t] & 1) ^ 1))) break;
               tc_fence_after();
-              ++tiles[t];
               const uint32_t B = smem_u32(ring + (iv % kStages) * kTileBytes);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
+              for (int k = 0; k < 4; ++k)
                 umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, desc_mnmajor_sw128(B + k * 2048, kHalfTile, 1024),
                         id_pv, (j | k) != 0);
+              if (!(ok = wait(&bar.p_hi[t], tiles[t] & 1))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4; k < 8; ++k)
+                umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, desc_mnmajor_sw128(B + k * 2048, kHalfTile, 1024),
+                        id_pv, 1);
+              ++tiles[t];
               if (more) {
                 if (t == 0 && !(ok = full(ik))) break;
                 tc_fence_after();
@@ -291,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 9) {
       // ---------------------------------------------------------------- keys and values
+      Piece p = first_s;
       uint32_t kv = 0, tails = 0;
       const int per = kHalf / box;           // boxes of a tile: one lane each
       prefetch_tensormap(&maps.K);
@@ -346,61 +456,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t n = min(kv, (uint32_t)kStages);
         for (uint32_t i = kv - n; i < kv; ++i) mbar_wait(&bar.kv_full[i % kStages], (i / kStages) & 1, 1u << 20);
       }
-    } else {
-      // ---------------------------------------------------------------- queries: a warp a half block
-      const int t = warp - 10, c16 = lane & 15, r2 = lane >> 4;
-      uint32_t pieces = 0;
+    } else if (warp == 10) {
+      // ---------------------------------------------------------------- queries
+      Piece p = first_s;
+      const int c16 = lane & 15, r2 = lane >> 4;
+      const int step_t = 2 / g, step_h = 2 % g;       // from a row to the one two further
+      uint32_t pieces[2] = {0, 0};
       bool ok = true;
       do {
-        const int64_t R = (int64_t)p.v.n * g, r0 = (int64_t)p.m * kBlockRows + t * kHalf;
-        if (r0 >= R) continue;
-        ok = __all_sync(0xffffffffu, wait(&bar.q_empty[t], (pieces & 1) ^ 1));
-        if (!ok) break;
-        ++pieces;
-        const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g * a.q_hs + 8 * c16;
-        const uint32_t dst = smem_u32(Qs + t * kTileBytes + (c16 >> 3) * kHalfTile);
-#pragma unroll 4
-        for (int i = 0; i < kHalf / 2; ++i) {
-          const int rr = 2 * i + r2;
-          const int64_t r = r0 + rr;
-          const int rc = (int)min(r, R - 1), tok = rc / g;
-          const T* src = Q + (int64_t)tok * a.q_ts + (int64_t)(rc - tok * g) * a.q_hs;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4)),
-                       "l"(src), "r"(r < R ? 16u : 0u)
-                       : "memory");
+        for (int t = 0; t < 2 && ok; ++t) {
+          const int R = p.v.n * g, r0 = p.m * kBlockRows + t * kHalf;
+          if (r0 >= R) break;
+          ok = __all_sync(0xffffffffu, wait(&bar.q_empty[t], (pieces[t] & 1) ^ 1));
+          if (!ok) break;
+          ++pieces[t];
+          int tok = (r0 + r2) / g, hd = (r0 + r2) - tok * g;
+          const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g * a.q_hs + 8 * c16;
+          const uint32_t dst = smem_u32(Qs + t * kTileBytes + (c16 >> 3) * kHalfTile);
+#pragma unroll 8
+          for (int i = 0; i < kHalf / 2; ++i) {
+            const int rr = 2 * i + r2;
+            const bool in = r0 + rr < R;
+            const T* src = in ? Q + (int64_t)tok * a.q_ts + (int64_t)hd * a.q_hs : Q;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4)),
+                         "l"(src), "r"(in ? 16u : 0u)
+                         : "memory");
+            tok += step_t;
+            hd += step_h;
+            if (hd >= g) {
+              hd -= g;
+              ++tok;
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_shared();
+          mbar_arrive(&bar.q_full[t]);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_shared();
-        mbar_arrive(&bar.q_full[t]);
-      } while (next(p, b, g, causal));
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      } while (ok && next(p, b, g, causal));
     }
   } else {
     // ------------------------------------------------------------------ softmax: a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    Piece p = first_s;
     const int t = warp >> 2, wq = warp & 3;
     const uint32_t tS = tmem + t * kHalf + ((uint32_t)(32 * wq) << 16), tO = tS + 2 * kHalf;
     const bool neg = a.scale < 0.0f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // not 0: a masked score times 0 is no number
     uint32_t tiles = 0, pieces = 0;
     bool ok = true;
-    Split split;
-    split.s = -1;
-    int64_t at = st.lo;
     do {
-      const int64_t R = (int64_t)p.v.n * g, r0 = (int64_t)p.m * kBlockRows + t * kHalf;
+      const int R = p.v.n * g, r0 = p.m * kBlockRows + t * kHalf;
       const bool began = p.t0 == 0, ends = p.t1 == p.T;
-      if (tid == 0 && began && !ends) {
-        split.s = p.s;
-        split.h = p.h;
-        split.m = p.m;
-        split.slot = 1;
-        split.c_last = owner_of(at + p.T - 1, st.W, st.G);
-      }
-      at += p.t1 - p.t0;
+      if (tid == 0 && began && !ends)   // the share's last piece: left is what it has of the item
+        ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[1] + (p.T - p.t1) - 1, range_s[0], range_s[2]), 1};
       if (r0 >= R) continue;
-      const int64_t r = r0 + 32 * wq + lane;
-      const int rc = (int)min(r, R - 1), tok = rc / g;
+      const int r = r0 + 32 * wq + lane;
+      const int rc = min(r, R - 1), tok = rc / g;
       const int lim = causal ? p.v.len - p.v.n + tok : p.v.len - 1;
       const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);      // the least of the warp's rows
       float m = -INFINITY, l = 0.0f;
@@ -417,20 +528,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kHalf; ++i) s[i] = -s[i];
         }
-        if (j * kHalf + kHalf - 1 > lim_warp) {
+        const bool edge = j * kHalf + kHalf - 1 > lim_warp;
+        if (edge) {
           const int rel = lim - j * kHalf;
 #pragma unroll
           for (int i = 0; i < kHalf; ++i) s[i] = i > rel ? -INFINITY : s[i];
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < kHalf; i += 4)
+        for (int i = 4; i < kHalf - 4; i += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[i + k]);
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2);
+          for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[kHalf - 4 + k]);
+        const float mn = max3(m, max3(mx[0], mx[1], mx[2]) * scale2, mx[3] * scale2);
         if (j == p.t0) {
           m = mn;
-        } else if (__any_sync(0xffffffffu, mn - m > kFollow || (m == -INFINITY && mn > m))) {
+        } else if (__any_sync(0xffffffffu, mn - m > kFollow)) {
           const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
           m = mn;
           l *= f;
@@ -446,24 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float sub = m == -INFINITY ? 0.0f : -m;
-        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = ex2(fmaf(s[64 * c + 2 * i], scale2, sub)), y = ex2(fmaf(s[64 * c + 2 * i + 1], scale2, sub));
-            ls[i & 1] += x;
-            ls[2 + (i & 1)] += y;
-            w[i] = pack2(T(), x, y);
-          }
-          tmem_st32(tS + 32 * c, w);
-        }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[t]);
+        if (edge) weights<T, 0>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
+        else weights<T, kPoly>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
       if (!ok) break;
       ok = __all_sync(0xffffffffu, wait(&bar.o_full[t], pieces & 1));
@@ -532,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_empty[t]);
     } while (next(p, b, g, causal));
-    if (tid == 0) ws.list[blockIdx.x] = split;
   }
   tc_fence_before();
   __syncthreads();

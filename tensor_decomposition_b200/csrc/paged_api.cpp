@@ -292,6 +292,8 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   if (q_heads <= 0 || q_heads % pages->shape.heads)
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: q_heads must be a positive multiple of the %d KV heads", what,
                      pages->shape.heads);
+  if ((int64_t)batch->total_q * q_heads > INT32_MAX - 1024)
+    return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 query rows", what);
   if (!prefix_out != !prefix_lse)
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: prefix_out and prefix_lse come together", what);
   if (batch->total_q == 0 || batch->num_seqs == 0) return JOLT_OK;

@@ -5,7 +5,7 @@ import math
 
 import pytest
 
-from paged_common import D, Cache, check_attention, freqs, norm_rope_ref
+from paged_common import D, Cache, attention_ref, check_attention, freqs, norm_rope_ref
 
 pytestmark = pytest.mark.gpu
 SCALE = 1.0 / math.sqrt(D)
@@ -355,9 +355,11 @@ def test_bad_bounds_and_pages_are_skipped_and_reported(J, chunks):
     J.jolt_pages_status(pages)
     K0, V0 = c.K.clone(), c.V.clone()
     kv = x = c.randn(c.total, 2, D)
+    ref, _, tol, _ = attention_ref(c, Q, SCALE, True)
+    assert ((good.double() - ref).abs() <= tol).all()
 
     def expect(text, rows):
-        """The call reports `text`; the rows of the other sequences are as before; then all is well again."""
+        """The call reports `text`; the rows of the other sequences are right; then all is well again."""
         out = torch.full_like(good, math.nan)
         J.jolt_paged_attention(pages, batch, Q, out, SCALE)
         with pytest.raises(J.JoltError) as e:
@@ -366,8 +368,8 @@ def test_bad_bounds_and_pages_are_skipped_and_reported(J, chunks):
         J.jolt_pages_status(pages)
         for s in range(3):
             r = slice(c.starts[s], c.starts[s + 1])
-            if s not in rows:
-                assert torch.equal(out[r], good[r])
+            if s not in rows:   # not the same bits: a skipped sequence shifts where the others are divided
+                assert ((out[r].double() - ref[r]).abs() <= tol[r]).all()
         J.jolt_paged_append(pages, batch, x, kv)
         with pytest.raises(J.JoltError):
             J.jolt_pages_status(pages)

@@ -13,7 +13,8 @@ namespace {
 
 using namespace pattn;
 
-// The items that lie in several CTAs' shares: a warp a row, the parts weighted by their maxima.
+// The items that lie in several CTAs' shares, the parts weighted by their maxima. Parts of up to 16
+// rows lie row by row: a warp a row.
 template <typename T>
 __global__ void __launch_bounds__(128) k_attn_combine(const PagedAttnArgs a, const Workspace ws) {
   grid_wait();
@@ -21,40 +22,84 @@ __global__ void __launch_bounds__(128) k_attn_combine(const PagedAttnArgs a, con
   if (sp.s < 0) return;
   const int lane = threadIdx.x & 31, c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
   const SeqView v = seq_view(a.b, sp.s);
-  const int g = a.Hq / a.b.heads, R = min(ws.rows, v.n * g - sp.m * ws.rows);
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < R; r += 4 * gridDim.y) {
-    float mx = -INFINITY;
-    for (int c = lane; c < parts; c += 32) {
-      const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
-      mx = fmaxf(mx, ws.ml[at].x);
-    }
+  const int g = a.Hq / a.b.heads, R = v.n * g;
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (r >= R) return;
+  float mx = -INFINITY;
+  for (int c = lane; c < parts; c += 32) {
+    const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
+    mx = fmaxf(mx, ws.ml[at].x);
+  }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float ls = 0.0f;
-    if (mx != -INFINITY) {
+  for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float ls = 0.0f;
+  if (mx != -INFINITY) {
 #pragma unroll 4
-      for (int c = 0; c < parts; ++c) {
-        const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
-        const float2 p = ws.ml[at];
-        const float4 x = *reinterpret_cast<const float4*>(ws.o + at * kD + 4 * lane);
-        const float f = ex2(p.x - mx);
-        ls = fmaf(p.y, f, ls);
-        y.x = fmaf(x.x, f, y.x);
-        y.y = fmaf(x.y, f, y.y);
-        y.z = fmaf(x.z, f, y.z);
-        y.w = fmaf(x.w, f, y.w);
+    for (int c = 0; c < parts; ++c) {
+      const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
+      const float2 p = ws.ml[at];
+      const float4 x = *reinterpret_cast<const float4*>(ws.o + at * kD + 4 * lane);
+      const float f = ex2(p.x - mx);
+      ls = fmaf(p.y, f, ls);
+      y.x = fmaf(x.x, f, y.x);
+      y.y = fmaf(x.y, f, y.y);
+      y.z = fmaf(x.z, f, y.z);
+      y.w = fmaf(x.w, f, y.w);
+    }
+  }
+  finish_row<T>(a, (int64_t)(v.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y, mx, ls);
+}
+
+// The same for blocks of 256 rows, whose parts lie in blocks of four features with the rows next to one
+// another: a CTA takes 32 rows, a lane a row and its warp every fourth block of features, and the rows
+// come together in shared memory.
+template <typename T>
+__global__ void __launch_bounds__(128) k_attn_combine_blocks(const PagedAttnArgs a, const Workspace ws) {
+  __shared__ float4 y_s[32][33];
+  grid_wait();
+  const Split sp = ws.list[blockIdx.x];
+  if (sp.s < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
+  const SeqView v = seq_view(a.b, sp.s);
+  const int g = a.Hq / a.b.heads, rb = blockIdx.y * 32, R = min(256, v.n * g - sp.m * 256);
+  if (rb >= R) return;
+  const bool in = rb + lane < R;
+  const float4* o = reinterpret_cast<const float4*>(ws.o);
+  float mx = -INFINITY, ls = 0.0f;
+  for (int c = 0; c < parts && in; ++c)
+    mx = fmaxf(mx, ws.ml[((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * 256 + rb + lane].x);
+  float4 y[8] = {};
+  if (in && mx != -INFINITY) {
+    for (int c = 0; c < parts; ++c) {
+      const int64_t slot = (int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0);
+      const float2 p = ws.ml[slot * 256 + rb + lane];
+      const float f = ex2(p.x - mx);
+      ls = fmaf(p.y, f, ls);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 x = o[(slot * 32 + warp + 4 * k) * 256 + rb + lane];
+        y[k].x = fmaf(x.x, f, y[k].x);
+        y[k].y = fmaf(x.y, f, y[k].y);
+        y[k].z = fmaf(x.z, f, y[k].z);
+        y[k].w = fmaf(x.w, f, y[k].w);
       }
     }
-    const int rr = sp.m * ws.rows + r;
-    finish_row<T>(a, (int64_t)(v.q0 + rr / g) * a.Hq + sp.h * g + rr % g, lane, y, mx, ls);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y_s[lane][warp + 4 * k] = y[k];
+  __syncthreads();
+  for (int i = warp; i < min(32, R - rb); i += 4) {
+    const int r = sp.m * 256 + rb + i;
+    finish_row<T>(a, (int64_t)(v.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y_s[i][lane],
+                  __shfl_sync(0xffffffffu, mx, i), __shfl_sync(0xffffffffu, ls, i));
   }
 }
 
 template <typename T>
 cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, std::min(16, (p.rows + 3) / 4));
+  cfg.gridDim = dim3(p.grid, p.decode ? 4 : 8);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];   // placed while the parts are still computed; waits for them itself
@@ -62,7 +107,7 @@ cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_attn_combine<T>, a, w);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, p.decode ? k_attn_combine<T> : k_attn_combine_blocks<T>, a, w);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();

@@ -69,12 +69,11 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sm, int64_t& t
 }
 
 // This CTA's share of the line: work(s) is the units of sequence s; a CTA takes min_units at least.
-// Called by all NT threads (NT a multiple of 32).
+// Called by all NT threads (NT a multiple of 32); sm: NT / 32 + 3 words of shared memory, free again on
+// return and a barrier.
 template <int NT, class F>
-__device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units) {
-  __shared__ int64_t sm[NT / 32];
-  __shared__ int64_t base_s, units_s;
-  __shared__ int seq_s;
+__device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units, int64_t* sm) {
+  int64_t &base_s = sm[NT / 32], &units_s = sm[NT / 32 + 1], &seq_s = sm[NT / 32 + 2];
   Start r{};
   const int tid = threadIdx.x;
   int64_t mine = tid < num_seqs ? work(tid) : 0, sum = mine;
@@ -110,7 +109,7 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units)
   }
   r.base = base_s;
   r.units = units_s;
-  r.s = seq_s;
+  r.s = (int)seq_s;
   return r;
 }
 

@@ -4,10 +4,11 @@
 // Two matrix products of 128 x 128 x 128 a tile of 128 keys and half block, and one exponential a
 // score: at 4 exponentials a cycle and sub-partition both take about 1000 cycles, so the tensor
 // pipe and the special function unit bound it alike. One persistent CTA an SM walks its share
-// of the units (128 keys of one item). Its warps: two softmax groups of four, one for each half
-// block (a thread a row); one that issues the MMAs (tcgen05, 128 x 128 accumulators in Tensor
+// of the units (128 keys of one item). Its warps: two softmax groups of eight, one for each half
+// block (two threads a row, 64 keys each, who agree on the maximum through shared memory: one thread a
+// row took 2350 cycles a tile against 2150, and twice as long to write its output); one that issues the MMAs (tcgen05, 128 x 128 accumulators in Tensor
 // Memory: scores and outputs of both halves fill its 512 columns); one that loads keys and values
-// by TMA, a box of up to 128 rows of a page at a time, into a ring of five 32 KB stages; one that gathers
+// by TMA, a box of up to 128 rows of a page at a time, into a ring of five 32 KB stages; two that gather
 // the query rows. While one half's scores are turned into weights, the tensor pipe works for the
 // other. Weights overwrite their scores in Tensor Memory and are the second product's A operand
 // from there, so only keys, values and queries pass through shared memory.
@@ -28,12 +29,12 @@ constexpr int kBlockRows = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr uint32_t kTileBytes = kHalf * kD * 2;
 constexpr uint32_t kHalfTile = kTileBytes / 2;   // 128 rows x 64 features
-constexpr int kThreads = 384;                // 12 warps, the last one idle (registers move by groups of four)
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;   // 256 x 200 + 128 x 104 = the launch's 384 x 168
-constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+constexpr int kRegsSoftmax = 104, kRegsOther = 64;   // 512 x 104 + 128 x 64 = the launch's 640 x 96
+constexpr int kSmem = (2 + kStages) * kTileBytes;
 constexpr int kItem = 2;                     // what an item costs besides its tiles, in tiles
 constexpr float kFollow = 8.0f;
-constexpr int kPoly = 2;                     // of 8 pairs of exponentials, those made by a polynomial
 
 struct Maps {
   CUtensorMap K, V;
@@ -58,12 +59,13 @@ __device__ __forceinline__ int tiles_of(const SeqView& v, int g, int m, bool cau
 struct Piece {
   int s, h, m, M, t0, t1, T;
   SeqView v;
-  int64_t left;     // units of the CTA's share behind the piece
+  int left;         // units of the CTA's share behind the piece
+  int more;         // whether there was one (told to the other warp of a pair)
 };
 // The piece of an item from its unit u on; false if the share ends before the item's first tile.
 __device__ __forceinline__ bool enter(Piece& p, int u, int g, bool causal) {
   p.T = tiles_of(p.v, g, p.m, causal);
-  const int take = (int)min((int64_t)(p.T + kItem - u), p.left);
+  const int take = min(p.T + kItem - u, p.left);
   p.left -= take;
   p.t0 = max(u - kItem, 0);
   p.t1 = u + take - kItem;
@@ -86,6 +88,27 @@ __device__ __forceinline__ bool next(Piece& p, const BatchView& b, int g, bool c
   return enter(p, 0, g, causal);
 }
 
+// Barrier of the two warps that share 32 rows.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// A warp's common place moved on by its first lane.
+__device__ __forceinline__ bool next_of_warp(Piece& p, const BatchView& b, int g, bool causal, int lane) {
+  __syncwarp();
+  bool more = false;
+  if (lane == 0) more = next(p, b, g, causal);
+  more = __shfl_sync(0xffffffffu, more, 0);
+  __syncwarp();
+  return more;
+}
+
+// The same for the two warps of a barrier.
+__device__ __forceinline__ bool next_of_pair(Piece& p, const BatchView& b, int g, bool causal, int id, bool first) {
+  pair_sync(id);
+  if (first) p.more = next(p, b, g, causal);
+  pair_sync(id);
+  return p.more;
+}
+
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -94,16 +117,13 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, 
       "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -158,65 +178,57 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// 2^x of a pair on the multiply-add units, for x <= 2^6: the nearest whole number taken off by adding and
-// subtracting 1.5 2^23 (its bits end up in the sum's last places), a polynomial of degree 5 for the
-// rest in [-1/2, 1/2] (least relative error with constant 1, 1.9e-7 evaluated in float32), the whole
-// number added to the exponent. Below 2^-126 the result is about 2^-126.
-__device__ __forceinline__ void ex2_poly(uint64_t x2, float& a, float& b) {
-  const float kRound = 12582912.0f;
-  float x, y;
-  unpair(x2, x, y);
-  x2 = pair_of(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
-  const uint64_t n = add2(x2, pair_of(kRound, kRound));
-  const uint64_t f = fma2(add2(n, pair_of(-kRound, -kRound)), pair_of(-1.0f, -1.0f), x2);
-  uint64_t q = fma2(f, pair_of(0.001326472731307149f, 0.001326472731307149f), pair_of(0.009671512991189957f, 0.009671512991189957f));
-  q = fma2(q, f, pair_of(0.05550733581185341f, 0.05550733581185341f));
-  q = fma2(q, f, pair_of(0.24022242426872253f, 0.24022242426872253f));
-  q = fma2(q, f, pair_of(0.6931470036506653f, 0.6931470036506653f));
-  q = fma2(q, f, pair_of(1.0f, 1.0f));
-  float n0, n1, q0, q1;
-  unpair(n, n0, n1);
-  unpair(q, q0, q1);
-  a = __int_as_float(__float_as_int(q0) + (__float_as_int(n0) << 23));
-  b = __int_as_float(__float_as_int(q1) + (__float_as_int(n1) << 23));
-}
-
-// One row's weights 2^(s scale2 + sub), rounded to the type, written over its scores (tS); their sum
-// goes to l unrounded. kP of 8 pairs are made by the polynomial, so that the special function unit
-// is not what the two softmax groups wait for. The first half is announced while the second is made.
-template <typename T, int kP>
-__device__ __forceinline__ void weights(const float (&s)[kHalf], float scale2, float sub, float& l, uint32_t tS,
+// The weights 2^(s scale2 + sub) of half a row, rounded to the type, written to Tensor Memory (tP); their
+// sum goes to l unrounded. The first half is announced while the second is made. (Making 1 or 2 of 8
+// exponentials by a polynomial on the multiply-add units, to spare the special function unit, gave 0 and
+// -8 % on a chunk of 2048 tokens over 32768 keys.)
+template <typename T>
+__device__ __forceinline__ void weights(const float (&s)[64], float scale2, float sub, float& l, uint32_t tP,
                                         uint64_t* lo, uint64_t* hi, int lane) {
   const uint64_t sc = pair_of(scale2, scale2), sb = pair_of(sub, sub);
   uint64_t sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 2; ++c) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const uint64_t x2 = fma2(pair_of(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sc, sb);
       float x, y;
-      if ((i & 7) < kP) {
-        ex2_poly(x2, x, y);
-      } else {
-        unpair(x2, x, y);
-        x = ex2(x);
-        y = ex2(y);
-      }
+      unpair(x2, x, y);
+      x = ex2(x);
+      y = ex2(y);
       sum[i & 1] = add2(sum[i & 1], pair_of(x, y));
       w[i] = pack2(T(), x, y);
     }
-    tmem_st16(tS + 16 * c, w);
-    if (c & 1) {
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c == 3 ? hi : lo);
-    }
+    tmem_st16(tP + 16 * c, w);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c ? hi : lo);
   }
   float x, y;
   unpair(add2(sum[0], sum[1]), x, y);
   l += x + y;
+}
+
+// Four lanes each hold four 16-byte blocks; afterwards block k of a lane is its own numbered block of
+// the group's lane k.
+__device__ __forceinline__ void transpose4(uint32_t (&y)[4][4], int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & d) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t give = up ? y[k][e] : y[k | d][e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+        if (up) y[k][e] = got;
+        else y[k | d][e] = got;
+      }
+    }
+  }
 }
 
 // A bounded wait that also ends when another role of the CTA has given up. The clock is looked at
@@ -237,10 +249,11 @@ struct Waits {
           : "r"(a), "r"(parity)
           : "memory");
       if (done) return true;
+      if (*gave_up) return false;
       if ((it & 63) == 0) {
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
-        if (*gave_up || now - t0 > kWaitLimitNs) {
+        if (now - t0 > kWaitLimitNs) {
           *gave_up = 1;
           atomicOr(status, PST_TIMEOUT);
           return false;
@@ -253,14 +266,14 @@ struct Waits {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_chunk(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws, int box) {
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(1024) uint8_t sm[];   // what is static takes the rest, 3 KB
   __shared__ __align__(8) Bars bar;
   __shared__ uint32_t tmem_s;
   __shared__ int gave_up;
-  __shared__ Piece first_s;
+  __shared__ Piece piece_s[kSoftmaxWarps / 2 + 4];   // places on the line: the softmax pairs', the others'
   __shared__ bool any_s;
+  __shared__ __align__(8) float both_s[2][2][kHalf];   // what the two threads of a row tell each other
   __shared__ int64_t range_s[3];   // all units, the end of this CTA's, CTAs with work
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchView& b = a.b;
   const int g = a.Hq / b.heads;
@@ -275,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.q_full[t], 32);
       mbar_init(&bar.q_empty[t], 1);
       mbar_init(&bar.s_full[t], 1);
-      mbar_init(&bar.p_lo[t], 4);
-      mbar_init(&bar.p_hi[t], 4);
+      mbar_init(&bar.p_lo[t], kSoftmaxWarps / 2);
+      mbar_init(&bar.p_hi[t], kSoftmaxWarps / 2);
       mbar_init(&bar.o_full[t], 1);
-      mbar_init(&bar.o_empty[t], 4);
+      mbar_init(&bar.o_empty[t], kSoftmaxWarps / 2);
     }
     mbar_init(&bar.tail, 1);
     gave_up = 0;
@@ -294,12 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = 0; m < M; ++m) n += tiles_of(v, g, m, causal) + kItem;
         return n * b.heads;
       },
-      kItem + 2);
+      kItem + 2, reinterpret_cast<int64_t*>(both_s));
   if ((int)blockIdx.x >= st.G) {
     if (tid == 0) ws.list[blockIdx.x].s = -1;
     return;
   }
-  if (warp == 8) {
+  if (warp == kSoftmaxWarps) {
     tmem_alloc(&tmem_s, 512);
     tmem_relinquish();
   }
@@ -314,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     at %= per;
     p.m = 0;
     for (int n; at >= (n = tiles_of(p.v, g, p.m, causal) + kItem); at -= n) ++p.m;
-    p.left = st.hi - st.lo;
+    p.left = (int)(st.hi - st.lo);
     any_s = enter(p, (int)at, g, causal);   // a share can lie in an item's first units only
-    first_s = p;
+    for (Piece& q : piece_s) q = p;
     range_s[0] = st.W;
     range_s[1] = st.hi;
     range_s[2] = st.G;
@@ -332,32 +345,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (!any_s) {
     // nothing to do: on to the end
-  } else if (warp >= 8) {
+  } else if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) {
+    if (warp == kSoftmaxWarps) {
       // ---------------------------------------------------------------- MMA issue
       if (elect_one()) {
-        Piece p = first_s;
+        Piece& p = piece_s[kSoftmaxWarps / 2];
         constexpr uint32_t id_qk = idesc<T>(), id_pv = idesc<T>() | (1u << 16);   // V: MN-major
         uint32_t kv = 0, pieces[2] = {0, 0}, tiles[2] = {0, 0};
         bool ok = true;
         auto full = [&](uint32_t i) { return wait(&bar.kv_full[i % kStages], (i / kStages) & 1); };
         auto qk = [&](int t, uint32_t i) {
-          const uint32_t A = smem_u32(Qs + t * kTileBytes), B = smem_u32(ring + (i % kStages) * kTileBytes);
+          const uint64_t A = desc_kmajor_sw128(smem_u32(Qs + t * kTileBytes));
+          const uint64_t B = desc_kmajor_sw128(smem_u32(ring + (i % kStages) * kTileBytes));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * kHalfTile + (k & 3) * 32;
-            umma_bf16(tmem + t * kHalf, desc_kmajor_sw128(A + off), desc_kmajor_sw128(B + off), id_qk, k != 0);
+          for (int k = 0; k < 8; ++k) {   // the address field counts 16 bytes
+            const uint32_t off = ((k >> 2) * kHalfTile + (k & 3) * 32) >> 4;
+            umma_bf16(tmem + t * kHalf, A + off, B + off, id_qk, k != 0);
           }
           umma_commit(&bar.s_full[t]);
         };
         do {
           const int nt = p.t1 - p.t0;
           const int two = p.v.n * g - p.m * kBlockRows > kHalf ? 2 : 1;
-          for (int t = 0; t < two && ok; ++t) ok = wait(&bar.q_full[t], pieces[t] & 1);
-          if (!ok || !(ok = full(kv))) break;
-          tc_fence_after();
-          for (int t = 0; t < two; ++t) qk(t, kv);
+          if (!(ok = full(kv))) break;
+          for (int t = 0; t < two; ++t) {
+            if (!(ok = wait(&bar.q_full[t], pieces[t] & 1))) break;
+            tc_fence_after();
+            qk(t, kv);
+          }
+          if (!ok) break;
           umma_commit(&bar.kv_empty[kv % kStages]);
           if (nt == 1)
             for (int t = 0; t < two; ++t) umma_commit(&bar.q_empty[t]);
@@ -369,17 +386,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = wait(&bar.p_lo[t], tiles[t] & 1))) break;
               if (j == 0 && !(ok = wait(&bar.o_empty[t], (pieces[t] & 1) ^ 1))) break;
               tc_fence_after();
-              const uint32_t B = smem_u32(ring + (iv % kStages) * kTileBytes);
+              const uint64_t B = desc_mnmajor_sw128(smem_u32(ring + (iv % kStages) * kTileBytes), kHalfTile, 1024);
+              // 16 keys a step: the first 32 of each 64 are announced first
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, desc_mnmajor_sw128(B + k * 2048, kHalfTile, 1024),
-                        id_pv, (j | k) != 0);
-              if (!(ok = wait(&bar.p_hi[t], tiles[t] & 1))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 4; k < 8; ++k)
-                umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, desc_mnmajor_sw128(B + k * 2048, kHalfTile, 1024),
-                        id_pv, 1);
+              for (int i = 0; i < 8; ++i) {
+                const int k = (i & 1) | ((i & 2) << 1) | ((i & 4) >> 1);   // 0 1 4 5 2 3 6 7
+                if (i == 4) {
+                  if (!(ok = wait(&bar.p_hi[t], tiles[t] & 1))) break;
+                  tc_fence_after();
+                }
+                umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, B + k * (2048 >> 4), id_pv, (j | i) != 0);
+              }
+              if (!ok) break;
               ++tiles[t];
               if (more) {
                 if (t == 0 && !(ok = full(ik))) break;
@@ -398,23 +416,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < two; ++t) ++pieces[t];
         } while (ok && next(p, b, g, causal));
       }
-    } else if (warp == 9) {
+    } else if (warp == kSoftmaxWarps + 1) {
       // ---------------------------------------------------------------- keys and values
-      Piece p = first_s;
+      Piece& p = piece_s[warp - kSoftmaxWarps / 2];
       uint32_t kv = 0, tails = 0;
       const int per = kHalf / box;           // boxes of a tile: one lane each
       prefetch_tensormap(&maps.K);
       prefetch_tensormap(&maps.V);
       bool ok = true;
       do {
-        for (int j = p.t0; j < p.t1 && ok; ++j) {
+        const int t0 = p.t0, t1 = p.t1, len = p.v.len, h = p.h, seq = p.s;
+        for (int j = t0; j < t1 && ok; ++j) {
           const int key = j * kHalf + lane * box;     // this lane's box
           int page = -1;
-          const bool mine = lane < per && key < p.v.len;
-          if (mine) page = page_of(b, p.s, key);
+          const bool mine = lane < per && key < len;
+          if (mine) page = page_of(b, seq, key);
           const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
           const bool whole = __all_sync(0xffffffffu, !mine || page >= 0);
-          const bool ends = (j + 1) * kHalf > p.v.len;
+          const bool ends = (j + 1) * kHalf > len;
           for (int kind = 0; kind < 2; ++kind, ++kv) {
             const uint32_t s = kv % kStages;
             ok = __all_sync(0xffffffffu, wait(&bar.kv_empty[s], ((kv / kStages) & 1) ^ 1));
@@ -430,15 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (page >= 0) {
               const CUtensorMap* map = kind ? &maps.V : &maps.K;
               const int row = key % b.page_size;
-              tma_load_4d(dst + lane * box * 128, map, fb, 0, row, p.h, page);
-              tma_load_4d(dst + kHalfTile + lane * box * 128, map, fb, 64, row, p.h, page);
+              tma_load_4d(dst + lane * box * 128, map, fb, 0, row, h, page);
+              tma_load_4d(dst + kHalfTile + lane * box * 128, map, fb, 64, row, h, page);
             }
             if (fix) {
               ok = __all_sync(0xffffffffu, wait(&bar.tail, tails & 1));
               ++tails;
               if (!ok) break;
               for (int r = lane; r < kHalf; r += 32) {
-                if (((good >> (r / box)) & 1) && j * kHalf + r < p.v.len) continue;
+                if (((good >> (r / box)) & 1) && j * kHalf + r < len) continue;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                   *reinterpret_cast<uint4*>(dst + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
@@ -451,63 +470,67 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-      } while (ok && next(p, b, g, causal));
+      } while (ok && next_of_warp(p, b, g, causal, lane));
       if (!ok) {   // copies in flight land before the CTA's memory is given up
         const uint32_t n = min(kv, (uint32_t)kStages);
         for (uint32_t i = kv - n; i < kv; ++i) mbar_wait(&bar.kv_full[i % kStages], (i / kStages) & 1, 1u << 20);
       }
-    } else if (warp == 10) {
-      // ---------------------------------------------------------------- queries
-      Piece p = first_s;
-      const int c16 = lane & 15, r2 = lane >> 4;
+    } else {
+      // ---------------------------------------------------------------- queries: a warp a half block
+      Piece& p = piece_s[warp - kSoftmaxWarps / 2];
+      const int t = warp - kSoftmaxWarps - 2, c16 = lane & 15, r2 = lane >> 4;
       const int step_t = 2 / g, step_h = 2 % g;       // from a row to the one two further
-      uint32_t pieces[2] = {0, 0};
+      uint32_t pieces = 0;
       bool ok = true;
       do {
-        for (int t = 0; t < 2 && ok; ++t) {
-          const int R = p.v.n * g, r0 = p.m * kBlockRows + t * kHalf;
-          if (r0 >= R) break;
-          ok = __all_sync(0xffffffffu, wait(&bar.q_empty[t], (pieces[t] & 1) ^ 1));
-          if (!ok) break;
-          ++pieces[t];
-          int tok = (r0 + r2) / g, hd = (r0 + r2) - tok * g;
-          const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g * a.q_hs + 8 * c16;
-          const uint32_t dst = smem_u32(Qs + t * kTileBytes + (c16 >> 3) * kHalfTile);
-#pragma unroll 8
-          for (int i = 0; i < kHalf / 2; ++i) {
-            const int rr = 2 * i + r2;
-            const bool in = r0 + rr < R;
-            const T* src = in ? Q + (int64_t)tok * a.q_ts + (int64_t)hd * a.q_hs : Q;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4)),
-                         "l"(src), "r"(in ? 16u : 0u)
-                         : "memory");
-            tok += step_t;
-            hd += step_h;
-            if (hd >= g) {
-              hd -= g;
-              ++tok;
-            }
+        const int R = p.v.n * g, r0 = p.m * kBlockRows + t * kHalf;
+        if (r0 >= R) continue;
+        ok = __all_sync(0xffffffffu, wait(&bar.q_empty[t], (pieces & 1) ^ 1));
+        if (!ok) break;
+        ++pieces;
+        int tok = (r0 + r2) / g, hd = (r0 + r2) - tok * g;
+        const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g * a.q_hs + 8 * c16;
+        const uint32_t dst = smem_u32(Qs + t * kTileBytes + (c16 >> 3) * kHalfTile);
+#pragma unroll 4
+        for (int i = 0; i < kHalf / 2; ++i) {
+          const int rr = 2 * i + r2;
+          const bool in = r0 + rr < R;
+          const T* src = in ? Q + (int64_t)tok * a.q_ts + (int64_t)hd * a.q_hs : Q;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4)),
+                       "l"(src), "r"(in ? 16u : 0u)
+                       : "memory");
+          tok += step_t;
+          hd += step_h;
+          if (hd >= g) {
+            hd -= g;
+            ++tok;
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_async_shared();
-          mbar_arrive(&bar.q_full[t]);
         }
-      } while (ok && next(p, b, g, causal));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_shared();
+        mbar_arrive(&bar.q_full[t]);
+      } while (next_of_warp(p, b, g, causal, lane));
     }
   } else {
-    // ------------------------------------------------------------------ softmax: a thread a row
+    // ------------------------------------------------------------------ softmax: two threads a row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    Piece p = first_s;
-    const int t = warp >> 2, wq = warp & 3;
-    const uint32_t tS = tmem + t * kHalf + ((uint32_t)(32 * wq) << 16), tO = tS + 2 * kHalf;
+    Piece& p = piece_s[4 * (warp >> 3) + (warp & 3)];
+    const int t = warp >> 3, side = (warp >> 2) & 1, wq = warp & 3;   // half block, half of the keys (features), rows
+    const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+    const uint32_t tS = tmem + t * kHalf + lanes + 64 * side;
+    const uint32_t tP = tmem + t * kHalf + lanes + 32 * side;
+    const uint32_t tO = tmem + (2 + t) * kHalf + lanes + 64 * side;
+    float* mine = &both_s[t][side][32 * wq + lane];
+    float* other = &both_s[t][side ^ 1][32 * wq + lane];
     const bool neg = a.scale < 0.0f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // not 0: a masked score times 0 is no number
     uint32_t tiles = 0, pieces = 0;
-    bool ok = true;
+    // A wait that gives up does not end this role: the barriers of a pair need both of its warps, and
+    // the other waits give up at once then. The result is reported as void.
     do {
       const int R = p.v.n * g, r0 = p.m * kBlockRows + t * kHalf;
       const bool began = p.t0 == 0, ends = p.t1 == p.T;
-      if (tid == 0 && began && !ends)   // the share's last piece: left is what it has of the item
+      if (tid == 0 && began && !ends)   // the share's last piece
         ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[1] + (p.T - p.t1) - 1, range_s[0], range_s[2]), 1};
       if (r0 >= R) continue;
       const int r = r0 + 32 * wq + lane;
@@ -515,34 +538,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = causal ? p.v.len - p.v.n + tok : p.v.len - 1;
       const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);      // the least of the warp's rows
       float m = -INFINITY, l = 0.0f;
-      for (int j = p.t0; j < p.t1; ++j) {
-        ok = __all_sync(0xffffffffu, wait(&bar.s_full[t], tiles & 1));
-        if (!ok) break;
+      const int t0 = p.t0, t1 = p.t1;
+      for (int j = t0; j < t1; ++j) {
+        wait(&bar.s_full[t], tiles & 1);
+        __syncwarp();
         ++tiles;
         tc_fence_after();
-        float s[kHalf];
+        float s[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
         tmem_ld_wait();
         if (neg) {
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) s[i] = -s[i];
+          for (int i = 0; i < 64; ++i) s[i] = -s[i];
         }
-        const bool edge = j * kHalf + kHalf - 1 > lim_warp;
-        if (edge) {
-          const int rel = lim - j * kHalf;
+        const int key0 = j * kHalf + 64 * side;
+        if (key0 + 63 > lim_warp) {
+          const int rel = lim - key0;
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) s[i] = i > rel ? -INFINITY : s[i];
+          for (int i = 0; i < 64; ++i) s[i] = i > rel ? -INFINITY : s[i];
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < kHalf - 4; i += 8)
+        for (int i = 4; i < 60; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[kHalf - 4 + k]);
-        const float mn = max3(m, max3(mx[0], mx[1], mx[2]) * scale2, mx[3] * scale2);
-        if (j == p.t0) {
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
+        const float mh = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+        *mine = mh;
+        pair_sync(1 + 4 * t + wq);   // both have read their scores now: weights may overwrite them
+        const float mn = fmaxf(m, fmaxf(mh, *other) * scale2);
+        if (j == t0) {
           m = mn;
         } else if (__any_sync(0xffffffffu, mn - m > kFollow)) {
           const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
@@ -551,21 +578,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the scores being complete, so is every earlier product: the output is at rest
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * c, o);
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * c, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(tO + 32 * c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(tO + 16 * c, o);
           }
         }
         const float sub = m == -INFINITY ? 0.0f : -m;
-        if (edge) weights<T, 0>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
-        else weights<T, kPoly>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
+        weights<T>(s, scale2, sub, l, tP, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
-      if (!ok) break;
-      ok = __all_sync(0xffffffffu, wait(&bar.o_full[t], pieces & 1));
-      if (!ok) break;
+      *mine = l;
+      pair_sync(1 + 4 * t + wq);
+      l = side ? *other + l : l + *other;
+      wait(&bar.o_full[t], pieces & 1);
+      __syncwarp();
       ++pieces;
       tc_fence_after();
       const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g + (rc - tok * g);
@@ -583,58 +611,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float il = l > 0.0f ? 1.0f / l : 0.0f;
         inv *= il;
         w *= il;
+        // Four lanes (four rows) exchange their 16-byte blocks, so that a store writes 64 bytes of a row
+        const int64_t out_row = row * kD + 64 * side + 8 * (lane & 3);
+        const uint32_t live = __ballot_sync(0xffffffffu, r < R);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_ld_wait();
-          if (r < R) {
-            float y[32];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t y[4][4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * inv;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[16];
+            tmem_ld16(tO + 32 * c + 16 * h, o);
+            tmem_ld_wait();
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * inv;
             if (w > 0.0f) {
-              const float4* pre = reinterpret_cast<const float4*>(a.pre_out + row * kD + 32 * c);
+              const float4* pre = reinterpret_cast<const float4*>(a.pre_out + row * kD + 64 * side + 32 * c + 16 * h);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < 4; ++i) {
                 const float4 x = pre[i];
-                y[4 * i] = fmaf(w, x.x, y[4 * i]);
-                y[4 * i + 1] = fmaf(w, x.y, y[4 * i + 1]);
-                y[4 * i + 2] = fmaf(w, x.z, y[4 * i + 2]);
-                y[4 * i + 3] = fmaf(w, x.w, y[4 * i + 3]);
+                v[4 * i] = fmaf(w, x.x, v[4 * i]);
+                v[4 * i + 1] = fmaf(w, x.y, v[4 * i + 1]);
+                v[4 * i + 2] = fmaf(w, x.z, v[4 * i + 2]);
+                v[4 * i + 3] = fmaf(w, x.w, v[4 * i + 3]);
               }
             }
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + row * kD + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack2(T(), y[8 * i], y[8 * i + 1]), pack2(T(), y[8 * i + 2], y[8 * i + 3]),
-                                  pack2(T(), y[8 * i + 4], y[8 * i + 5]), pack2(T(), y[8 * i + 6], y[8 * i + 7]));
+            for (int i = 0; i < 8; ++i) y[2 * h + (i >> 2)][i & 3] = pack2(T(), v[2 * i], v[2 * i + 1]);
+          }
+          transpose4(y, lane);   // y[k]: block (lane & 3) of the row of lane (lane & ~3) + k
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int from = (lane & ~3) + k;
+            const int64_t at = __shfl_sync(0xffffffffu, out_row, from) + 32 * c + 8 * ((lane & 3) - k);
+            if ((live >> from) & 1)
+              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + at) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
           }
         }
-        if (a.lse && r < R) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (a.lse && side == 0 && r < R) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
       } else {
-        const int64_t slot = ((int64_t)blockIdx.x * 2 + (began ? 1 : 0)) * kBlockRows + t * kHalf + 32 * wq + lane;
+        // parts: blocks of four features, rows next to one another
+        const int64_t slot = (int64_t)blockIdx.x * 2 + (began ? 1 : 0);
+        const int row_in = t * kHalf + 32 * wq + lane;
+        float4* dst = reinterpret_cast<float4*>(ws.o) + (slot * 32 + 16 * side) * kBlockRows + row_in;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
+          uint32_t o[16];
+          tmem_ld16(tO + 16 * c, o);
           tmem_ld_wait();
           if (r < R) {
-            uint4* dst = reinterpret_cast<uint4*>(ws.o + slot * kD + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 4; ++i)
+              dst[(4 * c + i) * kBlockRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
           }
         }
-        if (r < R) ws.ml[slot] = make_float2(m, l);
+        if (side == 0 && r < R) ws.ml[slot * kBlockRows + row_in] = make_float2(m, l);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_empty[t]);
-    } while (next(p, b, g, causal));
+    } while (next_of_pair(p, b, g, causal, 1 + 4 * t + wq, side == 0 && lane == 0));
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == kSoftmaxWarps) tmem_dealloc(tmem, 512);
 }
 
 template <typename T>

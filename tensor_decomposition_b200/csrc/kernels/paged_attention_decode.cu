@@ -102,11 +102,12 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttnArgs a, const Workspace ws) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ float2 ml_s[kWarps][kRows];
+  __shared__ int64_t scan_s[kWarps + 3];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, pair = lane & 3;
   const BatchView& b = a.b;
   grid_release();
   const Start st = find_start<kThreads>(
-      b.num_seqs, [&](int s) { return (int64_t)units_of(seq_view(b, s)) * b.heads; }, kMinUnits);
+      b.num_seqs, [&](int s) { return (int64_t)units_of(seq_view(b, s)) * b.heads; }, kMinUnits, scan_s);
   if ((int)blockIdx.x >= st.G) {
     if (tid == 0) ws.list[blockIdx.x].s = -1;
     return;

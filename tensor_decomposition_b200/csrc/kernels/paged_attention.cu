@@ -14,41 +14,79 @@ namespace {
 using namespace pattn;
 
 // The items that lie in several CTAs' shares, the parts weighted by their maxima. Parts of up to 16
-// rows lie row by row: a warp a row.
+// rows lie row by row: four rows a CTA, four warps a row (one warp a row took 0.25 us a part).
+constexpr int kSubs = 4;
 template <typename T>
-__global__ void __launch_bounds__(128) k_attn_combine(const PagedAttnArgs a, const Workspace ws) {
+__global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, const Workspace ws) {
+  __shared__ float4 y_s[4][kSubs][32];
+  __shared__ float2 ml_s[4][kSubs];
   grid_wait();
   const Split sp = ws.list[blockIdx.x];
   if (sp.s < 0) return;
-  const int lane = threadIdx.x & 31, c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & 3, rw = warp >> 2;
+  const int c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
   const SeqView v = seq_view(a.b, sp.s);
   const int g = a.Hq / a.b.heads, R = v.n * g;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (r >= R) return;
-  float mx = -INFINITY;
-  for (int c = lane; c < parts; c += 32) {
-    const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
-    mx = fmaxf(mx, ws.ml[at].x);
-  }
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+  const int r = blockIdx.y * 4 + rw;
+  if ((int)blockIdx.y * 4 >= R) return;
+  float mx = -INFINITY, ls = 0.0f;
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float ls = 0.0f;
-  if (mx != -INFINITY) {
-#pragma unroll 4
-    for (int c = 0; c < parts; ++c) {
-      const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
-      const float2 p = ws.ml[at];
-      const float4 x = *reinterpret_cast<const float4*>(ws.o + at * kD + 4 * lane);
-      const float f = ex2(p.x - mx);
-      ls = fmaf(p.y, f, ls);
+  if (r < R) {
+    for (int b0 = 0; b0 < parts; b0 += 8 * kSubs) {   // eight parts in flight
+      float2 p[8];
+      float4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = b0 + sub + kSubs * i;
+        p[i] = make_float2(-INFINITY, 0.0f);
+        x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < parts) {
+          const int64_t at = ((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * ws.rows + r;
+          p[i] = ws.ml[at];
+          x[i] = *reinterpret_cast<const float4*>(ws.o + at * kD + 4 * lane);
+        }
+      }
+      float mn = mx;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mn = fmaxf(mn, p[i].x);
+      if (mn == -INFINITY) continue;
+      const float f0 = ex2(mx - mn);
+      mx = mn;
+      ls *= f0;
+      y.x *= f0; y.y *= f0; y.z *= f0; y.w *= f0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = ex2(p[i].x - mn);
+        ls = fmaf(p[i].y, f, ls);
+        y.x = fmaf(x[i].x, f, y.x);
+        y.y = fmaf(x[i].y, f, y.y);
+        y.z = fmaf(x[i].z, f, y.z);
+        y.w = fmaf(x[i].w, f, y.w);
+      }
+    }
+    y_s[rw][sub][lane] = y;
+    if (lane == 0) ml_s[rw][sub] = make_float2(mx, ls);
+  }
+  __syncthreads();
+  if (r >= R || sub != 0) return;
+  float mn = mx;
+#pragma unroll
+  for (int i = 1; i < kSubs; ++i) mn = fmaxf(mn, ml_s[rw][i].x);
+  y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  ls = 0.0f;
+  if (mn != -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < kSubs; ++i) {
+      const float f = ex2(ml_s[rw][i].x - mn);
+      const float4 x = y_s[rw][i][lane];
+      ls = fmaf(ml_s[rw][i].y, f, ls);
       y.x = fmaf(x.x, f, y.x);
       y.y = fmaf(x.y, f, y.y);
       y.z = fmaf(x.z, f, y.z);
       y.w = fmaf(x.w, f, y.w);
     }
   }
-  finish_row<T>(a, (int64_t)(v.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y, mx, ls);
+  finish_row<T>(a, (int64_t)(v.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y, mn, ls);
 }
 
 // The same for blocks of 256 rows, whose parts lie in blocks of four features with the rows next to one
@@ -100,7 +138,7 @@ template <typename T>
 cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid, p.decode ? 4 : 8);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(p.decode ? 512 : 128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];   // placed while the parts are still computed; waits for them itself
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -119,12 +157,22 @@ size_t ml_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * 
 
 }  // namespace
 
-// Up to 16 rows of a chunk reading one KV head run in the kernel for few rows, whose MMAs hold 16.
+// Up to 16 rows of a chunk reading one KV head run in the kernel for few rows, whose MMAs hold 16. Where
+// clusters of 8 CTAs, one for each item, all run at once (33 and more do not: 9.0 us instead of 5.9) and
+// their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0 instead of 7.7 us
+// at 1024 keys, 11.9 and 10.9 at 4096, 19.3 and 13.5 at 8192; 32 items: 26 instead of 32 at 8192).
+constexpr int kTeamTokens = 4096, kTeamItems = 32;
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   AttnPlan p;
   const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)a.b.max_q * (a.Hq / a.b.heads);
   p.decode = rows <= 16;
   p.rows = p.decode ? 16 : 256;
+  const int64_t items = (int64_t)a.b.heads * a.b.num_seqs;
+  if (p.decode && items <= kTeamItems && (tokens <= kTeamTokens || items >= kTeamItems - 4)) {
+    p.team = 1;
+    p.grid = (int)items * 8;
+    return p;
+  }
   const int unit = p.decode ? 64 : 128;
   const int64_t units = std::max<int64_t>(1, (tokens + unit - 1) / unit) * std::max<int64_t>(1, (rows + p.rows - 1) / p.rows) *
                         a.b.heads * a.b.num_seqs;
@@ -141,7 +189,7 @@ cudaError_t paged_attention(const PagedAttnArgs& a, const AttnPlan& p, void* scr
   w.list = reinterpret_cast<Split*>(at + o_bytes(p) + ml_bytes(p));
   w.rows = p.rows;
   const cudaError_t e = p.decode ? attn_decode(a, p, w, s) : attn_chunk(a, p, w, s);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.team) return e;
   return a.dtype == JOLT_BF16 ? combine<__nv_bfloat16>(a, p, w, s) : combine<__half>(a, p, w, s);
 }
 

@@ -686,7 +686,8 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
   Maps maps;
   maps.K = *static_cast<const CUtensorMap*>(a.kmap);
   maps.V = *static_cast<const CUtensorMap*>(a.vmap);
-  cudaError_t e = cudaFuncSetAttribute(k_attn_chunk<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static SmemFlags allowed;
+  cudaError_t e = allow_smem(k_attn_chunk<T>, kSmem, a.device, allowed);
   if (e != cudaSuccess) return e;
   k_attn_chunk<T><<<p.grid, kThreads, kSmem, s>>>(a, maps, w, box);
   note_launch();

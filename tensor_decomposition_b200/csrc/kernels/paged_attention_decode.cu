@@ -10,6 +10,8 @@
 // either way, and warps that run apart need no barrier. The weights enter the second product as
 // a rounded part and a rounded remainder (two MMAs), so that only the output's rounding is left.
 // Warps meet where an item ends or the share does.
+#include <cooperative_groups.h>
+
 #include "paged_attention.cuh"
 
 namespace jolt {
@@ -27,6 +29,8 @@ constexpr int kCtas = 2;                  // per SM
 constexpr int kRows = 16;
 constexpr int kMinUnits = 1;
 constexpr int kSmem = kWarps * kStages * 2 * kTile;
+constexpr int kTeamCtas = 8;
+constexpr int kTeamSmem = kSmem + kRows * kD * 4;
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -98,28 +102,44 @@ __device__ __forceinline__ void advance(Cursor& c, const BatchView& b) {
   } while (c.U == 0);
 }
 
-template <typename T>
+// kTeam: instead of a share of the line a CTA takes an eighth of the item of its cluster, and the cluster's
+// CTAs combine through one another's shared memory: one launch and no scratch.
+template <typename T, bool kTeam>
 __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttnArgs a, const Workspace ws) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ float2 ml_s[kWarps][kRows];
+  __shared__ float2 team_ml[kTeam ? kRows : 1];
   __shared__ int64_t scan_s[kWarps + 3];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, pair = lane & 3;
   const BatchView& b = a.b;
-  grid_release();
-  const Start st = find_start<kThreads>(
-      b.num_seqs, [&](int s) { return (int64_t)units_of(seq_view(b, s)) * b.heads; }, kMinUnits, scan_s);
-  if ((int)blockIdx.x >= st.G) {
-    if (tid == 0) ws.list[blockIdx.x].s = -1;
-    return;
-  }
   const int g = a.Hq / b.heads;
   const float scale2 = a.scale * kLog2e;
+  Start st{};
   Cursor lc;
-  lc.s = st.s;
-  lc.v = seq_view(b, st.s);
-  lc.U = units_of(lc.v);
-  lc.h = (int)((st.lo - st.base) / lc.U);
-  lc.u = (int)((st.lo - st.base) % lc.U);
+  if (kTeam) {
+    const int item = blockIdx.x / kTeamCtas, rank = blockIdx.x % kTeamCtas;
+    lc.s = item / b.heads;
+    lc.h = item % b.heads;
+    lc.v = seq_view(b, lc.s);
+    if (lc.v.n == 0) return;   // the whole cluster
+    lc.U = units_of(lc.v);
+    st.lo = (int64_t)rank * lc.U / kTeamCtas;
+    st.hi = (int64_t)(rank + 1) * lc.U / kTeamCtas;
+    lc.u = (int)st.lo;
+  } else {
+    grid_release();
+    st = find_start<kThreads>(
+        b.num_seqs, [&](int s) { return (int64_t)units_of(seq_view(b, s)) * b.heads; }, kMinUnits, scan_s);
+    if ((int)blockIdx.x >= st.G) {
+      if (tid == 0) ws.list[blockIdx.x].s = -1;
+      return;
+    }
+    lc.s = st.s;
+    lc.v = seq_view(b, st.s);
+    lc.U = units_of(lc.v);
+    lc.h = (int)((st.lo - st.base) / lc.U);
+    lc.u = (int)((st.lo - st.base) % lc.U);
+  }
   Cursor cc = lc;
   const int count = (int)(st.hi - st.lo);
 
@@ -305,7 +325,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttn
               reinterpret_cast<const float*>(sm + (w * kStages + stage) * 2 * kTile) + r * kD + 4 * (lane ^ ((r & 7) << 1)));
           y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
         }
-        if (whole) {
+        if (kTeam) {
+          *reinterpret_cast<float4*>(sm + kSmem + r * (4 * kD) + 16 * lane) = y;
+          if (lane == 0) team_ml[r] = make_float2(mx, ls);
+        } else if (whole) {
           const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
           finish_row<T>(a, row, lane, y, mx, ls);
         } else {
@@ -326,14 +349,66 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttn
     }
     if (i + 1 < count) advance(cc, b);
   }
-  if (tid == 0) ws.list[blockIdx.x] = split;
+  if (!kTeam) {
+    if (tid == 0) ws.list[blockIdx.x] = split;
+    return;
+  }
+  // the cluster's parts: CTA k finishes the rows k and k + 8, a warp each
+  if (count == 0 && tid < kRows) team_ml[tid] = make_float2(-INFINITY, 0.0f);
+  const cooperative_groups::cluster_group team = cooperative_groups::this_cluster();
+  team.sync();
+  const int r = blockIdx.x % kTeamCtas + kTeamCtas * warp;
+  if (r < cc.v.n * g) {
+    float2 p[kTeamCtas];
+    float4 x[kTeamCtas], y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float mx = -INFINITY, ls = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kTeamCtas; ++c) {
+      p[c] = *team.map_shared_rank(&team_ml[r], c);
+      x[c] = *reinterpret_cast<const float4*>(team.map_shared_rank(sm + kSmem + r * (4 * kD) + 16 * lane, c));
+    }
+#pragma unroll
+    for (int c = 0; c < kTeamCtas; ++c) mx = fmaxf(mx, p[c].x);
+#pragma unroll
+    for (int c = 0; c < kTeamCtas; ++c) {
+      if (p[c].x == -INFINITY) continue;   // no keys, and perhaps no output written
+      const float f = ex2(p[c].x - mx);
+      ls = fmaf(p[c].y, f, ls);
+      y.x = fmaf(x[c].x, f, y.x);
+      y.y = fmaf(x[c].y, f, y.y);
+      y.z = fmaf(x[c].z, f, y.z);
+      y.w = fmaf(x[c].w, f, y.w);
+    }
+    finish_row<T>(a, (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g, lane, y, mx, ls);
+  }
+  team.sync();   // no CTA leaves while another reads from it
 }
 
 template <typename T>
 cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k_attn_decode<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static SmemFlags allowed, allowed_team;
+  cudaError_t e;
+  if (p.team) {
+    e = allow_smem(k_attn_decode<T, true>, kTeamSmem, a.device, allowed_team);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kTeamSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kTeamCtas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_attn_decode<T, true>, a, w);
+  } else {
+    e = allow_smem(k_attn_decode<T, false>, kSmem, a.device, allowed);
+    if (e != cudaSuccess) return e;
+    k_attn_decode<T, false><<<p.grid, kThreads, kSmem, s>>>(a, w);
+  }
   if (e != cudaSuccess) return e;
-  k_attn_decode<T><<<p.grid, kThreads, kSmem, s>>>(a, w);
   note_launch();
   return cudaGetLastError();
 }

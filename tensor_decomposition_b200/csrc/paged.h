@@ -73,14 +73,15 @@ struct RopeArgs {
 };
 // Queries (and keys) normed and rotated, out of place or in place.
 cudaError_t norm_rope(jolt_dtype t, int tokens, const RowsIn& Q, const RowsOut& Qo, const RowsIn& K,
-                      const RowsOut& Ko, const RopeArgs& r, cudaStream_t s);
+                      const RowsOut& Ko, const RopeArgs& r, int sms, cudaStream_t s);
 // Keys (normed and rotated) and values written to the pages.
 cudaError_t paged_append(jolt_dtype t, const BatchView& b, const RowsIn& K, const RowsIn& V, void* K_pages,
-                         void* V_pages, const RopeArgs& r, cudaStream_t s);
+                         void* V_pages, const RopeArgs& r, int sms, cudaStream_t s);
 
 struct PagedAttnArgs {
   BatchView b;
   jolt_dtype dtype;
+  int32_t device;
   const void *K, *V;           // pages [num_pages][heads][page_size][128]
   const void *kmap, *vmap;     // their tensor maps (host CUtensorMap)
   const void* Q;
@@ -94,7 +95,7 @@ struct PagedAttnArgs {
 };
 // How a call is run: which kernel, its CTAs, the rows of an item's block and the scratch it needs.
 struct AttnPlan {
-  int32_t decode = 0, grid = 0, rows = 0;
+  int32_t decode = 0, team = 0, grid = 0, rows = 0;
   size_t bytes = 0;
 };
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms);

@@ -53,6 +53,7 @@ void give_slot(int dev, int32_t* p) {
 }
 
 cudaError_t sm_count(int dev, int* out) {
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
   static std::atomic<int> n[kDevices];
   int v = n[dev].load(std::memory_order_relaxed);
   if (v == 0) {
@@ -248,8 +249,12 @@ JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const v
     ko.p = K_out; ko.ts = ko_token_stride; ko.hs = ko_head_stride;
   }
   cudaStream_t s = (cudaStream_t)cuda_stream;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = sm_count(dev, &sms);
+  if (e != cudaSuccess) return cuda_fail(what, e);
   ProfScope prof("qk_norm_rope", s);
-  const cudaError_t e = norm_rope(dtype, tokens, q, qo, k, ko, rope_of(eps, positions, inv_freq, rope_dim, interleaved), s);
+  e = norm_rope(dtype, tokens, q, qo, k, ko, rope_of(eps, positions, inv_freq, rope_dim, interleaved), sms, s);
   return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
 }
 
@@ -275,9 +280,12 @@ JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* bat
   k.p = K; k.ts = k_token_stride; k.hs = k_head_stride; k.heads = H; k.w = k_weight;
   v.p = V; v.ts = v_token_stride; v.hs = v_head_stride; v.heads = H;
   cudaStream_t s = (cudaStream_t)cuda_stream;
+  int sms = 0;
+  cudaError_t e = sm_count(pages->device, &sms);
+  if (e != cudaSuccess) return cuda_fail(what, e);
   ProfScope prof("paged_append", s);
-  const cudaError_t e = paged_append(pages->shape.dtype, view_of(pages, batch), k, v, pages->K, pages->V,
-                                     rope_of(eps, positions, inv_freq, rope_dim, interleaved), s);
+  e = paged_append(pages->shape.dtype, view_of(pages, batch), k, v, pages->K, pages->V,
+                                     rope_of(eps, positions, inv_freq, rope_dim, interleaved), sms, s);
   return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
 }
 
@@ -307,6 +315,7 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   PagedAttnArgs a{};
   a.b = view_of(pages, batch);
   a.dtype = pages->shape.dtype;
+  a.device = pages->device;
   a.K = pages->K; a.V = pages->V;
   a.kmap = &pages->kmap; a.vmap = &pages->vmap;
   a.Q = Q; a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.Hq = q_heads;

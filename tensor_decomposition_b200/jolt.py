@@ -124,9 +124,9 @@ def _check(status: int):
 
 
 def _stream_ptr(cuda_stream):
-    if cuda_stream is None:
+    if cuda_stream is None:   # the raw handle: making a torch Stream object takes 3 us
         import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if hasattr(cuda_stream, "cuda_stream"):
         return ctypes.c_void_p(cuda_stream.cuda_stream)
     return ctypes.c_void_p(int(cuda_stream))
@@ -326,7 +326,7 @@ class Pages:
         self.heads, self.dtype, self.device = int(K_pages.shape[1]), K_pages.dtype, K_pages.get_device()
 
     def __del__(self):
-        if getattr(self, "handle", None):
+        if getattr(self, "handle", None) and _lib is not None:   # None while the interpreter shuts down
             _lib.jolt_pages_destroy(self.handle)
             self.handle = None
 
@@ -359,14 +359,13 @@ def _here(device):
 
 def _rows(t, name, tokens, heads, dtype, device):
     """(pointer, token stride, head stride) of a [tokens][heads][128] tensor with contiguous rows."""
-    if t.shape != (tokens, heads, 128) or t.dtype != dtype:
-        raise ValueError(f"{name} must be [{tokens}][{heads}][128] {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
-    s = t.stride()
-    if s[2] != 1:
+    if t.shape != (tokens, heads, 128) or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor [{tokens}][{heads}][128] {dtype} on device {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    ts, hs, one = t.stride()
+    if one != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), s[0] if tokens > 1 else 0, s[1] if heads > 1 else 0
+    return t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0
 
 
 def _array(t, name, shape, dtype, device):
@@ -380,10 +379,10 @@ def _array(t, name, shape, dtype, device):
 
 def _rope(positions, inv_freq, tokens, device):
     """(positions pointer, inv_freq pointer, rope_dim)."""
-    import torch
     if inv_freq is None:
         return None, None, 0
-    n = inv_freq.numel()
+    import torch
+    n = inv_freq.shape[0]
     return (_array(positions, "positions", (tokens,), torch.int32, device),
             _array(inv_freq, "inv_freq", (n,), torch.float32, device), 2 * n)
 

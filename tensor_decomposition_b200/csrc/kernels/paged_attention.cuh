@@ -3,7 +3,6 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 
 #include "../paged.h"
 
@@ -143,19 +142,6 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace pattn
-
-// Allow a kernel its dynamic shared memory, once a device (`done`: the kernel's own flags).
-struct SmemFlags {
-  std::atomic<bool> on[64] = {};
-};
-template <class K>
-inline cudaError_t allow_smem(K* kernel, int bytes, int device, SmemFlags& done) {
-  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-  if (done.on[device].load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.on[device].store(true, std::memory_order_release);
-  return e;
-}
 
 // The two kernels.
 cudaError_t attn_decode(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s);

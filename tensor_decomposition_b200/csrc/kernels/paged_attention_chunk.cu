@@ -15,6 +15,7 @@
 // The weights are rounded to the type of the values (the tensor pipe takes no wider ones); their sum
 // is not. A maximum that grows by less than 8 (in units of log 2) is not followed: weights up to 2^8
 // are as exact, and most rescalings of the output fall away.
+#include "f32x2.cuh"
 #include "paged_attention.cuh"
 #include "sm100.cuh"
 
@@ -23,6 +24,7 @@ namespace {
 
 using namespace pattn;
 using namespace sm100;
+using namespace f32x2;
 
 constexpr int kHalf = 128;                   // rows of a half block, keys of a tile
 constexpr int kBlockRows = 2 * kHalf;
@@ -91,6 +93,13 @@ __device__ __forceinline__ bool next(Piece& p, const BatchView& b, int g, bool c
 // Barrier of the two warps that share 32 rows.
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
+// And of the four that share them when both halves have the same rows.
+__device__ __forceinline__ void quad_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Whether an item's rows fill one half only: the halves then take its tiles in turn, with the same
+// queries, and their outputs are joined at the end.
+__device__ __forceinline__ bool solo(const Piece& p, int g) { return p.v.n * g - p.m * kBlockRows <= kHalf; }
+
 // A warp's common place moved on by its first lane.
 __device__ __forceinline__ bool next_of_warp(Piece& p, const BatchView& b, int g, bool causal, int lane) {
   __syncwarp();
@@ -154,25 +163,6 @@ __device__ __forceinline__ constexpr uint32_t idesc<__half>() {
   return idesc_f16_f32(kHalf, kHalf);
 }
 
-// Two float32 in one register pair, and its packed arithmetic.
-__device__ __forceinline__ uint64_t pair_of(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -228,6 +218,21 @@ __device__ __forceinline__ void transpose4(uint32_t (&y)[4][4], int lane) {
         else y[k | d][e] = got;
       }
     }
+  }
+}
+
+// Sixteen columns of a row's output times f0, and with those of half 1 times f1.
+__device__ __forceinline__ void output16(uint32_t t0, float f0, bool both, float f1, float (&v)[16]) {
+  uint32_t o[16];
+  tmem_ld16(t0, o);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * f0;
+  if (both) {
+    tmem_ld16(t0 + kHalf, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
   }
 }
 
@@ -352,11 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         Piece& p = piece_s[kSoftmaxWarps / 2];
         constexpr uint32_t id_qk = idesc<T>(), id_pv = idesc<T>() | (1u << 16);   // V: MN-major
-        uint32_t kv = 0, pieces[2] = {0, 0}, tiles[2] = {0, 0};
+        uint32_t kv = 0, queries[2] = {0, 0}, outputs[2] = {0, 0}, tiles[2] = {0, 0};
         bool ok = true;
         auto full = [&](uint32_t i) { return wait(&bar.kv_full[i % kStages], (i / kStages) & 1); };
-        auto qk = [&](int t, uint32_t i) {
-          const uint64_t A = desc_kmajor_sw128(smem_u32(Qs + t * kTileBytes));
+        auto qk = [&](int t, int q, uint32_t i) {   // scores of half t, from queries q and the stage
+          const uint64_t A = desc_kmajor_sw128(smem_u32(Qs + q * kTileBytes));
           const uint64_t B = desc_kmajor_sw128(smem_u32(ring + (i % kStages) * kTileBytes));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {   // the address field counts 16 bytes
@@ -365,55 +370,82 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit(&bar.s_full[t]);
         };
+        auto pv = [&](int t, uint32_t i, bool first) {   // output of half t (+)= its weights times the stage
+          if (!wait(&bar.p_lo[t], tiles[t] & 1)) return false;
+          if (first && !wait(&bar.o_empty[t], (outputs[t]++ & 1) ^ 1)) return false;
+          tc_fence_after();
+          const uint64_t B = desc_mnmajor_sw128(smem_u32(ring + (i % kStages) * kTileBytes), kHalfTile, 1024);
+          // 16 keys a step: the first 32 of each 64 are announced first
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const int k = (n & 1) | ((n & 2) << 1) | ((n & 4) >> 1);   // 0 1 4 5 2 3 6 7
+            if (n == 4) {
+              if (!wait(&bar.p_hi[t], tiles[t] & 1)) return false;
+              tc_fence_after();
+            }
+            umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, B + k * (2048 >> 4), id_pv, !first || n != 0);
+          }
+          ++tiles[t];
+          return true;
+        };
+        auto query = [&](int t) {
+          const bool in = wait(&bar.q_full[t], queries[t]++ & 1);
+          tc_fence_after();
+          return in;
+        };
         do {
           const int nt = p.t1 - p.t0;
-          const int two = p.v.n * g - p.m * kBlockRows > kHalf ? 2 : 1;
-          if (!(ok = full(kv))) break;
-          for (int t = 0; t < two; ++t) {
-            if (!(ok = wait(&bar.q_full[t], pieces[t] & 1))) break;
-            tc_fence_after();
-            qk(t, kv);
-          }
-          if (!ok) break;
-          umma_commit(&bar.kv_empty[kv % kStages]);
-          if (nt == 1)
-            for (int t = 0; t < two; ++t) umma_commit(&bar.q_empty[t]);
-          for (int j = 0; j < nt && ok; ++j) {
-            const uint32_t iv = kv + 1, ik = kv + 2;   // V of this tile, K of the next
-            const bool more = j + 1 < nt;
-            for (int t = 0; t < two; ++t) {
-              if (t == 0 && !(ok = full(iv))) break;
-              if (!(ok = wait(&bar.p_lo[t], tiles[t] & 1))) break;
-              if (j == 0 && !(ok = wait(&bar.o_empty[t], (pieces[t] & 1) ^ 1))) break;
+          if (solo(p, g)) {
+            // the halves take the tiles in turn, each ahead of the other by its softmax
+            const int lead = min(nt, 2);
+            if (!(ok = query(0))) break;
+            for (int j = 0; j < lead && (ok = full(kv)); ++j, ++kv) {
               tc_fence_after();
-              const uint64_t B = desc_mnmajor_sw128(smem_u32(ring + (iv % kStages) * kTileBytes), kHalfTile, 1024);
-              // 16 keys a step: the first 32 of each 64 are announced first
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int k = (i & 1) | ((i & 2) << 1) | ((i & 4) >> 1);   // 0 1 4 5 2 3 6 7
-                if (i == 4) {
-                  if (!(ok = wait(&bar.p_hi[t], tiles[t] & 1))) break;
-                  tc_fence_after();
-                }
-                umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, B + k * (2048 >> 4), id_pv, (j | i) != 0);
-              }
-              if (!ok) break;
-              ++tiles[t];
-              if (more) {
-                if (t == 0 && !(ok = full(ik))) break;
+              qk(j, 0, kv);
+              umma_commit(&bar.kv_empty[kv % kStages]);
+            }
+            if (ok && nt <= 2) umma_commit(&bar.q_empty[0]);
+            for (int j = 0; j < nt && ok; ++j) {
+              const int t = j & 1;
+              if (!(ok = full(kv) && pv(t, kv, j < 2))) break;
+              umma_commit(&bar.kv_empty[kv++ % kStages]);
+              if (j + 2 < nt) {
+                if (!(ok = full(kv))) break;
                 tc_fence_after();
-                qk(t, ik);
-                if (j + 2 == nt) umma_commit(&bar.q_empty[t]);
+                qk(t, 0, kv);
+                if (j + 3 == nt) umma_commit(&bar.q_empty[0]);
+                umma_commit(&bar.kv_empty[kv++ % kStages]);
               } else {
                 umma_commit(&bar.o_full[t]);
               }
             }
+          } else {
+            ok = full(kv);
+            for (int t = 0; t < 2 && ok; ++t)
+              if ((ok = query(t))) qk(t, t, kv);
             if (!ok) break;
-            umma_commit(&bar.kv_empty[iv % kStages]);
-            if (more) umma_commit(&bar.kv_empty[ik % kStages]);
-            kv += 2;
+            umma_commit(&bar.kv_empty[kv % kStages]);
+            if (nt == 1)
+              for (int t = 0; t < 2; ++t) umma_commit(&bar.q_empty[t]);
+            for (int j = 0; j < nt && ok; ++j, kv += 2) {
+              const uint32_t iv = kv + 1, ik = kv + 2;   // V of this tile, K of the next
+              const bool more = j + 1 < nt;
+              for (int t = 0; t < 2 && ok; ++t) {
+                if (!(ok = (t || full(iv)) && pv(t, iv, j == 0))) break;
+                if (more) {
+                  if (!(ok = t || full(ik))) break;
+                  tc_fence_after();
+                  qk(t, t, ik);
+                  if (j + 2 == nt) umma_commit(&bar.q_empty[t]);
+                } else {
+                  umma_commit(&bar.o_full[t]);
+                }
+              }
+              if (!ok) break;
+              umma_commit(&bar.kv_empty[iv % kStages]);
+              if (more) umma_commit(&bar.kv_empty[ik % kStages]);
+            }
           }
-          for (int t = 0; t < two; ++t) ++pieces[t];
         } while (ok && next(p, b, g, causal));
       }
     } else if (warp == kSoftmaxWarps + 1) {
@@ -425,16 +457,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensormap(&maps.V);
       bool ok = true;
       do {
-        const int t0 = p.t0, t1 = p.t1, len = p.v.len, h = p.h, seq = p.s;
-        for (int j = t0; j < t1 && ok; ++j) {
-          const int key = j * kHalf + lane * box;     // this lane's box
-          int page = -1;
-          const bool mine = lane < per && key < len;
-          if (mine) page = page_of(b, seq, key);
-          const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
-          const bool whole = __all_sync(0xffffffffu, !mine || page >= 0);
-          const bool ends = (j + 1) * kHalf > len;
-          for (int kind = 0; kind < 2; ++kind, ++kv) {
+        const int t0 = p.t0, nt = p.t1 - t0, len = p.v.len, h = p.h, seq = p.s;
+        const bool alone = solo(p, g);
+        for (int x = 0; x < 2 * nt && ok; ++x, ++kv) {
+            // K0 V0 K1 V1 ..., or as the halves take them in turn K0 K1 V0 K2 V1 K3 ... V(nt - 2) V(nt - 1)
+            int kind = x & 1, j = x >> 1;
+            if (alone && x > 0 && nt > 1) {
+              kind = x > 1 && ((x & 1) == 0 || x == 2 * nt - 1);
+              j = x == 1 ? 1 : x == 2 * nt - 1 ? nt - 1 : (x & 1) ? (x + 1) >> 1 : (x - 2) >> 1;
+            }
+            j += t0;
+            const int key = j * kHalf + lane * box;     // this lane's box
+            int page = -1;
+            const bool mine = lane < per && key < len;
+            if (mine) page = page_of(b, seq, key);
+            const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+            const bool whole = __all_sync(0xffffffffu, !mine || page >= 0);
+            const bool ends = (j + 1) * kHalf > len;
             const uint32_t s = kv % kStages;
             ok = __all_sync(0xffffffffu, wait(&bar.kv_empty[s], ((kv / kStages) & 1) ^ 1));
             if (!ok) break;
@@ -468,7 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&bar.kv_full[s]);
             }
-          }
         }
       } while (ok && next_of_warp(p, b, g, causal, lane));
       if (!ok) {   // copies in flight land before the CTA's memory is given up
@@ -521,28 +559,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tP = tmem + t * kHalf + lanes + 32 * side;
     const uint32_t tO = tmem + (2 + t) * kHalf + lanes + 64 * side;
     float* mine = &both_s[t][side][32 * wq + lane];
-    float* other = &both_s[t][side ^ 1][32 * wq + lane];
+    const float* other = &both_s[t][side ^ 1][32 * wq + lane];
     const bool neg = a.scale < 0.0f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // not 0: a masked score times 0 is no number
-    uint32_t tiles = 0, pieces = 0;
+    uint32_t tiles = 0, outputs[2] = {0, 0};
     // A wait that gives up does not end this role: the barriers of a pair need both of its warps, and
     // the other waits give up at once then. The result is reported as void.
     do {
-      const int R = p.v.n * g, r0 = p.m * kBlockRows + t * kHalf;
-      const bool began = p.t0 == 0, ends = p.t1 == p.T;
+      const bool alone = solo(p, g), began = p.t0 == 0, ends = p.t1 == p.T;
+      const int R = p.v.n * g, r0 = p.m * kBlockRows + (alone ? 0 : t * kHalf);
       if (tid == 0 && began && !ends)   // the share's last piece
         ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[1] + (p.T - p.t1) - 1, range_s[0], range_s[2]), 1};
-      if (r0 >= R) continue;
+      const int t1 = p.t1, every = alone ? 2 : 1, t0 = p.t0 + (alone ? t : 0);   // this half's tiles
+      const bool rows = r0 + 32 * wq < R;         // whether the warp has any
       const int r = r0 + 32 * wq + lane;
       const int rc = min(r, R - 1), tok = rc / g;
       const int lim = causal ? p.v.len - p.v.n + tok : p.v.len - 1;
       const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);      // the least of the warp's rows
       float m = -INFINITY, l = 0.0f;
-      const int t0 = p.t0, t1 = p.t1;
-      for (int j = t0; j < t1; ++j) {
+      for (int j = t0; j < t1; j += every) {
         wait(&bar.s_full[t], tiles & 1);
         __syncwarp();
         ++tiles;
+        if (!rows) {   // whatever the weights are, no row that is stored comes of them
+          if (lane == 0) {
+            mbar_arrive(&bar.p_lo[t]);
+            mbar_arrive(&bar.p_hi[t]);
+          }
+          continue;
+        }
         tc_fence_after();
         float s[64];
 #pragma unroll
@@ -589,13 +634,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = m == -INFINITY ? 0.0f : -m;
         weights<T>(s, scale2, sub, l, tP, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
+      // the products are in (so both warps are done with what they told each other)
+      const bool used[2] = {true, !alone || p.t1 - p.t0 > 1};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (used[k] && (k == t || alone)) {
+          wait(&bar.o_full[k], outputs[k] & 1);
+          __syncwarp();
+        }
+        if (used[k]) ++outputs[k];
+      }
+      tc_fence_after();
       *mine = l;
       pair_sync(1 + 4 * t + wq);
       l = side ? *other + l : l + *other;
-      wait(&bar.o_full[t], pieces & 1);
-      __syncwarp();
-      ++pieces;
-      tc_fence_after();
+      float f0 = 1.0f, f1 = 0.0f;                 // weights of the two halves' outputs
+      if (alone) {
+        // half 1 tells half 0 its maximum and sum and is done; half 0 reads both outputs
+        pair_sync(1 + 4 * t + wq);
+        if (t == 1) *mine = side ? l : m;
+        quad_sync(9 + wq);
+        if (t == 0) {
+          const float m1 = both_s[1][0][32 * wq + lane], l1 = both_s[1][1][32 * wq + lane], mn = fmaxf(m, m1);
+          if (mn != -INFINITY) {
+            f0 = ex2(m - mn);
+            f1 = ex2(m1 - mn);
+            l = l * f0 + l1 * f1;
+            m = mn;
+          }
+        }
+        quad_sync(9 + wq);
+        if (t == 1) continue;
+      }
+      const bool both = alone && used[1];
       const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g + (rc - tok * g);
       if (began && ends) {
         float inv = 1.0f, w = 0.0f;
@@ -609,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float il = l > 0.0f ? 1.0f / l : 0.0f;
-        inv *= il;
+        f0 *= inv * il;
+        f1 *= inv * il;
         w *= il;
         // Four lanes (four rows) exchange their 16-byte blocks, so that a store writes 64 bytes of a row
         const int64_t out_row = row * kD + 64 * side + 8 * (lane & 3);
@@ -619,12 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t y[4][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t o[16];
-            tmem_ld16(tO + 32 * c + 16 * h, o);
-            tmem_ld_wait();
             float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * inv;
+            output16(tO + 32 * c + 16 * h, f0, both, f1, v);
             if (w > 0.0f) {
               const float4* pre = reinterpret_cast<const float4*>(a.pre_out + row * kD + 64 * side + 32 * c + 16 * h);
 #pragma unroll
@@ -652,25 +720,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // parts: blocks of four features, rows next to one another
         const int64_t slot = (int64_t)blockIdx.x * 2 + (began ? 1 : 0);
-        const int row_in = t * kHalf + 32 * wq + lane;
+        const int row_in = r - p.m * kBlockRows;
         float4* dst = reinterpret_cast<float4*>(ws.o) + (slot * 32 + 16 * side) * kBlockRows + row_in;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t o[16];
-          tmem_ld16(tO + 16 * c, o);
-          tmem_ld_wait();
+          float v[16];
+          output16(tO + 16 * c, f0, both, f1, v);
           if (r < R) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              dst[(4 * c + i) * kBlockRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+              dst[(4 * c + i) * kBlockRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
         if (side == 0 && r < R) ws.ml[slot * kBlockRows + row_in] = make_float2(m, l);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.o_empty[t]);
+      if (lane == 0) {
+        mbar_arrive(&bar.o_empty[t]);
+        if (both) mbar_arrive(&bar.o_empty[1]);   // for half 1, which went on
+      }
     } while (next_of_pair(p, b, g, causal, 1 + 4 * t + wq, side == 0 && lane == 0));
   }
   tc_fence_before();

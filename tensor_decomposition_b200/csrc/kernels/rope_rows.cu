@@ -9,65 +9,55 @@
 // Each row is read and written once, which bounds the kernel for long inputs (HBM); short inputs
 // are bound by latency. A CTA takes a tile of tokens, about 80 rows, 16 lanes a row (16 bytes each) and
 // up to five rows a lane in flight at once: with one token a CTA the append of 16 rows a token ran at 1.4
-// TB/s. The tile's sines are computed once (a thread each, while the rows are on their way) and used by
-// all heads from shared memory; the append's page lookup is one parallel pass over the batch's offsets
-// instead of a search.
+// TB/s, so it runs at 3.8. The tile's sines are computed once (a thread each, while the rows are on their
+// way) and used by all heads from shared memory; the append's page lookup is one parallel pass over the
+// batch's offsets instead of a search. (Persistent CTAs with a ring of asynchronous copies, and tiles of
+// two to four times the rows, were 8 to 25 % slower: the issue slots are 70 % busy as it is.)
 #include <algorithm>
 
 #include "../paged.h"
+#include "f32x2.cuh"
 
 namespace jolt {
 namespace {
+
+using namespace f32x2;
 
 constexpr int kThreads = 256;
 constexpr int kSlots = kThreads / 16;   // rows at a time
 constexpr int kBatch = 5;               // rows a slot keeps in flight
 constexpr int kMaxTile = 16;            // tokens of a tile
 
+// Four elements of a row, as two pairs.
+__device__ __forceinline__ uint64_t wide(__nv_bfloat16, uint32_t v) {
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+  return pair_of(a.x, a.y);
+}
+__device__ __forceinline__ uint64_t wide(__half, uint32_t v) {
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return pair_of(a.x, a.y);
+}
+__device__ __forceinline__ uint32_t narrow(__nv_bfloat16, uint64_t p) {
+  float x, y;
+  unpair(p, x, y);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&a);
+}
+__device__ __forceinline__ uint32_t narrow(__half, uint64_t p) {
+  float x, y;
+  unpair(p, x, y);
+  const __half2 a = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&a);
+}
 template <typename T>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16> {
-  static __device__ __forceinline__ void get(const uint4& v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec<__half> {
-  static __device__ __forceinline__ void get(const uint4& v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
+__device__ __forceinline__ void get4(T, const uint2& v, uint64_t* x) {
+  x[0] = wide(T(), v.x);
+  x[1] = wide(T(), v.y);
+}
+template <typename T>
+__device__ __forceinline__ uint2 put4(T, const uint64_t* x) {
+  return make_uint2(narrow(T(), x[0]), narrow(T(), x[1]));
+}
 
 struct RowsArgs {
   RowsIn A, B;       // A: queries, or the append's keys; B: keys, or the append's values
@@ -77,30 +67,27 @@ struct RowsArgs {
   int32_t tokens, tile;
 };
 
-__device__ __forceinline__ void get8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-template <typename T, bool kPaged>
+// A lane holds two runs of four features of its row, o0 and o1, such that it has both members of
+// four rotated pairs (angles 4 l .. 4 l + 3) or eight features behind the rotated ones.
+template <typename T, bool kPaged, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
-  extern __shared__ __align__(16) float trig[];        // [tile][2][128]: a feature's cosine, its partner's signed sine
+  extern __shared__ __align__(16) float trig[];        // [tile][2][64] cosines and sines of the pairs
   __shared__ __align__(16) float w_s[2][kD];           // norm weights
   __shared__ int64_t dst_s[kMaxTile];                  // append: page row in elements from the pages' base; < 0: none
   __shared__ int pos_s[kMaxTile], seq_s[kMaxTile];     // append: place in the cache, sequence (-1: none)
   const int tid = threadIdx.x, slot = tid >> 4, l = tid & 15;
   const int t0 = blockIdx.x * a.tile, nt = min(a.tile, a.tokens - t0);
-  const int nA = a.A.heads, nR = a.A.heads + a.B.heads, rows = nt * nR;
+  const int nA = a.A.heads, nR = a.A.heads + a.B.heads;
   const int step_t = kSlots / nR, step_r = kSlots % nR;
   const bool rot = a.r.inv_freq != nullptr;
   const bool normA = a.A.w != nullptr, normB = !kPaged && a.B.w != nullptr;
-  const T* A = reinterpret_cast<const T*>(a.A.p) + 8 * l;
-  const T* B = reinterpret_cast<const T*>(a.B.p) + 8 * l;
+  const int h = a.r.rope_dim >> 1;
+  const bool turned = 8 * l < a.r.rope_dim;
+  const int o0 = kInterleaved || !turned ? 8 * l : 4 * l, o1 = kInterleaved || !turned ? 8 * l + 4 : 4 * l + h;
 
   // rows slot, slot + 16, ...: token i of the tile, row r of the token
   int i = slot / nR, r = slot - i * nR;
-  auto step = [&](int& ti, int& tr) {
+  auto advance = [&](int& ti, int& tr) {
     ti += step_t;
     tr += step_r;
     if (tr >= nR) {
@@ -108,15 +95,18 @@ __global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
       ++ti;
     }
   };
-  uint4 v[kBatch] = {};
+  uint2 v[kBatch][2] = {};
   auto load = [&](int ti, int tr) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (ti < nt) {
-        const int64_t t = t0 + ti;
-        v[k] = *reinterpret_cast<const uint4*>(tr < nA ? A + t * a.A.ts + tr * a.A.hs : B + t * a.B.ts + (tr - nA) * a.B.hs);
+        const int t = t0 + ti;
+        const T* src = tr < nA ? reinterpret_cast<const T*>(a.A.p) + (int64_t)t * a.A.ts + (int64_t)tr * a.A.hs
+                               : reinterpret_cast<const T*>(a.B.p) + (int64_t)t * a.B.ts + (int64_t)(tr - nA) * a.B.hs;
+        v[k][0] = *reinterpret_cast<const uint2*>(src + o0);
+        v[k][1] = *reinterpret_cast<const uint2*>(src + o1);
       }
-      step(ti, tr);
+      advance(ti, tr);
     }
   };
   load(i, r);
@@ -148,75 +138,79 @@ __global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
     }
   }
   if (rot) {
-    const int h = a.r.rope_dim >> 1;
-    for (int u = tid; u < nt * 64; u += kThreads) {
-      const int t = u >> 6, f = u & 63;
-      float c = 1.0f, s = 0.0f;
-      int x, y;                 // the pair's features
-      if (f < h) {
-        const int pos = kPaged && !a.r.positions ? (seq_s[t] >= 0 ? pos_s[t] : 0) : a.r.positions[t0 + t];
-        // parts of a turn, in float64 up to the last whole turn
-        double turn = (double)pos * ((double)a.r.inv_freq[f] * 0.15915494309189533577);
-        turn -= rint(turn);
-        sincospif(2.0f * (float)turn, &s, &c);
-        x = a.r.interleaved ? 2 * f : f;
-        y = a.r.interleaved ? 2 * f + 1 : f + h;
-      } else {                  // features that are not rotated
-        x = 2 * f;
-        y = 2 * f + 1;
-      }
-      float* row = trig + t * (2 * kD);
-      row[x] = row[y] = c;
-      row[kD + x] = -s;
-      row[kD + y] = s;
+    for (int u = tid; u < nt * h; u += kThreads) {
+      const int t = u / h, f = u - t * h;
+      const int pos = kPaged && !a.r.positions ? (seq_s[t] >= 0 ? pos_s[t] : 0) : a.r.positions[t0 + t];
+      // parts of a turn, in float64 up to the last whole turn
+      double turn = (double)pos * ((double)a.r.inv_freq[f] * 0.15915494309189533577);
+      turn -= rint(turn);
+      sincospif(2.0f * (float)turn, &trig[t * kD + 64 + f], &trig[t * kD + f]);
     }
   }
   __syncthreads();
 
-  // the 16 lanes of a row take part in its shuffles together
-  const uint32_t mask = 0xffffu << (tid & 16);
-  const int e0 = 8 * l, h8 = a.r.rope_dim >> 4;       // lanes of the first halves of half-split pairs
-  const bool inside = e0 < a.r.rope_dim;
-  const int partner = !inside ? l : l < h8 ? l + h8 : l - h8;
+  const uint32_t mask = 0xffffu << (tid & 16);   // the 16 lanes of a row, who take part in its sum
   for (;;) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (i >= nt) break;
       const bool isA = r < nA;
-      const int64_t t = t0 + i;
-      uint4 out = v[k];
+      uint2 y0 = v[k][0], y1 = v[k][1];
       if (!kPaged || isA) {     // values of the append go out as they are
-        float x[8];
-        Vec<T>::get(out, x);
+        uint64_t x[4];          // features o0, + 1; + 2, + 3; o1, + 1; + 2, + 3
+        get4(T(), y0, x);
+        get4(T(), y1, x + 2);
         if (isA ? normA : normB) {
-          float q = 0.0f, w[8];
+          uint64_t q2 = mul2(x[0], x[0]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
+          for (int e = 1; e < 4; ++e) q2 = fma2(x[e], x[e], q2);
+          float q, qb;
+          unpair(q2, q, qb);
+          q += qb;
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(mask, q, o, 16);
-          const float f = 1.0f / sqrtf(q * (1.0f / kD) + a.r.eps);
-          get8(&w_s[isA ? 0 : 1][e0], w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * f * w[e];
+          const float f = rsqrtf(fmaf(q, 1.0f / kD, a.r.eps));
+          const float* w = w_s[isA ? 0 : 1];
+          const float4 wa = *reinterpret_cast<const float4*>(w + o0), wb = *reinterpret_cast<const float4*>(w + o1);
+          const uint64_t f2 = pair_of(f, f);
+          x[0] = mul2(x[0], mul2(f2, pair_of(wa.x, wa.y)));
+          x[1] = mul2(x[1], mul2(f2, pair_of(wa.z, wa.w)));
+          x[2] = mul2(x[2], mul2(f2, pair_of(wb.x, wb.y)));
+          x[3] = mul2(x[3], mul2(f2, pair_of(wb.z, wb.w)));
         }
-        if (rot) {
-          float c[8], s[8], p[8];
-          get8(trig + i * (2 * kD) + e0, c);
-          get8(trig + i * (2 * kD) + kD + e0, s);
+        if (turned) {
+          const float4 c = *reinterpret_cast<const float4*>(trig + i * kD + 4 * l);
+          const float4 s = *reinterpret_cast<const float4*>(trig + i * kD + 64 + 4 * l);
+          if (kInterleaved) {     // (u, v) -> (u, v) c + (-v, u) s
+            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = a.r.interleaved ? x[e ^ 1] : __shfl_sync(mask, x[e], partner, 16);
-          if (inside) {
+            for (int e = 0; e < 4; ++e) {
+              float u, w;
+              unpair(x[e], u, w);
+              x[e] = fma2(pair_of(w, u), pair_of(-sn[e], sn[e]), mul2(x[e], pair_of(cs[e], cs[e])));
+            }
+          } else {
+            const uint64_t c2[2] = {pair_of(c.x, c.y), pair_of(c.z, c.w)}, s2[2] = {pair_of(s.x, s.y), pair_of(s.z, s.w)};
+            const uint64_t n2[2] = {pair_of(-s.x, -s.y), pair_of(-s.z, -s.w)};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf(p[e], s[e], x[e] * c[e]);
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t u = x[e];
+              x[e] = fma2(x[2 + e], n2[e], mul2(u, c2[e]));
+              x[2 + e] = fma2(u, s2[e], mul2(x[2 + e], c2[e]));
+            }
           }
         }
-        out = Vec<T>::put(x);
+        y0 = put4(T(), x);
+        y1 = put4(T(), x + 2);
       }
       if (!kPaged || dst_s[i] >= 0) {
-        T* dst = reinterpret_cast<T*>(isA ? a.Ao.p : a.Bo.p) + (kPaged ? dst_s[i] : t * (isA ? a.Ao.ts : a.Bo.ts)) + e0;
-        *reinterpret_cast<uint4*>(dst + (isA ? r * a.Ao.hs : (r - nA) * a.Bo.hs)) = out;
+        T* dst = reinterpret_cast<T*>(isA ? a.Ao.p : a.Bo.p) +
+                 (kPaged ? dst_s[i] : (int64_t)(t0 + i) * (isA ? a.Ao.ts : a.Bo.ts)) +
+                 (int64_t)(isA ? r : r - nA) * (isA ? a.Ao.hs : a.Bo.hs);
+        *reinterpret_cast<uint2*>(dst + o0) = y0;
+        *reinterpret_cast<uint2*>(dst + o1) = y1;
       }
-      step(i, r);
+      advance(i, r);
     }
     if (i >= nt) return;
     load(i, r);
@@ -226,14 +220,16 @@ __global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
 template <bool kPaged>
 cudaError_t launch(jolt_dtype t, int tokens, RowsArgs a, int sms, cudaStream_t s) {
   if (tokens <= 0) return cudaSuccess;
-  const int nR = a.A.heads + a.B.heads;
-  // five rows a slot, but smaller tiles as long as the GPU is not full
-  const int full = std::max(1, std::min(kMaxTile, kSlots * kBatch / nR));
+  const int64_t nR64 = (int64_t)a.A.heads + a.B.heads;
+  if (nR64 * tokens > INT32_MAX) return cudaErrorInvalidValue;   // refused by the caller
+  const int nR = (int)nR64;
+  // as many tokens as a tile's rows hold, fewer where that would leave the GPU without work
   a.tokens = tokens;
-  a.tile = std::max(1, std::min<int>(full, tokens / (2 * sms)));
-  const int grid = (tokens + a.tile - 1) / a.tile, bytes = a.tile * 2 * kD * (int)sizeof(float);
-  if (t == JOLT_BF16) k_rope_rows<__nv_bfloat16, kPaged><<<grid, kThreads, bytes, s>>>(a);
-  else k_rope_rows<__half, kPaged><<<grid, kThreads, bytes, s>>>(a);
+  a.tile = std::max(1, std::min({kMaxTile, kSlots * kBatch / nR, tokens / (2 * sms)}));
+  const int grid = (tokens + a.tile - 1) / a.tile, bytes = a.tile * kD * (int)sizeof(float);
+  auto kernel = t == JOLT_BF16 ? (a.r.interleaved ? k_rope_rows<__nv_bfloat16, kPaged, true> : k_rope_rows<__nv_bfloat16, kPaged, false>)
+                               : (a.r.interleaved ? k_rope_rows<__half, kPaged, true> : k_rope_rows<__half, kPaged, false>);
+  kernel<<<grid, kThreads, bytes, s>>>(a);
   note_launch();
   return cudaGetLastError();
 }

@@ -5,6 +5,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "jolt_internal.h"
 
 namespace jolt {
@@ -54,16 +56,29 @@ __device__ __forceinline__ int page_of(const BatchView& b, int s, int pos) {
   return p;
 }
 
+// Allow a kernel its dynamic shared memory, once a device (`done`: the kernel's own flags).
+struct SmemFlags {
+  std::atomic<bool> on[64] = {};
+};
+template <class K>
+inline cudaError_t allow_smem(K* kernel, int bytes, int device, SmemFlags& done) {
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (done.on[device].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.on[device].store(true, std::memory_order_release);
+  return e;
+}
+
 // Rows of 128 elements of a tensor [tokens][heads][128]; element strides.
 struct RowsIn {
   const void* p = nullptr;
-  int64_t ts = 0, hs = 0;
+  int32_t ts = 0, hs = 0;
   int32_t heads = 0;
   const void* w = nullptr;     // norm weight [128], or null
 };
 struct RowsOut {
   void* p = nullptr;
-  int64_t ts = 0, hs = 0;
+  int32_t ts = 0, hs = 0;
 };
 struct RopeArgs {
   const int32_t* positions = nullptr;   // [tokens], or null (paged: the token's index in its cache)

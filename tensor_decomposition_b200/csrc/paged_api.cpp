@@ -86,6 +86,8 @@ jolt_status check_rows(const char* what, const char* name, const void* p, int64_
   if (!aligned16(p) || ts % 8 || hs % 8)
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: %s rows must start on 16-byte boundaries (strides a multiple of 8)", what,
                      name);
+  if (ts > INT32_MAX || ts < -INT32_MAX || hs > INT32_MAX || hs < -INT32_MAX)
+    return host_fail(JOLT_ERR_UNSUPPORTED, "%s: strides of %s beyond 2^31 elements", what, name);
   return JOLT_OK;
 }
 
@@ -238,15 +240,17 @@ JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const v
   if (st == JOLT_OK && k_heads > 0) st = check_rows(what, "K_out", K_out, ko_token_stride, ko_head_stride, k_heads);
   if (st == JOLT_OK) st = check_rope(what, positions, true, inv_freq, rope_dim);
   if (st != JOLT_OK) return st;
+  if (((int64_t)q_heads + k_heads) * tokens > INT32_MAX)
+    return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 rows", what);
   if (!aligned16(q_weight) || !aligned16(k_weight))
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: weights must be 16-byte aligned", what);
   RowsIn q, k;
   RowsOut qo, ko;
-  q.p = Q; q.ts = q_token_stride; q.hs = q_head_stride; q.heads = q_heads; q.w = q_weight;
-  qo.p = Q_out; qo.ts = qo_token_stride; qo.hs = qo_head_stride;
+  q.p = Q; q.ts = (int32_t)q_token_stride; q.hs = (int32_t)q_head_stride; q.heads = q_heads; q.w = q_weight;
+  qo.p = Q_out; qo.ts = (int32_t)qo_token_stride; qo.hs = (int32_t)qo_head_stride;
   if (k_heads > 0) {
-    k.p = K; k.ts = k_token_stride; k.hs = k_head_stride; k.heads = k_heads; k.w = k_weight;
-    ko.p = K_out; ko.ts = ko_token_stride; ko.hs = ko_head_stride;
+    k.p = K; k.ts = (int32_t)k_token_stride; k.hs = (int32_t)k_head_stride; k.heads = k_heads; k.w = k_weight;
+    ko.p = K_out; ko.ts = (int32_t)ko_token_stride; ko.hs = (int32_t)ko_head_stride;
   }
   cudaStream_t s = (cudaStream_t)cuda_stream;
   int dev = 0, sms = 0;
@@ -273,12 +277,13 @@ JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* bat
   if (st == JOLT_OK) st = check_rows(what, "V", V, v_token_stride, v_head_stride, H);
   if (st == JOLT_OK) st = check_rope(what, positions, false, inv_freq, rope_dim);
   if (st != JOLT_OK) return st;
+  if (2 * (int64_t)H * batch->total_q > INT32_MAX) return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 rows", what);
   if (!aligned16(k_weight)) return host_fail(JOLT_ERR_INVALID_ARG, "%s: the weight must be 16-byte aligned", what);
   st = check_device(what, pages);
   if (st != JOLT_OK) return st;
   RowsIn k, v;
-  k.p = K; k.ts = k_token_stride; k.hs = k_head_stride; k.heads = H; k.w = k_weight;
-  v.p = V; v.ts = v_token_stride; v.hs = v_head_stride; v.heads = H;
+  k.p = K; k.ts = (int32_t)k_token_stride; k.hs = (int32_t)k_head_stride; k.heads = H; k.w = k_weight;
+  v.p = V; v.ts = (int32_t)v_token_stride; v.hs = (int32_t)v_head_stride; v.heads = H;
   cudaStream_t s = (cudaStream_t)cuda_stream;
   int sms = 0;
   cudaError_t e = sm_count(pages->device, &sms);

@@ -36,6 +36,8 @@ def _t(name):
     (17, 7, 3, True, 16, True, 5),
     (9, 64, 8, True, 0, False, 0),
     (33, 12, 4, False, 96, False, 1 << 20),
+    (700, 96, 8, True, 128, False, 9),          # more rows a token than a CTA takes at once
+    (5000, 3, 2, True, 32, True, 1000),         # many tokens a CTA
 ])
 def test_norm_rope(J, dtype, tokens, hq, hk, norm, rope, inter, start):
     import torch
@@ -78,6 +80,8 @@ def test_norm_rope_of_nothing(J):
     ([100, 5, 0, 64], [3, 5, 0, 64], 3, 48, True, 64, True, True, 0),
     ([2, 300], [5, 299], 2, 256, True, 128, False, False, 7),        # three tokens before the cache's begin: dropped
     ([33] * 300, [1] * 300, 2, 16, False, 0, False, False, 0),       # more sequences than a CTA has threads
+    ([3000, 77, 2100], [2999, 5, 2050], 1, 32, True, 128, False, False, 9),   # many tokens a CTA, sequences meeting in one
+    ([50, 9], [50, 2], 48, 16, True, 128, True, False, 0),           # more rows a token than a CTA takes at once
 ])
 def test_append(J, dtype, kv, chunks, heads, page, norm, rope, inter, own_pos, pad):
     import torch
@@ -435,3 +439,10 @@ def test_binding_refuses(J):
         J.jolt_batch(c.q_start.long(), c.kv_len, c.table, 1, 1)
     with pytest.raises(ValueError):
         J.jolt_batch(c.q_start, c.kv_len[:0], c.table, 1, 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [17, 32, 127, 128, 129, 257, 300, 384])
+def test_row_blocks_of_every_fill(J, dtype, n):
+    """Chunks whose last block of rows holds one to 256 of them, over one key tile, two, three and many."""
+    _attend(J, Cache([n, n + 100, n + 256, n + 5000], [n] * 4, 1, 16, _t(dtype), seed=n), 1)

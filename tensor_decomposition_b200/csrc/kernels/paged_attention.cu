@@ -13,7 +13,7 @@ namespace {
 
 using namespace pattn;
 
-// The items that lie in several CTAs' shares, the parts weighted by their maxima. Parts of up to 16
+// The items that lie in several CTAs' shares, the parts weighted by their maxima. Parts of up to 32
 // rows lie row by row: four rows a CTA, four warps a row (one warp a row took 0.25 us a part).
 constexpr int kSubs = 4;
 template <typename T>
@@ -25,8 +25,7 @@ __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, con
   if (sp.s < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & 3, rw = warp >> 2;
   const int c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
-  const SeqView v = seq_view(a.b, sp.s);
-  const int g = a.Hq / a.b.heads, R = v.n * g;
+  const int g = a.Hq / a.b.heads, R = sp.rows;
   const int r = blockIdx.y * 4 + rw;
   if ((int)blockIdx.y * 4 >= R) return;
   float mx = -INFINITY, ls = 0.0f;
@@ -86,7 +85,7 @@ __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, con
       y.w = fmaf(x.w, f, y.w);
     }
   }
-  finish_row<T>(a, (int64_t)(v.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y, mn, ls);
+  finish_row<T>(a, (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y, mn, ls);
 }
 
 // The same for blocks of 256 rows, whose parts lie in blocks of four features with the rows next to one
@@ -99,29 +98,31 @@ __global__ void __launch_bounds__(128) k_attn_combine_blocks(const PagedAttnArgs
   const Split sp = ws.list[blockIdx.x];
   if (sp.s < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
-  const SeqView v = seq_view(a.b, sp.s);
-  const int g = a.Hq / a.b.heads, rb = blockIdx.y * 32, R = min(256, v.n * g - sp.m * 256);
+  const int g = a.Hq / a.b.heads, rb = blockIdx.y * 32, R = sp.rows;
   if (rb >= R) return;
   const bool in = rb + lane < R;
   const float4* o = reinterpret_cast<const float4*>(ws.o);
   float mx = -INFINITY, ls = 0.0f;
-  for (int c = 0; c < parts && in; ++c)
-    mx = fmaxf(mx, ws.ml[((int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0)) * 256 + rb + lane].x);
   float4 y[8] = {};
-  if (in && mx != -INFINITY) {
-    for (int c = 0; c < parts; ++c) {
-      const int64_t slot = (int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0);
-      const float2 p = ws.ml[slot * 256 + rb + lane];
-      const float f = ex2(p.x - mx);
-      ls = fmaf(p.y, f, ls);
+#pragma unroll 2
+  for (int c = 0; c < parts; ++c) {
+    if (!in) break;
+    const int64_t slot = (int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0);
+    const float2 p = ws.ml[slot * 256 + rb + lane];
+    float4 x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 x = o[(slot * 32 + warp + 4 * k) * 256 + rb + lane];
-        y[k].x = fmaf(x.x, f, y[k].x);
-        y[k].y = fmaf(x.y, f, y[k].y);
-        y[k].z = fmaf(x.z, f, y[k].z);
-        y[k].w = fmaf(x.w, f, y[k].w);
-      }
+    for (int k = 0; k < 8; ++k) x[k] = o[(slot * 32 + warp + 4 * k) * 256 + rb + lane];
+    const float mn = fmaxf(mx, p.x);
+    if (mn == -INFINITY) continue;
+    const float f0 = ex2(mx - mn), f = ex2(p.x - mn);
+    mx = mn;
+    ls = fmaf(ls, f0, p.y * f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k].x = fmaf(y[k].x, f0, x[k].x * f);
+      y[k].y = fmaf(y[k].y, f0, x[k].y * f);
+      y[k].z = fmaf(y[k].z, f0, x[k].z * f);
+      y[k].w = fmaf(y[k].w, f0, x[k].w * f);
     }
   }
 #pragma unroll
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(128) k_attn_combine_blocks(const PagedAttnArgs
   __syncthreads();
   for (int i = warp; i < min(32, R - rb); i += 4) {
     const int r = sp.m * 256 + rb + i;
-    finish_row<T>(a, (int64_t)(v.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y_s[i][lane],
+    finish_row<T>(a, (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y_s[i][lane],
                   __shfl_sync(0xffffffffu, mx, i), __shfl_sync(0xffffffffu, ls, i));
   }
 }
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(128) k_attn_combine_blocks(const PagedAttnArgs
 template <typename T>
 cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, p.decode ? 4 : 8);
+  cfg.gridDim = dim3(p.grid, p.decode ? (p.most + 3) / 4 : (p.most + 31) / 32);
   cfg.blockDim = dim3(p.decode ? 512 : 128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];   // placed while the parts are still computed; waits for them itself
@@ -157,7 +158,7 @@ size_t ml_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * 
 
 }  // namespace
 
-// Up to 16 rows of a chunk reading one KV head run in the kernel for few rows, whose MMAs hold 16. Where
+// Up to 32 rows of a chunk reading one KV head run in the kernel for few rows. Where
 // clusters of 8 CTAs, one for each item, all run at once (33 and more do not: 9.0 us instead of 5.9) and
 // their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0 instead of 7.7 us
 // at 1024 keys, 11.9 and 10.9 at 4096, 19.3 and 13.5 at 8192; 32 items: 26 instead of 32 at 8192).
@@ -165,8 +166,9 @@ constexpr int kTeamTokens = 4096, kTeamItems = 32;
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   AttnPlan p;
   const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)a.b.max_q * (a.Hq / a.b.heads);
-  p.decode = rows <= 16;
-  p.rows = p.decode ? 16 : 256;
+  p.decode = rows <= 32;
+  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 256;
+  p.most = (int)std::max<int64_t>(1, std::min<int64_t>(rows, p.rows));
   const int64_t items = (int64_t)a.b.heads * a.b.num_seqs;
   if (p.decode && items <= kTeamItems && (tokens <= kTeamTokens || items >= kTeamItems - 4)) {
     p.team = 1;
@@ -176,7 +178,7 @@ AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   const int unit = p.decode ? 64 : 128;
   const int64_t units = std::max<int64_t>(1, (tokens + unit - 1) / unit) * std::max<int64_t>(1, (rows + p.rows - 1) / p.rows) *
                         a.b.heads * a.b.num_seqs;
-  p.grid = (int)std::min<int64_t>((p.decode ? 2 : 1) * (int64_t)sms, units);
+  p.grid = (int)std::min<int64_t>((p.rows == 16 ? 3 : p.rows == 32 ? 2 : 1) * (int64_t)sms, units);
   p.bytes = o_bytes(p) + ml_bytes(p) + up256(p.grid * sizeof(Split));
   return p;
 }

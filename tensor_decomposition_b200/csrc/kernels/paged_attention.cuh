@@ -5,9 +5,12 @@
 #include <algorithm>
 
 #include "../paged.h"
+#include "sm100.cuh"
 
 namespace jolt {
 namespace pattn {
+
+using namespace sm100;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -29,6 +32,7 @@ struct Split {
   int32_t s, h, m;     // sequence, KV head, block of rows; s < 0: none
   int32_t c_last;      // CTA that holds its last unit (the first one is the list's index)
   int32_t slot;        // slot of its first part
+  int32_t q0, rows;    // first token of the sequence's chunk; rows of the item
 };
 struct Workspace {
   float* o;            // [G][2][rows][128]
@@ -135,6 +139,43 @@ __device__ __forceinline__ void finish_row(const PagedAttnArgs& a, int64_t row, 
   *reinterpret_cast<uint2*>(reinterpret_cast<T*>(a.out) + row * kD + 4 * lane) = *reinterpret_cast<const uint2*>(y);
   if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
+
+// Tensor maps of the pages.
+struct Maps {
+  CUtensorMap K, V;
+};
+
+// A bounded wait that also ends when another role of the CTA has given up. The clock is looked at
+// only every 64 polls.
+struct Waits {
+  volatile int* gave_up;
+  int32_t* status;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+      uint32_t done;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done)
+          : "r"(a), "r"(parity)
+          : "memory");
+      if (done) return true;
+      if (*gave_up) return false;
+      if ((it & 63) == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+          *gave_up = 1;
+          atomicOr(status, PST_TIMEOUT);
+          return false;
+        }
+      }
+    }
+  }
+};
 
 // Wait for the kernels before this one in the stream (a launch that was let start early).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -38,10 +38,6 @@ constexpr int kSmem = (2 + kStages) * kTileBytes;
 constexpr int kItem = 2;                     // what an item costs besides its tiles, in tiles
 constexpr float kFollow = 8.0f;
 
-struct Maps {
-  CUtensorMap K, V;
-};
-
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full[2], q_empty[2], s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
@@ -235,38 +231,6 @@ __device__ __forceinline__ void output16(uint32_t t0, float f0, bool both, float
     for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
   }
 }
-
-// A bounded wait that also ends when another role of the CTA has given up. The clock is looked at
-// only every 64 polls.
-struct Waits {
-  volatile int* gave_up;
-  int32_t* status;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    const uint32_t a = smem_u32(bar);
-    uint64_t t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-      uint32_t done;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(a), "r"(parity)
-          : "memory");
-      if (done) return true;
-      if (*gave_up) return false;
-      if ((it & 63) == 0) {
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs) {
-          *gave_up = 1;
-          atomicOr(status, PST_TIMEOUT);
-          return false;
-        }
-      }
-    }
-  }
-};
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -569,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool alone = solo(p, g), began = p.t0 == 0, ends = p.t1 == p.T;
       const int R = p.v.n * g, r0 = p.m * kBlockRows + (alone ? 0 : t * kHalf);
       if (tid == 0 && began && !ends)   // the share's last piece
-        ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[1] + (p.T - p.t1) - 1, range_s[0], range_s[2]), 1};
+        ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[1] + (p.T - p.t1) - 1, range_s[0], range_s[2]), 1,
+                                    p.v.q0, min(kBlockRows, R - p.m * kBlockRows)};
       const int t1 = p.t1, every = alone ? 2 : 1, t0 = p.t0 + (alone ? t : 0);   // this half's tiles
       const bool rows = r0 + 32 * wq < R;         // whether the warp has any
       const int r = r0 + 32 * wq + lane;
@@ -753,8 +718,8 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
   int box = kHalf;
   while (a.b.page_size % box) box /= 2;      // 16 at least
   Maps maps;
-  maps.K = *static_cast<const CUtensorMap*>(a.kmap);
-  maps.V = *static_cast<const CUtensorMap*>(a.vmap);
+  maps.K = a.maps[0];
+  maps.V = a.maps[1];
   static SmemFlags allowed;
   cudaError_t e = allow_smem(k_attn_chunk<T>, kSmem, a.device, allowed);
   if (e != cudaSuccess) return e;

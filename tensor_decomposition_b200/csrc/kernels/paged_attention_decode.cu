@@ -1,15 +1,18 @@
-// Paged attention of few query rows: at most 16 rows of a sequence's chunk read one KV head (single
-// tokens with up to 16 query heads a KV head, a few drafted tokens).
+// Paged attention of few query rows: at most 32 rows of a sequence's chunk read one KV head (single
+// tokens, a few drafted ones).
 //
 // Keys and values are read once and nothing else is large, so HBM bounds it; what costs is keeping
 // enough bytes in flight. A CTA walks its share of the units (64 keys of one item), each of its four
-// warps 16 of the keys, by itself: its own ring of asynchronous 16-byte copies (swizzled so that the
-// matrix loads meet no bank conflicts; rows behind the sequence are filled with zeros), its own
-// running maximum, sum and output (16 rows x 128 in registers). 16 keys never straddle a page. The
+// warps 16 of the keys, by itself: its own ring of TMA boxes (16 rows x 64 features, swizzled so that
+// the matrix loads meet no bank conflicts; 16 keys never straddle a page), its own running maximum, sum
+// and output (16 rows x 128 in registers). Copies by the threads, 16 bytes each, took 680 of a unit's
+// 2000 cycles. The
 // products are m16n8k16 MMAs with the query rows padded to 16: with so few rows the tensor pipe idles
 // either way, and warps that run apart need no barrier. The weights enter the second product as
 // a rounded part and a rounded remainder (two MMAs), so that only the output's rounding is left.
-// Warps meet where an item ends or the share does.
+// Warps meet where an item ends or the share does. For 17 to 32 rows a warp has two blocks of 16, whose
+// queries it reads from shared memory each time (their fragments would not fit the registers beside two
+// outputs). A warp for each block on a common ring, with a barrier a unit, ran at half the speed.
 #include <cooperative_groups.h>
 
 #include "paged_attention.cuh"
@@ -19,28 +22,26 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kKeys = 16;                 // keys of a warp in a unit
-constexpr int kUnit = kKeys * kWarps;
-constexpr int kTile = kKeys * kD * 2;     // bytes of a warp's keys (or values)
-constexpr int kStages = 3;
-constexpr int kCtas = 2;                  // per SM
-constexpr int kRows = 16;
+constexpr int kSlices = 4;                // slices of a unit's keys
+constexpr int kKeys = 16;                 // keys of a slice
+constexpr int kUnit = kKeys * kSlices;
+constexpr int kTile = kKeys * kD * 2;     // bytes of a slice's keys (or values)
 constexpr int kMinUnits = 1;
-constexpr int kSmem = kWarps * kStages * 2 * kTile;
 constexpr int kTeamCtas = 8;
-constexpr int kTeamSmem = kSmem + kRows * kD * 4;
+constexpr int kThreads = 32 * kSlices;
+// kT: blocks of 16 query rows. CTAs per SM and stages of a ring: what registers and shared memory allow.
+template <int kT>
+constexpr int kCtas = kT == 1 ? 3 : 2;
+template <int kT>
+constexpr int kStages = kT == 1 ? 2 : 3;
+// Shared memory: the rings, the queries (kT = 2), a team's part.
+template <int kT>
+constexpr int kRing = kSlices * kStages<kT> * 2 * kTile;
+template <int kT>
+constexpr int kSmem = kRing<kT> + (kT > 1 ? 16 * kT * kD * 2 : 0);
+template <int kT>
+constexpr int kTeamSmem = kSmem<kT> + 16 * kT * kD * 4;
 
-__device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -104,16 +105,28 @@ __device__ __forceinline__ void advance(Cursor& c, const BatchView& b) {
 
 // kTeam: instead of a share of the line a CTA takes an eighth of the item of its cluster, and the cluster's
 // CTAs combine through one another's shared memory: one launch and no scratch.
-template <typename T, bool kTeam>
-__global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttnArgs a, const Workspace ws) {
-  extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ float2 ml_s[kWarps][kRows];
+template <typename T, int kT, bool kTeam>
+__global__ void __launch_bounds__(kThreads, kCtas<kT>)
+    k_attn_decode(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws) {
+  constexpr int kRows = 16 * kT, kDeep = kStages<kT>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ __align__(8) uint64_t full_s[kSlices][kStages<kT>];
+  __shared__ int valid_s[kSlices][kStages<kT>];      // rows of a stage that hold keys
+  __shared__ int gave_up;
+  __shared__ float2 ml_s[kSlices][kRows];
   __shared__ float2 team_ml[kTeam ? kRows : 1];
-  __shared__ int64_t scan_s[kWarps + 3];
+  __shared__ int64_t scan_s[kSlices + 3];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, pair = lane & 3;
   const BatchView& b = a.b;
   const int g = a.Hq / b.heads;
   const float scale2 = a.scale * kLog2e;
+  if (tid < kSlices * kDeep) mbar_init(&full_s[0][0] + tid, 1);
+  if (tid == 0) {
+    gave_up = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&maps.K);
+    prefetch_tensormap(&maps.V);
+  }
   Start st{};
   Cursor lc;
   if (kTeam) {
@@ -143,198 +156,244 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttn
   Cursor cc = lc;
   const int count = (int)(st.hi - st.lo);
 
-  // ---- loads: one commit group a unit, empty ones behind the last
-  uint8_t* ring = sm + warp * (kStages * 2 * kTile);
-  const int c16 = lane & 15, r2 = lane >> 4;
+  // ---- loads: a phase of the stage's barrier a unit, empty where the unit has no page
+  __syncthreads();
+  uint8_t* ring = sm + warp * (kDeep * 2 * kTile);
+  const Waits wait{&gave_up, b.status};
   int pg_s = -1, pg_u0 = 0, pg = -1;     // this lane's page: that of unit pg_u0 + lane of sequence pg_s
   int issued = 0;
   auto issue = [&](int stage) {
-    if (issued < count) {
-      if (lc.s != pg_s || lc.u < pg_u0 || lc.u >= pg_u0 + 32) {
-        pg_s = lc.s;
-        pg_u0 = lc.u;
-        const int64_t key = (int64_t)(lc.u + lane) * kUnit + warp * kKeys;
-        pg = key < lc.v.len ? page_of(b, lc.s, (int)key) : -1;
-      }
-      const int key0 = lc.u * kUnit + warp * kKeys;
-      const int page = __shfl_sync(0xffffffffu, pg, lc.u - pg_u0);
-      const int valid = page < 0 ? 0 : lc.v.len - key0;   // rows that hold keys (may exceed 16)
-      const int64_t off = (((int64_t)max(page, 0) * b.heads + lc.h) * b.page_size + (page < 0 ? 0 : key0 % b.page_size)) * kD;
-      const T* K = reinterpret_cast<const T*>(a.K) + off + r2 * kD + 8 * c16;
-      const T* V = reinterpret_cast<const T*>(a.V) + off + r2 * kD + 8 * c16;
-      const uint32_t dst = smem_of(ring + stage * 2 * kTile);
-#pragma unroll
-      for (int i = 0; i < kKeys / 2; ++i) {
-        const int r = 2 * i + r2;
-        const uint32_t d = dst + r * (2 * kD) + ((c16 ^ (r & 7)) << 4);
-        const uint32_t bytes = r < valid ? 16u : 0u;
-        copy16(d, K + 2 * i * kD, bytes);
-        copy16(d + kTile, V + 2 * i * kD, bytes);
-      }
-      ++issued;
-      if (issued < count) advance(lc, b);
+    if (issued == count) return;
+    if (lc.s != pg_s || lc.u < pg_u0 || lc.u >= pg_u0 + 32) {
+      pg_s = lc.s;
+      pg_u0 = lc.u;
+      const int64_t key = (int64_t)(lc.u + lane) * kUnit + warp * kKeys;
+      pg = key < lc.v.len ? page_of(b, lc.s, (int)key) : -1;
     }
-    copy_commit();
+    const int page = __shfl_sync(0xffffffffu, pg, lc.u - pg_u0);
+    if (lane == 0) {
+      const int key0 = lc.u * kUnit + warp * kKeys;
+      uint64_t* bar = &full_s[warp][stage];
+      valid_s[warp][stage] = page < 0 ? 0 : min(kKeys, lc.v.len - key0);
+      if (page >= 0) {
+        const int row = key0 % b.page_size;
+        uint8_t* dst = ring + stage * 2 * kTile;
+        mbar_arrive_expect_tx(bar, 2 * kTile);
+        tma_load_4d(dst, &maps.K, bar, 0, row, lc.h, page);
+        tma_load_4d(dst + kTile / 2, &maps.K, bar, 64, row, lc.h, page);
+        tma_load_4d(dst + kTile, &maps.V, bar, 0, row, lc.h, page);
+        tma_load_4d(dst + kTile * 3 / 2, &maps.V, bar, 64, row, lc.h, page);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    ++issued;
+    if (issued < count) advance(lc, b);
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kDeep - 1; ++i) issue(i);
 
-  uint32_t q[8][4];
-  float o[16][4], m[2], l[2];
-  int lim[2];
+  uint32_t q[8][4];          // queries, A fragments: of the item (kT = 1) or of the block at work
+  float o[kT][16][4], m[kT][2], l[kT][2];
+  int lim[kT][2];
   bool fresh = true;         // the next unit begins an item (or this CTA's part of one)
   bool began = cc.u == 0;    // the current item began in this CTA's range
   Split split;
   split.s = -1;
 
   for (int i = 0; i < count; ++i) {
-    const int stage = i % kStages;
-    copy_wait<kStages - 2>();
+    const int stage = i % kDeep;
+    wait(&full_s[warp][stage], (i / kDeep) & 1);   // void results are reported where it gives up
     __syncwarp();
-    issue((i + kStages - 1) % kStages);
+    issue((i + kDeep - 1) % kDeep);
     if (fresh) {
       fresh = false;
       const int R = cc.v.n * g;
-      const T* Q = reinterpret_cast<const T*>(a.Q);
+      const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)cc.v.q0 * a.q_ts + (int64_t)cc.h * g * a.q_hs;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = quad + 8 * k;
-        const int tok = r / g;
-        lim[k] = r < R ? (a.causal ? cc.v.len - cc.v.n + tok : cc.v.len - 1) : -1;
-        const T* p = Q + (int64_t)(cc.v.q0 + tok) * a.q_ts + (int64_t)(cc.h * g + r % g) * a.q_hs + 2 * pair;
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          q[j][k] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j) : 0u;
-          q[j][k + 2] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j + 8) : 0u;
+        for (int k = 0; k < 2; ++k) {
+          const int r = 16 * t + quad + 8 * k;
+          const int tok = r / g;
+          lim[t][k] = r < R ? (a.causal ? cc.v.len - cc.v.n + tok : cc.v.len - 1) : -1;
+          if (kT == 1) {
+            const T* p = Q + (int64_t)tok * a.q_ts + (int64_t)(r % g) * a.q_hs + 2 * pair;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              q[j][k] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j) : 0u;
+              q[j][k + 2] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j + 8) : 0u;
+            }
+          }
+          m[t][k] = -INFINITY;
+          l[t][k] = 0.0f;
         }
-        m[k] = -INFINITY;
-        l[k] = 0.0f;
+      if (kT > 1) {   // no warp reads the queries before: the last item's end was a barrier
+        for (int u = tid; u < kRows * 16; u += kThreads) {
+          const int r = u >> 4, c = u & 15, tok = r / g;
+          const uint4 x = r < R ? *reinterpret_cast<const uint4*>(Q + (int64_t)tok * a.q_ts + (int64_t)(r - tok * g) * a.q_hs + 8 * c)
+                                : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sm + kRing<kT> + r * (2 * kD) + ((c ^ (r & 7)) << 4)) = x;
+        }
+        __syncthreads();
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][j][e] = 0.0f;
     }
-    const uint32_t Ks = smem_of(ring + stage * 2 * kTile), Vs = Ks + kTile;
+    const uint32_t Ks = smem_u32(ring + stage * 2 * kTile), Vs = Ks + kTile;
     const int key0 = cc.u * kUnit + warp * kKeys;
     if (key0 < cc.v.len) {
+      const int valid = valid_s[warp][stage];
+      if (valid < kKeys) {
+        // rows without keys are zeroed: values, since a weight of zero does not hide what lies in the page
+        // (scores are masked), and all of a bad page
+        for (int u = lane; u < 4 * 8 * (kKeys - valid); u += 32) {
+          const int part = u & 3, c = (u >> 2) & 7, r = valid + (u >> 5);
+          *reinterpret_cast<uint4*>(ring + stage * 2 * kTile + part * (kTile / 2) + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();   // before the stage's next copy
+        __syncwarp();
+      }
       // scores of 16 rows x 16 keys: matrices (keys 0-7, 8-15) x (features 0-7, 8-15) of each k-step
-      float s[2][4] = {};
-      const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = (lane >> 3) & 1;
+      float s[kT][2][4] = {};
+      const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = (lane >> 3) & 1, vrow = lane & 15, vcol = lane >> 4;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t k4[4];
-        ldsm4(Ks + mrow * (2 * kD) + (((2 * j + mcol) ^ (mrow & 7)) << 4), k4);
-        mma(T(), s[0], q[j], k4[0], k4[1]);
-        mma(T(), s[1], q[j], k4[2], k4[3]);
+        ldsm4(Ks + (j >> 2) * (kTile / 2) + mrow * 128 + (((2 * (j & 3) + mcol) ^ (mrow & 7)) << 4), k4);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          if (kT > 1) ldsm4(smem_u32(sm + kRing<kT>) + (16 * t + vrow) * (2 * kD) + (((2 * j + vcol) ^ (vrow & 7)) << 4), q[j]);
+          mma(T(), s[t][0], q[j], k4[0], k4[1]);
+          mma(T(), s[t][1], q[j], k4[2], k4[3]);
+        }
       }
       // running softmax in units of log 2; lane: rows quad and quad + 8, keys 2 pair, + 1 of each block of 8
       const bool edge = key0 + kKeys - 1 > (a.causal ? cc.v.len - cc.v.n : cc.v.len - 1) || cc.v.n * g < kRows;
-      float mn[2] = {m[0], m[1]};
+      uint32_t hi[kT][4], lo[kT][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int t = 0; t < kT; ++t) {
+        float mn[2] = {m[t][0], m[t][1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[n][e] * scale2;
-          if (edge && key0 + 8 * n + 2 * pair + (e & 1) > lim[e >> 1]) x = -INFINITY;
-          s[n][e] = x;
-          mn[e >> 1] = fmaxf(mn[e >> 1], x);
-        }
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 1));
-        mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 2));
-      }
-      if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+          for (int e = 0; e < 4; ++e) {
+            float x = s[t][n][e] * scale2;
+            if (edge && key0 + 8 * n + 2 * pair + (e & 1) > lim[t][e >> 1]) x = -INFINITY;
+            s[t][n][e] = x;
+            mn[e >> 1] = fmaxf(mn[e >> 1], x);
+          }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float f = mn[k] == -INFINITY ? 1.0f : ex2(m[k] - mn[k]);
-          m[k] = mn[k];
-          l[k] *= f;
+          mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 1));
+          mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 2));
+        }
+        if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1])) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            o[j][2 * k] *= f;
-            o[j][2 * k + 1] *= f;
+          for (int k = 0; k < 2; ++k) {
+            const float f = mn[k] == -INFINITY ? 1.0f : ex2(m[t][k] - mn[k]);
+            m[t][k] = mn[k];
+            l[t][k] *= f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              o[t][j][2 * k] *= f;
+              o[t][j][2 * k + 1] *= f;
+            }
           }
         }
+        const float sub[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0], m[t][1] == -INFINITY ? 0.0f : m[t][1]};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[t][n][e] = ex2(s[t][n][e] - sub[e >> 1]);
+            l[t][e >> 1] += s[t][n][e];
+          }
+        split2(T(), s[t][0][0], s[t][0][1], hi[t][0], lo[t][0]);
+        split2(T(), s[t][0][2], s[t][0][3], hi[t][1], lo[t][1]);
+        split2(T(), s[t][1][0], s[t][1][1], hi[t][2], lo[t][2]);
+        split2(T(), s[t][1][2], s[t][1][3], hi[t][3], lo[t][3]);
       }
-      const float sub[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] = ex2(s[n][e] - sub[e >> 1]);
-          l[e >> 1] += s[n][e];
-        }
-      uint32_t hi[4], lo[4];
-      split2(T(), s[0][0], s[0][1], hi[0], lo[0]);
-      split2(T(), s[0][2], s[0][3], hi[1], lo[1]);
-      split2(T(), s[1][0], s[1][1], hi[2], lo[2]);
-      split2(T(), s[1][2], s[1][3], hi[3], lo[3]);
       // weighted values: matrices (keys 0-7, 8-15) x (8 features), transposed
-      const int vrow = lane & 15, vcol = lane >> 4;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t v4[4];
-        ldsm4t(Vs + vrow * (2 * kD) + (((2 * j + vcol) ^ (vrow & 7)) << 4), v4);
-        mma(T(), o[2 * j], hi, v4[0], v4[1]);
-        mma(T(), o[2 * j + 1], hi, v4[2], v4[3]);
-        mma(T(), o[2 * j], lo, v4[0], v4[1]);
-        mma(T(), o[2 * j + 1], lo, v4[2], v4[3]);
+        ldsm4t(Vs + (j >> 2) * (kTile / 2) + vrow * 128 + (((2 * (j & 3) + vcol) ^ (vrow & 7)) << 4), v4);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          mma(T(), o[t][2 * j], hi[t], v4[0], v4[1]);
+          mma(T(), o[t][2 * j + 1], hi[t], v4[2], v4[3]);
+        }
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          mma(T(), o[t][2 * j], lo[t], v4[0], v4[1]);
+          mma(T(), o[t][2 * j + 1], lo[t], v4[2], v4[3]);
+        }
       }
     }
     const bool ends = cc.u + 1 == cc.U;
     if (ends || i + 1 == count) {
-      // join the four warps: maxima and sums first, then the outputs, each warp's in its own stage
-      // that was just read (rows of 128 floats; 16-byte blocks swizzled by the row)
+      // join the four warps: maxima and sums first, then the outputs, a block of rows at a time, each warp's
+      // in its own stage that was just read (rows of 128 floats; 16-byte blocks swizzled by the row)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-        if (pair == 0) ml_s[warp][quad + 8 * k] = make_float2(m[k], l[k]);
-      }
-      __syncthreads();
-      float* so = reinterpret_cast<float*>(ring + stage * 2 * kTile);
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = quad + 8 * k;
-        float mx = ml_s[0][r].x;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, ml_s[w][r].x);
-        const float f = mx == -INFINITY ? 0.0f : ex2(m[k] - mx);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int blk = (2 * j + (pair >> 1)) ^ ((r & 7) << 1);
-          *reinterpret_cast<float2*>(so + r * kD + 4 * blk + 2 * (pair & 1)) = make_float2(o[j][2 * k] * f, o[j][2 * k + 1] * f);
+        for (int k = 0; k < 2; ++k) {
+          l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 1);
+          l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 2);
+          if (pair == 0) ml_s[warp][16 * t + quad + 8 * k] = make_float2(m[t][k], l[t][k]);
         }
-      }
-      __syncthreads();
       const int R = cc.v.n * g;
       const bool whole = ends && began;
       const int slot = began ? 1 : 0;
-      for (int r = warp; r < R; r += kWarps) {
-        float mx = -INFINITY, ls = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml_s[w][r].x);
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int t = 0; t < kT; ++t) {
+        __syncthreads();
+        float* so = reinterpret_cast<float*>(ring + stage * 2 * kTile);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 p = ml_s[w][r];
-          ls += mx == -INFINITY ? 0.0f : p.y * ex2(p.x - mx);
-          const float4 x = *reinterpret_cast<const float4*>(
-              reinterpret_cast<const float*>(sm + (w * kStages + stage) * 2 * kTile) + r * kD + 4 * (lane ^ ((r & 7) << 1)));
-          y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+        for (int k = 0; k < 2; ++k) {
+          const int r = quad + 8 * k;
+          float mx = ml_s[0][16 * t + r].x;
+#pragma unroll
+          for (int w = 1; w < kSlices; ++w) mx = fmaxf(mx, ml_s[w][16 * t + r].x);
+          const float f = mx == -INFINITY ? 0.0f : ex2(m[t][k] - mx);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int blk = (2 * j + (pair >> 1)) ^ ((r & 7) << 1);
+            *reinterpret_cast<float2*>(so + r * kD + 4 * blk + 2 * (pair & 1)) =
+                make_float2(o[t][j][2 * k] * f, o[t][j][2 * k + 1] * f);
+          }
         }
-        if (kTeam) {
-          *reinterpret_cast<float4*>(sm + kSmem + r * (4 * kD) + 16 * lane) = y;
-          if (lane == 0) team_ml[r] = make_float2(mx, ls);
-        } else if (whole) {
-          const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
-          finish_row<T>(a, row, lane, y, mx, ls);
-        } else {
-          const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * ws.rows + r;
-          *reinterpret_cast<float4*>(ws.o + at * kD + 4 * lane) = y;
-          if (lane == 0) ws.ml[at] = make_float2(mx, ls);
+        __syncthreads();
+        for (int rr = warp; rr < min(16, R - 16 * t); rr += kSlices) {
+          const int r = 16 * t + rr;
+          float mx = -INFINITY, ls = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kSlices; ++w) mx = fmaxf(mx, ml_s[w][r].x);
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < kSlices; ++w) {
+            const float2 p = ml_s[w][r];
+            ls += mx == -INFINITY ? 0.0f : p.y * ex2(p.x - mx);
+            const float4 x = *reinterpret_cast<const float4*>(
+                reinterpret_cast<const float*>(sm + (w * kDeep + stage) * 2 * kTile) + rr * kD + 4 * (lane ^ ((rr & 7) << 1)));
+            y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+          }
+          if (kTeam) {
+            *reinterpret_cast<float4*>(sm + kSmem<kT> + r * (4 * kD) + 16 * lane) = y;
+            if (lane == 0) team_ml[r] = make_float2(mx, ls);
+          } else if (whole) {
+            const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
+            finish_row<T>(a, row, lane, y, mx, ls);
+          } else {
+            const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * ws.rows + r;
+            *reinterpret_cast<float4*>(ws.o + at * kD + 4 * lane) = y;
+            if (lane == 0) ws.ml[at] = make_float2(mx, ls);
+          }
         }
       }
       if (began && !ends) {
@@ -342,18 +401,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttn
         split.h = cc.h;
         split.m = 0;
         split.slot = slot;
+        split.q0 = cc.v.q0;
+        split.rows = R;
         split.c_last = owner_of(st.lo + i + (cc.U - 1 - cc.u), st.W, st.G);
       }
-      __syncthreads();   // the stages are written again
+      fence_async_shared();
+      __syncthreads();   // the stages are written again, by copies
       fresh = began = true;
     }
     if (i + 1 < count) advance(cc, b);
   }
+  if (*wait.gave_up)   // copies in flight land before the CTA's memory is given up
+    for (int i = max(0, count - kDeep); i < count; ++i) mbar_wait(&full_s[warp][i % kDeep], (i / kDeep) & 1, 1u << 20);
   if (!kTeam) {
     if (tid == 0) ws.list[blockIdx.x] = split;
     return;
   }
-  // the cluster's parts: CTA k finishes the rows k and k + 8, a warp each
+  // the cluster's parts: CTA k finishes the rows k, k + 8, ..., a warp each
   if (count == 0 && tid < kRows) team_ml[tid] = make_float2(-INFINITY, 0.0f);
   const cooperative_groups::cluster_group team = cooperative_groups::this_cluster();
   team.sync();
@@ -365,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttn
 #pragma unroll
     for (int c = 0; c < kTeamCtas; ++c) {
       p[c] = *team.map_shared_rank(&team_ml[r], c);
-      x[c] = *reinterpret_cast<const float4*>(team.map_shared_rank(sm + kSmem + r * (4 * kD) + 16 * lane, c));
+      x[c] = *reinterpret_cast<const float4*>(team.map_shared_rank(sm + kSmem<kT> + r * (4 * kD) + 16 * lane, c));
     }
 #pragma unroll
     for (int c = 0; c < kTeamCtas; ++c) mx = fmaxf(mx, p[c].x);
@@ -384,17 +448,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_attn_decode(const PagedAttn
   team.sync();   // no CTA leaves while another reads from it
 }
 
-template <typename T>
+template <typename T, int kT>
 cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
   static SmemFlags allowed, allowed_team;
+  Maps maps;
+  maps.K = a.maps[2];
+  maps.V = a.maps[3];
   cudaError_t e;
   if (p.team) {
-    e = allow_smem(k_attn_decode<T, true>, kTeamSmem, a.device, allowed_team);
+    e = allow_smem(k_attn_decode<T, kT, true>, kTeamSmem<kT>, a.device, allowed_team);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kTeamSmem;
+    cfg.dynamicSmemBytes = kTeamSmem<kT>;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -402,11 +469,11 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_attn_decode<T, true>, a, w);
+    e = cudaLaunchKernelEx(&cfg, k_attn_decode<T, kT, true>, a, maps, w);
   } else {
-    e = allow_smem(k_attn_decode<T, false>, kSmem, a.device, allowed);
+    e = allow_smem(k_attn_decode<T, kT, false>, kSmem<kT>, a.device, allowed);
     if (e != cudaSuccess) return e;
-    k_attn_decode<T, false><<<p.grid, kThreads, kSmem, s>>>(a, w);
+    k_attn_decode<T, kT, false><<<p.grid, kThreads, kSmem<kT>, s>>>(a, maps, w);
   }
   if (e != cudaSuccess) return e;
   note_launch();
@@ -415,8 +482,9 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
 
 }  // namespace
 
-cudaError_t attn_decode(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
-  return a.dtype == JOLT_BF16 ? launch<__nv_bfloat16>(a, p, w, s) : launch<__half>(a, p, w, s);
+cudaError_t attn_decode(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s) {
+  if (p.rows == 16) return a.dtype == JOLT_BF16 ? launch<__nv_bfloat16, 1>(a, p, w, s) : launch<__half, 1>(a, p, w, s);
+  return a.dtype == JOLT_BF16 ? launch<__nv_bfloat16, 2>(a, p, w, s) : launch<__half, 2>(a, p, w, s);
 }
 
 }  // namespace jolt

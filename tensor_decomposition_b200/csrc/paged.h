@@ -98,7 +98,7 @@ struct PagedAttnArgs {
   jolt_dtype dtype;
   int32_t device;
   const void *K, *V;           // pages [num_pages][heads][page_size][128]
-  const void *kmap, *vmap;     // their tensor maps (host CUtensorMap)
+  const CUtensorMap* maps;     // host: K and V with boxes of gcd(page_size, 128) rows, K and V with 16 rows
   const void* Q;
   int64_t q_ts, q_hs;          // element strides of Q
   int32_t Hq;
@@ -110,7 +110,7 @@ struct PagedAttnArgs {
 };
 // How a call is run: which kernel, its CTAs, the rows of an item's block and the scratch it needs.
 struct AttnPlan {
-  int32_t decode = 0, team = 0, grid = 0, rows = 0;
+  int32_t decode = 0, team = 0, grid = 0, rows = 0, most = 0;   // most: rows an item can have
   size_t bytes = 0;
 };
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms);

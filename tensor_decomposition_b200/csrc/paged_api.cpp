@@ -14,7 +14,7 @@ struct jolt_pages_s {
   void *K = nullptr, *V = nullptr;
   int device = 0;
   int32_t* d_status = nullptr;
-  CUtensorMap kmap, vmap;   // boxes of gcd(page_size, 128) rows x 64 features
+  CUtensorMap maps[4];   // K and V in boxes of gcd(page_size, 128) rows x 64 features, K and V of 16 rows
 };
 
 namespace {
@@ -181,7 +181,10 @@ JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pag
   const uint64_t strides[3] = {row, row * P, row * P * sh.heads};
   uint32_t box = 128;
   while (P % box) box /= 2;
-  if (!tc_map_bf16_box(&p->kmap, K_pages, 4, dims, strides, box) || !tc_map_bf16_box(&p->vmap, V_pages, 4, dims, strides, box)) {
+  bool ok = true;
+  for (int i = 0; i < 4; ++i)
+    ok = ok && tc_map_bf16_box(&p->maps[i], i & 1 ? V_pages : K_pages, 4, dims, strides, i < 2 ? box : 16);
+  if (!ok) {
     delete p;
     return host_fail(JOLT_ERR_CUDA, "jolt_pages_create: tensor map rejected");
   }
@@ -322,7 +325,7 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   a.dtype = pages->shape.dtype;
   a.device = pages->device;
   a.K = pages->K; a.V = pages->V;
-  a.kmap = &pages->kmap; a.vmap = &pages->vmap;
+  a.maps = pages->maps;
   a.Q = Q; a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.Hq = q_heads;
   a.scale = scale; a.causal = causal != 0;
   a.pre_out = prefix_out; a.pre_lse = prefix_lse;

@@ -261,14 +261,24 @@ JOLT_API void jolt_pages_destroy(jolt_pages_t pages);
  *   [tokens]; inv_freq: device float32 [rope_dim / 2], rope_dim a multiple of 16 up to 128; both
  *   NULL for no rotation.
  */
-JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const void* Q, int64_t q_token_stride,
-                                       int64_t q_head_stride, int32_t q_heads, const void* q_weight, void* Q_out,
-                                       int64_t qo_token_stride, int64_t qo_head_stride, const void* K,
-                                       int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads,
-                                       const void* k_weight, void* K_out, int64_t ko_token_stride,
-                                       int64_t ko_head_stride, float eps, const int32_t* positions,
-                                       const float* inv_freq, int32_t rope_dim, int32_t interleaved,
-                                       void* cuda_stream);
+typedef struct {
+  const void* Q;
+  int64_t q_token_stride, q_head_stride;
+  const void* q_weight;
+  void* Q_out;
+  int64_t qo_token_stride, qo_head_stride;
+  const void* K;
+  int64_t k_token_stride, k_head_stride;
+  const void* k_weight;
+  void* K_out;
+  int64_t ko_token_stride, ko_head_stride;
+  const int32_t* positions;
+  const float* inv_freq;
+  jolt_dtype dtype;
+  int32_t tokens, q_heads, k_heads, rope_dim, interleaved;
+  float eps;
+} jolt_norm_rope;
+JOLT_API jolt_status jolt_qk_norm_rope(const jolt_norm_rope* args, void* cuda_stream);
 
 /*
  * jolt_paged_append - write the keys and values of a batch's new tokens to their places in the
@@ -278,11 +288,19 @@ JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const v
  *   sequence's pages. A token before the cache's begin (kv_len smaller than the chunk) is dropped.
  *   Two tokens of one batch must not share a place.
  */
-JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* batch, const void* K,
-                                       int64_t k_token_stride, int64_t k_head_stride, const void* V,
-                                       int64_t v_token_stride, int64_t v_head_stride, const void* k_weight, float eps,
-                                       const int32_t* positions, const float* inv_freq, int32_t rope_dim,
-                                       int32_t interleaved, void* cuda_stream);
+typedef struct {
+  const void* K;
+  int64_t k_token_stride, k_head_stride;
+  const void* V;
+  int64_t v_token_stride, v_head_stride;
+  const void* k_weight;
+  const int32_t* positions;
+  const float* inv_freq;
+  int32_t rope_dim, interleaved;
+  float eps;
+} jolt_new_rows;
+JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* batch, const jolt_new_rows* rows,
+                                       void* cuda_stream);
 
 /*
  * jolt_paged_attention - attention of a batch's new tokens over the pages, grouped-query as in
@@ -292,15 +310,25 @@ JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* bat
  *   appended before. prefix_out, prefix_lse: the attention of the same queries over another part of
  *   the context and the log of its sum of exponentials (both or neither): joined as a term
  *   e^(prefix_lse) of value prefix_out. A row without keys gets out = 0 and lse = -inf.
+ *   Where a row's keys are divided between CTAs depends on all lengths of the batch, so a row's last
+ *   places may too; the same call gives the same bits.
  * Q: device [total_q][q_heads][128] of the set's dtype, element strides as above. out: device
  *   [total_q][q_heads][128] of that dtype; lse: device float32 [total_q][q_heads], the log of the
  *   sum of exponentials, prefix included, or NULL. prefix_out, prefix_lse: device float32
- *   [total_q][q_heads][128] and [total_q][q_heads], or NULL. All four contiguous, 16-byte aligned.
+ *   [total_q][q_heads][128] and [total_q][q_heads], or NULL. All four contiguous; out and prefix_out
+ *   16-byte aligned.
  */
-JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* batch, const void* Q,
-                                          int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads, float scale,
-                                          int32_t causal, const float* prefix_out, const float* prefix_lse, void* out,
-                                          float* lse, void* cuda_stream);
+typedef struct {
+  const void* Q;
+  int64_t q_token_stride, q_head_stride;
+  const float *prefix_out, *prefix_lse;
+  void* out;
+  float* lse;
+  int32_t q_heads, causal;
+  float scale;
+} jolt_queries;
+JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* batch, const jolt_queries* queries,
+                                          void* cuda_stream);
 
 /*
  * jolt_rel_frob_error - ||ref - approx||_F / ||ref||_F over n elements (the error measure the

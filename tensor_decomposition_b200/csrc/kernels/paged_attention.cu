@@ -158,19 +158,24 @@ size_t ml_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * 
 
 }  // namespace
 
-// Up to 32 rows of a chunk reading one KV head run in the kernel for few rows. Where
-// clusters of 8 CTAs, one for each item, all run at once (33 and more do not: 9.0 us instead of 5.9) and
-// their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0 instead of 7.7 us
-// at 1024 keys, 11.9 and 10.9 at 4096, 19.3 and 13.5 at 8192; 32 items: 26 instead of 32 at 8192).
+// Up to 16 rows of a chunk reading one KV head run in the kernel for few rows; 17 to 32 do where there are
+// few items or long caches (16 x 8 items of 20 rows: 21, 31, 53, 121 and 384 us for 128, 512, 2048, 8192 and
+// 32768 keys, in the other kernel 16, 23, 52, 144 and 533; 4 x 8 items: 12, 16, 24, 47, 114 and 16, 21, 24,
+// 53, 148). Where clusters of 8 CTAs, one for each item, all run at once (33 and more do not: 9.0 us
+// instead of 5.9) and their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0
+// instead of 7.7 us at 1024 keys, 11.9 and 10.9 at 4096, 19.3 and 13.5 at 8192; 32 items: 26 instead of 32
+// at 8192).
+constexpr int kFewItems = 64, kFewTokens = 8192;
 constexpr int kTeamTokens = 4096, kTeamItems = 32;
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   AttnPlan p;
   const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)a.b.max_q * (a.Hq / a.b.heads);
-  p.decode = rows <= 32;
-  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 256;
-  p.most = (int)std::max<int64_t>(1, std::min<int64_t>(rows, p.rows));
   const int64_t items = (int64_t)a.b.heads * a.b.num_seqs;
-  if (p.decode && items <= kTeamItems && (tokens <= kTeamTokens || items >= kTeamItems - 4)) {
+  p.decode = rows <= 16 || (rows <= 32 && (items <= kFewItems || tokens >= kFewTokens));
+  p.rows = !p.decode ? 256 : rows <= 16 ? 16 : 32;
+  p.most = (int)std::max<int64_t>(1, std::min<int64_t>(rows, p.rows));
+  const int fit = p.rows == 16 ? kTeamItems : kTeamItems / 2;   // two CTAs an SM, or one
+  if (p.decode && items <= fit && (tokens <= kTeamTokens || items >= fit - fit / 8)) {
     p.team = 1;
     p.grid = (int)items * 8;
     return p;

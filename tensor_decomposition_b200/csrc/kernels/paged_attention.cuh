@@ -23,8 +23,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The work of a call is a line of units: the sequences in order, in each its items (the rows of one
-// KV head that are attended together), in each item its blocks of keys. CTA c of G takes the units
-// [c W / G, (c + 1) W / G), so that all CTAs end together whatever the lengths are. An item that falls
+// KV head that are attended together), in each item its blocks of keys. The CTAs take shares of one
+// length of it, so that all end together whatever the sequences' lengths are. An item that falls
 // into several CTAs leaves a part in each: its running maximum, sum and unscaled output, in slot 0 when
 // the item began before the CTA's range and slot 1 otherwise. Where an item begins in a CTA and
 // does not end there (one at most per CTA), the CTA lists it for the combining kernel.
@@ -41,11 +41,22 @@ struct Workspace {
   int32_t rows;
 };
 
-// CTA whose range holds unit u.
-__device__ __forceinline__ int owner_of(int64_t u, int64_t W, int G) { return (int)(((u + 1) * G - 1) / W); }
+// Quotient by a divisor that fits 32 bits; the long division only where the dividend does not.
+__device__ __forceinline__ int64_t quot(int64_t a, uint32_t b) {
+  return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / b);
+}
+// The shares: the first W % G CTAs have W / G + 1 units, the others W / G.
+__device__ __forceinline__ int64_t share_begin(int c, int64_t each, int64_t more) { return c * each + min((int64_t)c, more); }
+// CTA whose share holds unit u.
+__device__ __forceinline__ int owner_of(int64_t u, int64_t each, int64_t more) {
+  const int64_t longer = more * (each + 1);
+  if (u < longer) return (int)(u / (each + 1));
+  return (int)(more + (u - longer) / each);
+}
 
 struct Start {
-  int64_t W, lo, hi;   // all units, this CTA's range
+  int64_t each, more;  // units of a share, shares that have one more
+  int64_t lo, hi;      // this CTA's
   int64_t base, units; // the sequence that holds lo: its first unit, its number of them
   int32_t s, G;        // its index; CTAs that have work
 };
@@ -84,12 +95,13 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units,
   for (int s = tid + NT; s < num_seqs; s += NT) sum += work(s);
   int64_t total, base = 0;
   int64_t incl = block_scan<NT>(sum, sm, total);
-  r.W = total;
-  const int64_t most = (total + min_units - 1) / min_units;
+  const int64_t most = quot(total + min_units - 1, min_units);
   r.G = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
   if ((int)blockIdx.x >= r.G) return r;
-  r.lo = (int64_t)blockIdx.x * total / r.G;
-  r.hi = (int64_t)(blockIdx.x + 1) * total / r.G;
+  r.each = quot(total, r.G);
+  r.more = total - r.each * r.G;
+  r.lo = share_begin(blockIdx.x, r.each, r.more);
+  r.hi = share_begin(blockIdx.x + 1, r.each, r.more);
   if (num_seqs <= NT) {   // the scan just made is the one over sequences
     if (incl > r.lo && incl - mine <= r.lo) {
       base_s = incl - mine;

@@ -35,7 +35,7 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kRegsSoftmax = 104, kRegsOther = 64;   // 512 x 104 + 128 x 64 = the launch's 640 x 96
 constexpr int kSmem = (2 + kStages) * kTileBytes;
-constexpr int kItem = 2;                     // what an item costs besides its tiles, in tiles
+constexpr int kItem = 3;                     // what an item costs besides its tiles, in tiles
 constexpr float kFollow = 8.0f;
 
 struct Bars {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Piece piece_s[kSoftmaxWarps / 2 + 4];   // places on the line: the softmax pairs', the others'
   __shared__ bool any_s;
   __shared__ __align__(8) float both_s[2][2][kHalf];   // what the two threads of a row tell each other
-  __shared__ int64_t range_s[3];   // all units, the end of this CTA's, CTAs with work
+  __shared__ int64_t range_s[3];   // the end of this CTA's share, units of a share, shares with one more
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchView& b = a.b;
   const int g = a.Hq / b.heads;
@@ -266,6 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     gave_up = 0;
     fence_barrier_init();
   }
+  if (warp == kSoftmaxWarps) {
+    tmem_alloc(&tmem_s, 512);
+    tmem_relinquish();
+  }
   const Start st = find_start<kThreads>(
       b.num_seqs,
       [&](int s) {
@@ -279,29 +283,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       kItem + 2, reinterpret_cast<int64_t*>(both_s));
   if ((int)blockIdx.x >= st.G) {
     if (tid == 0) ws.list[blockIdx.x].s = -1;
+    if (warp == kSoftmaxWarps) tmem_dealloc(tmem_s, 512);
     return;
-  }
-  if (warp == kSoftmaxWarps) {
-    tmem_alloc(&tmem_s, 512);
-    tmem_relinquish();
   }
   if (tid == 0) {
     Piece p;
     p.s = st.s;
     p.v = seq_view(b, p.s);
     p.M = blocks_of(p.v, g);
-    const int64_t per = st.units / b.heads;
-    int64_t at = st.lo - st.base;
-    p.h = (int)(at / per);
-    at %= per;
+    const int64_t per = quot(st.units, b.heads), from = st.lo - st.base;   // (a head's units fit 32 bits)
+    p.h = (int)quot(from, (uint32_t)per);
+    int at = (int)(from - p.h * per);
     p.m = 0;
     for (int n; at >= (n = tiles_of(p.v, g, p.m, causal) + kItem); at -= n) ++p.m;
     p.left = (int)(st.hi - st.lo);
-    any_s = enter(p, (int)at, g, causal);   // a share can lie in an item's first units only
+    any_s = enter(p, at, g, causal);   // a share can lie in an item's first units only
     for (Piece& q : piece_s) q = p;
-    range_s[0] = st.W;
-    range_s[1] = st.hi;
-    range_s[2] = st.G;
+    range_s[0] = st.hi;
+    range_s[1] = st.each;
+    range_s[2] = st.more;
     ws.list[blockIdx.x].s = -1;
   }
   tc_fence_before();
@@ -493,8 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tok = (r0 + r2) / g, hd = (r0 + r2) - tok * g;
         const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g * a.q_hs + 8 * c16;
         const uint32_t dst = smem_u32(Qs + t * kTileBytes + (c16 >> 3) * kHalfTile);
+        const int pairs = (min(kHalf, R - r0) + 1) / 2;   // what lies behind the last row does not matter
 #pragma unroll 4
-        for (int i = 0; i < kHalf / 2; ++i) {
+        for (int i = 0; i < pairs; ++i) {
           const int rr = 2 * i + r2;
           const bool in = r0 + rr < R;
           const T* src = in ? Q + (int64_t)tok * a.q_ts + (int64_t)hd * a.q_hs : Q;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool alone = solo(p, g), began = p.t0 == 0, ends = p.t1 == p.T;
       const int R = p.v.n * g, r0 = p.m * kBlockRows + (alone ? 0 : t * kHalf);
       if (tid == 0 && began && !ends)   // the share's last piece
-        ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[1] + (p.T - p.t1) - 1, range_s[0], range_s[2]), 1,
+        ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[0] + (p.T - p.t1) - 1, range_s[1], range_s[2]), 1,
                                     p.v.q0, min(kBlockRows, R - p.m * kBlockRows)};
       const int t1 = p.t1, every = alone ? 2 : 1, t0 = p.t0 + (alone ? t : 0);   // this half's tiles
       const bool rows = r0 + 32 * wq < R;         // whether the warp has any
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mn = fmaxf(m, fmaxf(mh, *other) * scale2);
         if (j == t0) {
           m = mn;
-        } else if (__any_sync(0xffffffffu, mn - m > kFollow)) {
+        } else if (__any_sync(0xffffffffu, r < R && mn - m > kFollow)) {   // lanes behind the rows hold anything
           const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
           m = mn;
           l *= f;

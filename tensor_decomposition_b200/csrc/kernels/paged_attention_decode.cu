@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     lc.s = st.s;
     lc.v = seq_view(b, st.s);
     lc.U = units_of(lc.v);
-    lc.h = (int)((st.lo - st.base) / lc.U);
-    lc.u = (int)((st.lo - st.base) % lc.U);
+    lc.h = (int)quot(st.lo - st.base, lc.U);
+    lc.u = (int)(st.lo - st.base - (int64_t)lc.h * lc.U);
   }
   Cursor cc = lc;
   const int count = (int)(st.hi - st.lo);
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
         split.slot = slot;
         split.q0 = cc.v.q0;
         split.rows = R;
-        split.c_last = owner_of(st.lo + i + (cc.U - 1 - cc.u), st.W, st.G);
+        split.c_last = owner_of(st.lo + i + (cc.U - 1 - cc.u), st.each, st.more);
       }
       fence_async_shared();
       __syncthreads();   // the stages are written again, by copies

@@ -97,7 +97,6 @@ struct PagedAttnArgs {
   BatchView b;
   jolt_dtype dtype;
   int32_t device;
-  const void *K, *V;           // pages [num_pages][heads][page_size][128]
   const CUtensorMap* maps;     // host: K and V with boxes of gcd(page_size, 128) rows, K and V with 16 rows
   const void* Q;
   int64_t q_ts, q_hs;          // element strides of Q

@@ -100,8 +100,25 @@ jolt_status check_rope(const char* what, const int32_t* positions, bool position
   return JOLT_OK;
 }
 
-jolt_status check_batch(const char* what, const jolt_pages_s* pg, const jolt_batch* b) {
-  if (!pg || !b) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null pages or batch", what);
+RowsIn rows_in(const void* p, int64_t ts, int64_t hs, int heads, const void* w) {
+  RowsIn r;
+  r.p = p;
+  r.ts = (int32_t)ts;   // checked by check_rows
+  r.hs = (int32_t)hs;
+  r.heads = heads;
+  r.w = w;
+  return r;
+}
+RowsOut rows_out(void* p, int64_t ts, int64_t hs) {
+  RowsOut r;
+  r.p = p;
+  r.ts = (int32_t)ts;
+  r.hs = (int32_t)hs;
+  return r;
+}
+
+jolt_status check_batch(const char* what, const jolt_pages_s* pg, const jolt_batch* b, const void* args) {
+  if (!pg || !b || !args) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null pages, batch or arguments", what);
   if (b->num_seqs < 0 || b->total_q < 0 || b->max_q < 0 || b->max_pages < 0)
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: negative batch size", what);
   if (b->num_seqs > 0 && (!b->q_start || !b->kv_len || (b->max_pages > 0 && !b->page_table)))
@@ -224,36 +241,29 @@ JOLT_API jolt_status jolt_pages_status(jolt_pages_t p, void* cuda_stream) {
   return JOLT_OK;
 }
 
-JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const void* Q, int64_t q_token_stride,
-                                       int64_t q_head_stride, int32_t q_heads, const void* q_weight, void* Q_out,
-                                       int64_t qo_token_stride, int64_t qo_head_stride, const void* K,
-                                       int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads,
-                                       const void* k_weight, void* K_out, int64_t ko_token_stride,
-                                       int64_t ko_head_stride, float eps, const int32_t* positions,
-                                       const float* inv_freq, int32_t rope_dim, int32_t interleaved,
-                                       void* cuda_stream) {
+JOLT_API jolt_status jolt_qk_norm_rope(const jolt_norm_rope* args, void* cuda_stream) {
   const char* what = "jolt_qk_norm_rope";
   host_clear_error();
-  if (dtype != JOLT_BF16 && dtype != JOLT_F16) return host_fail(JOLT_ERR_UNSUPPORTED, "%s: rows are bf16 or f16", what);
-  if (tokens < 0 || k_heads < 0) return host_fail(JOLT_ERR_INVALID_ARG, "%s: negative size", what);
-  if (tokens == 0) return JOLT_OK;
-  jolt_status st = check_rows(what, "Q", Q, q_token_stride, q_head_stride, q_heads);
-  if (st == JOLT_OK) st = check_rows(what, "Q_out", Q_out, qo_token_stride, qo_head_stride, q_heads);
-  if (st == JOLT_OK && k_heads > 0) st = check_rows(what, "K", K, k_token_stride, k_head_stride, k_heads);
-  if (st == JOLT_OK && k_heads > 0) st = check_rows(what, "K_out", K_out, ko_token_stride, ko_head_stride, k_heads);
-  if (st == JOLT_OK) st = check_rope(what, positions, true, inv_freq, rope_dim);
+  if (!args) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null arguments", what);
+  const jolt_norm_rope& n = *args;
+  if (n.dtype != JOLT_BF16 && n.dtype != JOLT_F16) return host_fail(JOLT_ERR_UNSUPPORTED, "%s: rows are bf16 or f16", what);
+  if (n.tokens < 0 || n.k_heads < 0) return host_fail(JOLT_ERR_INVALID_ARG, "%s: negative size", what);
+  if (n.tokens == 0) return JOLT_OK;
+  jolt_status st = check_rows(what, "Q", n.Q, n.q_token_stride, n.q_head_stride, n.q_heads);
+  if (st == JOLT_OK) st = check_rows(what, "Q_out", n.Q_out, n.qo_token_stride, n.qo_head_stride, n.q_heads);
+  if (st == JOLT_OK && n.k_heads > 0) st = check_rows(what, "K", n.K, n.k_token_stride, n.k_head_stride, n.k_heads);
+  if (st == JOLT_OK && n.k_heads > 0) st = check_rows(what, "K_out", n.K_out, n.ko_token_stride, n.ko_head_stride, n.k_heads);
+  if (st == JOLT_OK) st = check_rope(what, n.positions, true, n.inv_freq, n.rope_dim);
   if (st != JOLT_OK) return st;
-  if (((int64_t)q_heads + k_heads) * tokens > INT32_MAX)
+  if (((int64_t)n.q_heads + n.k_heads) * n.tokens > INT32_MAX)
     return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 rows", what);
-  if (!aligned16(q_weight) || !aligned16(k_weight))
+  if (!aligned16(n.q_weight) || !aligned16(n.k_weight))
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: weights must be 16-byte aligned", what);
-  RowsIn q, k;
-  RowsOut qo, ko;
-  q.p = Q; q.ts = (int32_t)q_token_stride; q.hs = (int32_t)q_head_stride; q.heads = q_heads; q.w = q_weight;
-  qo.p = Q_out; qo.ts = (int32_t)qo_token_stride; qo.hs = (int32_t)qo_head_stride;
-  if (k_heads > 0) {
-    k.p = K; k.ts = (int32_t)k_token_stride; k.hs = (int32_t)k_head_stride; k.heads = k_heads; k.w = k_weight;
-    ko.p = K_out; ko.ts = (int32_t)ko_token_stride; ko.hs = (int32_t)ko_head_stride;
+  RowsIn q = rows_in(n.Q, n.q_token_stride, n.q_head_stride, n.q_heads, n.q_weight), k;
+  RowsOut qo = rows_out(n.Q_out, n.qo_token_stride, n.qo_head_stride), ko;
+  if (n.k_heads > 0) {
+    k = rows_in(n.K, n.k_token_stride, n.k_head_stride, n.k_heads, n.k_weight);
+    ko = rows_out(n.K_out, n.ko_token_stride, n.ko_head_stride);
   }
   cudaStream_t s = (cudaStream_t)cuda_stream;
   int dev = 0, sms = 0;
@@ -261,62 +271,57 @@ JOLT_API jolt_status jolt_qk_norm_rope(jolt_dtype dtype, int32_t tokens, const v
   if (e == cudaSuccess) e = sm_count(dev, &sms);
   if (e != cudaSuccess) return cuda_fail(what, e);
   ProfScope prof("qk_norm_rope", s);
-  e = norm_rope(dtype, tokens, q, qo, k, ko, rope_of(eps, positions, inv_freq, rope_dim, interleaved), sms, s);
+  e = norm_rope(n.dtype, n.tokens, q, qo, k, ko, rope_of(n.eps, n.positions, n.inv_freq, n.rope_dim, n.interleaved), sms, s);
   return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
 }
 
-JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* batch, const void* K,
-                                       int64_t k_token_stride, int64_t k_head_stride, const void* V,
-                                       int64_t v_token_stride, int64_t v_head_stride, const void* k_weight, float eps,
-                                       const int32_t* positions, const float* inv_freq, int32_t rope_dim,
-                                       int32_t interleaved, void* cuda_stream) {
+JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* batch, const jolt_new_rows* rows,
+                                       void* cuda_stream) {
   const char* what = "jolt_paged_append";
   host_clear_error();
-  jolt_status st = check_batch(what, pages, batch);
+  jolt_status st = check_batch(what, pages, batch, rows);
   if (st != JOLT_OK) return st;
+  const jolt_new_rows& r = *rows;
   const int H = pages->shape.heads;
   if (batch->total_q == 0 || batch->num_seqs == 0) return JOLT_OK;
-  st = check_rows(what, "K", K, k_token_stride, k_head_stride, H);
-  if (st == JOLT_OK) st = check_rows(what, "V", V, v_token_stride, v_head_stride, H);
-  if (st == JOLT_OK) st = check_rope(what, positions, false, inv_freq, rope_dim);
+  st = check_rows(what, "K", r.K, r.k_token_stride, r.k_head_stride, H);
+  if (st == JOLT_OK) st = check_rows(what, "V", r.V, r.v_token_stride, r.v_head_stride, H);
+  if (st == JOLT_OK) st = check_rope(what, r.positions, false, r.inv_freq, r.rope_dim);
   if (st != JOLT_OK) return st;
   if (2 * (int64_t)H * batch->total_q > INT32_MAX) return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 rows", what);
-  if (!aligned16(k_weight)) return host_fail(JOLT_ERR_INVALID_ARG, "%s: the weight must be 16-byte aligned", what);
+  if (!aligned16(r.k_weight)) return host_fail(JOLT_ERR_INVALID_ARG, "%s: the weight must be 16-byte aligned", what);
   st = check_device(what, pages);
   if (st != JOLT_OK) return st;
-  RowsIn k, v;
-  k.p = K; k.ts = (int32_t)k_token_stride; k.hs = (int32_t)k_head_stride; k.heads = H; k.w = k_weight;
-  v.p = V; v.ts = (int32_t)v_token_stride; v.hs = (int32_t)v_head_stride; v.heads = H;
   cudaStream_t s = (cudaStream_t)cuda_stream;
   int sms = 0;
   cudaError_t e = sm_count(pages->device, &sms);
   if (e != cudaSuccess) return cuda_fail(what, e);
   ProfScope prof("paged_append", s);
-  e = paged_append(pages->shape.dtype, view_of(pages, batch), k, v, pages->K, pages->V,
-                                     rope_of(eps, positions, inv_freq, rope_dim, interleaved), sms, s);
+  e = paged_append(pages->shape.dtype, view_of(pages, batch), rows_in(r.K, r.k_token_stride, r.k_head_stride, H, r.k_weight),
+                   rows_in(r.V, r.v_token_stride, r.v_head_stride, H, nullptr), pages->K, pages->V,
+                   rope_of(r.eps, r.positions, r.inv_freq, r.rope_dim, r.interleaved), sms, s);
   return e == cudaSuccess ? JOLT_OK : cuda_fail(what, e);
 }
 
-JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* batch, const void* Q,
-                                          int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads, float scale,
-                                          int32_t causal, const float* prefix_out, const float* prefix_lse, void* out,
-                                          float* lse, void* cuda_stream) {
+JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* batch, const jolt_queries* queries,
+                                          void* cuda_stream) {
   const char* what = "jolt_paged_attention";
   host_clear_error();
-  jolt_status st = check_batch(what, pages, batch);
+  jolt_status st = check_batch(what, pages, batch, queries);
   if (st != JOLT_OK) return st;
-  if (q_heads <= 0 || q_heads % pages->shape.heads)
+  const jolt_queries& q = *queries;
+  if (q.q_heads <= 0 || q.q_heads % pages->shape.heads)
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: q_heads must be a positive multiple of the %d KV heads", what,
                      pages->shape.heads);
-  if ((int64_t)batch->total_q * q_heads > INT32_MAX - 1024)
+  if ((int64_t)batch->total_q * q.q_heads > INT32_MAX - 1024)
     return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 query rows", what);
-  if (!prefix_out != !prefix_lse)
+  if (!q.prefix_out != !q.prefix_lse)
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: prefix_out and prefix_lse come together", what);
   if (batch->total_q == 0 || batch->num_seqs == 0) return JOLT_OK;
-  st = check_rows(what, "Q", Q, q_token_stride, q_head_stride, q_heads);
+  st = check_rows(what, "Q", q.Q, q.q_token_stride, q.q_head_stride, q.q_heads);
   if (st != JOLT_OK) return st;
-  if (!out) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null out", what);
-  if (!aligned16(out) || !aligned16(prefix_out))
+  if (!q.out) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null out", what);
+  if (!aligned16(q.out) || !aligned16(q.prefix_out))
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: out and prefix_out must be 16-byte aligned", what);
   st = check_device(what, pages);
   if (st != JOLT_OK) return st;
@@ -324,12 +329,11 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   a.b = view_of(pages, batch);
   a.dtype = pages->shape.dtype;
   a.device = pages->device;
-  a.K = pages->K; a.V = pages->V;
   a.maps = pages->maps;
-  a.Q = Q; a.q_ts = q_token_stride; a.q_hs = q_head_stride; a.Hq = q_heads;
-  a.scale = scale; a.causal = causal != 0;
-  a.pre_out = prefix_out; a.pre_lse = prefix_lse;
-  a.out = out; a.lse = lse;
+  a.Q = q.Q; a.q_ts = q.q_token_stride; a.q_hs = q.q_head_stride; a.Hq = q.q_heads;
+  a.scale = q.scale; a.causal = q.causal != 0;
+  a.pre_out = q.prefix_out; a.pre_lse = q.prefix_lse;
+  a.out = q.out; a.lse = q.lse;
   cudaStream_t s = (cudaStream_t)cuda_stream;
   ProfScope prof("paged_attention", s);
   int sms = 0;

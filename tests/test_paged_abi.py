@@ -55,10 +55,9 @@ def test_null_handles(J, untouched):
     d = J.BatchDesc(1, 1, 1, 1, p, p, p)
     calls = {
         "jolt_pages_status": lambda: L.jolt_pages_status(None, None),
-        "jolt_paged_append": lambda: L.jolt_paged_append(None, ctypes.addressof(d), p, 128, 128, p, 128, 128, None, 1e-6,
-                                                         None, None, 0, 0, None),
-        "jolt_paged_attention": lambda: L.jolt_paged_attention(None, ctypes.addressof(d), p, 128, 128, 8, 1.0, 1, None,
-                                                               None, p, None, None),
+        "jolt_qk_norm_rope": lambda: L.jolt_qk_norm_rope(None, None),
+        "jolt_paged_append": lambda: L.jolt_paged_append(None, ctypes.addressof(d), bytes(J._NEW_ROWS.size), None),
+        "jolt_paged_attention": lambda: L.jolt_paged_attention(None, ctypes.addressof(d), bytes(J._QUERIES.size), None),
     }
     for name, call in calls.items():
         assert call() == 1, name
@@ -71,15 +70,37 @@ def test_norm_rope_refuses(J, untouched):
     keep, p = _buf()
 
     def call(dtype=0, tokens=1, q=p, qs=128, hq=1, qo=p, k=None, hk=0, ko=None, w=None, pos=p, fr=p, rd=128):
-        return J._lib.jolt_qk_norm_rope(dtype, tokens, q, 128, qs, hq, w, qo, 128, 128, k, 128, 128, hk, None, ko, 128, 128,
-                                        1e-6, pos, fr, rd, 0, None)
+        z = [x or 0 for x in (q, w, qo, k, ko, pos, fr)]
+        return J._lib.jolt_qk_norm_rope(J._NORM_ROPE.pack(z[0], 128, qs, z[1], z[2], 128, 128, z[3], 128, 128, 0, z[4], 128,
+                                                          128, z[5], z[6], dtype, tokens, hq, hk, rd, 0, 1e-6), None)
 
     assert call(dtype=1) == 9                       # float32 rows
     assert call(tokens=-1) == 1
     assert call(q=None) == 1 and call(qo=None) == 1 and call(hq=0) == 1
+    assert call(qs=1 << 32) == 9                    # strides beyond 32 bits
+    assert call(hq=1 << 20, tokens=1 << 12) == 9    # rows beyond 32 bits
     assert call(qs=100) == 1 and call(q=p + 8) == 1 and call(w=p + 4) == 1
     assert call(hk=2, k=p) == 1 and call(hk=2, ko=p) == 1 and call(hk=-1) == 1
     assert call(pos=None) == 1
     for rd in (0, 8, 24, 144, -16):
         assert call(rd=rd) == 1
     assert call(tokens=0, q=None, qo=None) == 0     # nothing to do
+
+
+def test_packed_structs_match_the_header(J):
+    """The binding's packed layouts against the structs of the header, compiled by the host compiler."""
+    import os
+    import subprocess
+    import tempfile
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with tempfile.TemporaryDirectory() as d:
+        src = os.path.join(d, "s.c")
+        with open(src, "w") as f:
+            f.write('#include <stddef.h>\n#include <stdio.h>\n#include "jolt.h"\nint main(void) { printf("%zu %zu %zu %zu %zu",'
+                    'offsetof(jolt_norm_rope, eps), offsetof(jolt_new_rows, eps), offsetof(jolt_queries, scale),'
+                    'sizeof(jolt_batch), sizeof(jolt_page_shape)); return 0; }')
+        exe = os.path.join(d, "s")
+        subprocess.run(["gcc", "-I", os.path.join(root, "include"), src, "-o", exe], check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [J._NORM_ROPE.size - 4, J._NEW_ROWS.size - 4, J._QUERIES.size - 4, ctypes.sizeof(J.BatchDesc),
+                   ctypes.sizeof(J.PageShape)]

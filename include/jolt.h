@@ -190,6 +190,16 @@ JOLT_API jolt_status jolt_decode(jolt_stream_t stream, void* K_out, void* V_out,
 JOLT_API jolt_status jolt_attention(jolt_stream_t stream, const void* Q, int32_t q_heads, int32_t n_queries,
                                     float scale, float* out, void* cuda_stream);
 
+/*
+ * jolt_attention_lse - jolt_attention of one layer with the queries token by token, and the log of
+ *   each row's sum of exponentials, as jolt_paged_attention takes them for a prefix: a model whose
+ *   context is a compressed stream followed by tokens in pages attends to both with one call each.
+ * Q: device bf16 [n_queries][q_heads][head_dim] of layer `layer`; out: device float32, same shape;
+ *   lse: device float32 [n_queries][q_heads]. Otherwise as jolt_attention.
+ */
+JOLT_API jolt_status jolt_attention_lse(jolt_stream_t stream, int32_t layer, const void* Q, int32_t q_heads,
+                                        int32_t n_queries, float scale, float* out, float* lse, void* cuda_stream);
+
 /* ---------------------------------------------------------------- the growing cache
  * The codec compresses a cache that is complete; these entry points serve the part of a context
  * that still grows: query and key rows normed and rotated, keys and values appended to a paged

@@ -1474,19 +1474,19 @@ JOLT_API jolt_status jolt_decode(jolt_stream_t st, void* K_out, void* V_out, voi
   return JOLT_OK;
 }
 
-JOLT_API jolt_status jolt_attention(jolt_stream_t st, const void* Q, int32_t q_heads, int32_t n_queries,
-                                    float scale, float* out, void* cuda_stream) {
-  g_err.clear();
-  if (!st || !Q || !out) return fail(JOLT_ERR_INVALID_ARG, "jolt_attention: null stream, Q or out");
-  if (!st->has_v) return fail(JOLT_ERR_INVALID_ARG, "jolt_attention: the stream holds keys only");
-  if (st->dtype != JOLT_BF16) return fail(JOLT_ERR_UNSUPPORTED, "jolt_attention: bf16 streams only");
+static jolt_status stream_attention(const char* what, jolt_stream_t st, const void* Q, int32_t q_heads, int32_t n_queries,
+                                    float scale, float* out, float* lse, int layer0, int layers, int token_major,
+                                    void* cuda_stream) {
+  if (!st->has_v) return fail(JOLT_ERR_INVALID_ARG, "%s: the stream holds keys only", what);
+  if (st->dtype != JOLT_BF16) return fail(JOLT_ERR_UNSUPPORTED, "%s: bf16 streams only", what);
   if (q_heads <= 0 || n_queries <= 0 || q_heads % st->H != 0)
-    return fail(JOLT_ERR_INVALID_ARG, "jolt_attention: q_heads must be a positive multiple of the %d KV heads", st->H);
+    return fail(JOLT_ERR_INVALID_ARG, "%s: q_heads must be a positive multiple of the %d KV heads", what, st->H);
   cudaStream_t s = (cudaStream_t)cuda_stream;
   AttnArgs a;
-  a.L = st->L; a.H = st->H; a.T = st->T; a.D = st->D; a.Hq = q_heads; a.n = n_queries; a.R = std::max(st->R, 1);
+  a.L = layers; a.H = st->H; a.T = st->T; a.D = st->D; a.Hq = q_heads; a.n = n_queries; a.R = std::max(st->R, 1);
+  a.layer0 = layer0; a.token_major = token_major;
   a.scale = scale; a.meta = st->d_meta; a.body = st->d_body; a.Pi = st->d_Pi;
-  a.Q = reinterpret_cast<const __nv_bfloat16*>(Q); a.out = out;
+  a.Q = reinterpret_cast<const __nv_bfloat16*>(Q); a.out = out; a.lse = lse;
   a.nchunk = attn_chunks(st->T); a.ngroups = attn_groups(q_heads, st->H, n_queries);
   const size_t nqv = (size_t)a.L * q_heads * n_queries;
   const size_t floats = nqv * (kD + a.R) + (size_t)a.L * a.H * a.nchunk * a.ngroups * attn_part_floats(a.R);
@@ -1499,8 +1499,24 @@ JOLT_API jolt_status jolt_attention(jolt_stream_t st, const void* Q, int32_t q_h
   cudaError_t e = attention(a, s);
   cudaError_t e2 = cudaFreeAsync(scratch, s);
   if (e == cudaSuccess) e = e2;
-  if (e != cudaSuccess) return fail(JOLT_ERR_CUDA, "jolt_attention: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(JOLT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return JOLT_OK;
+}
+
+JOLT_API jolt_status jolt_attention(jolt_stream_t st, const void* Q, int32_t q_heads, int32_t n_queries,
+                                    float scale, float* out, void* cuda_stream) {
+  g_err.clear();
+  if (!st || !Q || !out) return fail(JOLT_ERR_INVALID_ARG, "jolt_attention: null stream, Q or out");
+  return stream_attention("jolt_attention", st, Q, q_heads, n_queries, scale, out, nullptr, 0, st->L, 0, cuda_stream);
+}
+
+JOLT_API jolt_status jolt_attention_lse(jolt_stream_t st, int32_t layer, const void* Q, int32_t q_heads,
+                                        int32_t n_queries, float scale, float* out, float* lse, void* cuda_stream) {
+  g_err.clear();
+  if (!st || !Q || !out || !lse) return fail(JOLT_ERR_INVALID_ARG, "jolt_attention_lse: null stream, Q, out or lse");
+  if (layer < 0 || layer >= st->L)
+    return fail(JOLT_ERR_INVALID_ARG, "jolt_attention_lse: layer %d of a stream of %d", layer, st->L);
+  return stream_attention("jolt_attention_lse", st, Q, q_heads, n_queries, scale, out, lse, layer, 1, 1, cuda_stream);
 }
 
 JOLT_API jolt_status jolt_rel_frob_error(const void* ref, const void* approx, uint64_t n, jolt_dtype dtype,

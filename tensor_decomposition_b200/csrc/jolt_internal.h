@@ -210,13 +210,15 @@ cudaError_t decode(const DecodeArgs& a, cudaStream_t s);
 // Attention over the compressed cache (attention.cu): out = softmax(scale Q K_hat^T) V_hat per
 // query, K_hat / V_hat never formed. Q, out: [L][Hq][n][D]; query head j reads KV head j / (Hq/H).
 struct AttnArgs {
-  int L, H, T, D, Hq, n, R;      // R: the stream's largest token rank (>= 1)
+  int L, H, T, D, Hq, n, R;      // R: the stream's largest token rank (>= 1); L layers from layer0 on
+  int layer0 = 0, token_major = 0;   // token_major: Q, out [n][Hq][D] of one layer
   float scale;
   const StreamMeta* meta;
   const uint8_t* body;
   const float* Pi;               // [D][D]
   const __nv_bfloat16* Q;
   float* out;
+  float* lse = nullptr;          // log of the sum of exponentials of each row, or null
   float* qpi;                    // scratch [L][Hq][n][D]
   float* qhat;                   // scratch [L][Hq][n][R]
   float* part;                   // scratch [L][H][nchunk][ngroups][attn_part_floats(R)]

@@ -33,8 +33,14 @@ struct LtView {
   const uint8_t* codes;
 };
 
+// Row of query i of head j of a layer in Q, out and the scratch: [layers][q_heads][n], or [n][q_heads] of one layer.
+__device__ __forceinline__ int64_t q_row(const AttnArgs& a, int layer, int j, int i) {
+  return a.token_major ? (int64_t)i * a.Hq + j : ((int64_t)layer * a.Hq + j) * a.n + i;
+}
+
 __device__ __forceinline__ LtView lt_view(const AttnArgs& a, int lt) {
   const StreamMeta* m = a.meta;
+  lt += 2 * a.layer0;
   LtView v;
   v.rt = m->lt_rank[lt][0];
   v.rd = m->lt_rank[lt][1];
@@ -51,15 +57,15 @@ __device__ __forceinline__ LtView lt_view(const AttnArgs& a, int lt) {
 // qpi = Pi^T q and qhat = G_h (U_D^T q) (keys of the query's layer); one CTA per query vector.
 __global__ void __launch_bounds__(128) k_attn_prep(AttnArgs a) {
   __shared__ float q[kD], qt[kD];
-  const int idx = blockIdx.x;                       // ((layer * Hq) + j) * n + i
-  const int layer = idx / (a.Hq * a.n), j = (idx / a.n) % a.Hq;
+  const int layer = blockIdx.x / (a.Hq * a.n), j = (blockIdx.x / a.n) % a.Hq;
+  const int64_t idx = q_row(a, layer, j, blockIdx.x % a.n);
   const int h = j / (a.Hq / a.H);
   const int tid = threadIdx.x;
-  q[tid] = bf(a.Q[(int64_t)idx * kD + tid]);
+  q[tid] = bf(a.Q[idx * kD + tid]);
   __syncthreads();
   float s = 0.0f;
   for (int e = 0; e < kD; ++e) s = fmaf(a.Pi[e * kD + tid], q[e], s);
-  a.qpi[(int64_t)idx * kD + tid] = s;
+  a.qpi[idx * kD + tid] = s;
   const LtView k = lt_view(a, 2 * layer);
   if (tid < k.rd) {
     float t = 0.0f;
@@ -73,7 +79,7 @@ __global__ void __launch_bounds__(128) k_attn_prep(AttnArgs a) {
       const __nv_bfloat16* g = k.G + ((int64_t)h * k.rt + r) * k.rd;
       for (int c = 0; c < k.rd; ++c) t = fmaf(bf(g[c]), qt[c], t);
     }
-    a.qhat[(int64_t)idx * a.R + r] = t;
+    a.qhat[idx * a.R + r] = t;
   }
 }
 
@@ -98,7 +104,7 @@ __global__ void __launch_bounds__(128) k_attn_partial(AttnArgs a) {
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
     const int qv = q0 + min(q, nq - 1);
-    const int64_t idx = ((int64_t)layer * a.Hq + h * g + qv / a.n) * a.n + qv % a.n;
+    const int64_t idx = q_row(a, layer, h * g + qv / a.n, qv % a.n);
     float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -278,8 +284,9 @@ __global__ void __launch_bounds__(128) k_attn_combine(AttnArgs a) {
     if (V.b)
       for (int d = 0; d < kD; ++d) o = fmaf(a.Pi[tid * kD + d], ay[d], o);
     const int qv = q0 + q;
-    const int64_t idx = ((int64_t)layer * a.Hq + h * g + qv / a.n) * a.n + qv % a.n;
+    const int64_t idx = q_row(a, layer, h * g + qv / a.n, qv % a.n);
     a.out[idx * kD + tid] = o;
+    if (a.lse && tid == 0) a.lse[idx] = mx + logf(lstar);
     __syncthreads();
   }
 }

@@ -33,7 +33,7 @@ EXPORTED = ["jolt_config_default", "jolt_plan", "jolt_plan_info", "jolt_encode",
             "jolt_stream_info", "jolt_stream_to_host", "jolt_stream_from_host", "jolt_export_debug", "jolt_stream_destroy",
             "jolt_plan_destroy", "jolt_last_error", "jolt_profile_enable", "jolt_profile_report",
             "jolt_launch_count", "jolt_alloc_count", "jolt_selftest_gemm_bf16", "jolt_selftest_gemm_bf16_layout",
-            "jolt_selftest_eig_dense", "jolt_selftest_eig_small", "jolt_attention", "jolt_pages_create",
+            "jolt_selftest_eig_dense", "jolt_selftest_eig_small", "jolt_attention", "jolt_attention_lse", "jolt_pages_create",
             "jolt_pages_status", "jolt_pages_destroy", "jolt_qk_norm_rope", "jolt_paged_append",
             "jolt_paged_attention"]
 
@@ -101,6 +101,7 @@ def _load():
         "jolt_selftest_eig_dense": (st, [i32, i32, i32, vp, vp, vp, vp]),
         "jolt_selftest_eig_small": (st, [i32, i32, vp, vp, vp, i32, vp]),
         "jolt_attention": (st, [vp, vp, i32, i32, ctypes.c_float, vp, vp]),
+        "jolt_attention_lse": (st, [vp, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp]),
         "jolt_pages_create": (st, [ctypes.POINTER(PageShape), vp, vp, vp, ctypes.POINTER(vp)]),
         "jolt_pages_status": (st, [vp, vp]),
         "jolt_pages_destroy": (None, [vp]),
@@ -315,6 +316,14 @@ def jolt_attention(stream: Stream, Q, out, scale: float, cuda_stream=None):
         raise ValueError("Q and out must be [layers][q_heads][n][head_dim] of the same shape")
     _check(_lib.jolt_attention(stream.handle, _dptr(Q), int(Q.shape[1]), int(Q.shape[2]), float(scale), _dptr(out),
                                _stream_ptr(cuda_stream)))
+
+
+def jolt_attention_lse(stream: Stream, layer: int, Q, out, lse, scale: float, cuda_stream=None):
+    """Q: bf16 CUDA tensor [n][q_heads][head_dim] of one layer; out: float32, same shape; lse: float32 [n][q_heads]."""
+    if Q.dim() != 3 or tuple(out.shape) != tuple(Q.shape) or tuple(lse.shape) != tuple(Q.shape[:2]):
+        raise ValueError("Q and out must be [n][q_heads][head_dim] of the same shape and lse [n][q_heads]")
+    _check(_lib.jolt_attention_lse(stream.handle, int(layer), _dptr(Q), int(Q.shape[1]), int(Q.shape[0]), float(scale),
+                                   _dptr(out), _dptr(lse), _stream_ptr(cuda_stream)))
 
 
 # ------------------------------------------------------------------ the growing cache

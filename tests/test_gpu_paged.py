@@ -5,7 +5,7 @@ import math
 
 import pytest
 
-from paged_common import D, Cache, attention_ref, check_attention, freqs, norm_rope_ref
+from paged_common import D, Cache, attention_ref, check_attention, freqs, half_step, norm_rope_ref
 
 pytestmark = pytest.mark.gpu
 SCALE = 1.0 / math.sqrt(D)
@@ -345,6 +345,71 @@ def test_a_run_of_them_together(J):
         J.jolt_paged_attention(pages, batch, q, out, SCALE, lse=L)
         check_attention(c, q, out, L, SCALE, True)
     J.jolt_pages_status(pages)
+
+
+@pytest.mark.parametrize("n", [1, 7])
+def test_compressed_prefix_and_paged_tail(J, n):
+    """A context whose first tokens are a compressed stream and the rest in pages: one layer's attention over
+    both, against softmax over the stream's reconstruction and the pages together, in 64 bits.
+
+    The stream's part is held to 1e-4 of the largest output and 1e-4 in its log-sum-exp as in the tests
+    of jolt_attention (32-bit sums of exact values); what the pages add is within attention_ref's
+    bound. A shift d of the prefix's log-sum-exp moves a row by at most d times twice its largest value."""
+    import numpy as np
+    import torch
+
+    import synth
+    from gpu_common import gpu_encode, host
+    from oracle import attention as oa
+    from oracle import stream as ostream
+    from oracle.jolt import decode_lt
+    from oracle.numerics import rotation_matrix
+    cfg = synth.config(1, layers=3, tokens=300, heads=4, seed=1709, groups=3)
+    K, V = synth.gen_cache_numpy(cfg)
+    _, st, _, _ = gpu_encode(cfg, K, V, synth.bf16_bytes(cfg) // 2, "sketch")
+    layer, hq, tail = 1, 8, 45
+    c = Cache([tail], [n], 4, 16, torch.bfloat16, seed=5)
+    Q = c.randn(n, hq, D, scale=0.7)
+    po = torch.full((n, hq, D), math.nan, device="cuda")
+    pl = torch.full((n, hq), math.nan, device="cuda")
+    out = torch.full((n, hq, D), math.nan, dtype=torch.bfloat16, device="cuda")
+    L = torch.full((n, hq), math.nan, device="cuda")
+    pages, batch = c.handles(J)
+    J.jolt_attention_lse(st, layer, Q, po, pl, SCALE)
+    J.jolt_paged_attention(pages, batch, Q, out, SCALE, lse=L, prefix_out=po, prefix_lse=pl)
+    J.jolt_pages_status(pages)
+    # the same rows as the entry point for all layers gives
+    whole = torch.zeros((3, hq, n, D), dtype=torch.bfloat16, device="cuda")
+    whole[layer] = Q.transpose(0, 1)
+    ow = torch.zeros(whole.shape, device="cuda")
+    J.jolt_attention(st, whole, ow, SCALE)
+    assert torch.equal(ow[layer].transpose(0, 1), po)
+    ost = ostream.parse(J.jolt_stream_to_host(st), lts={2 * layer, 2 * layer + 1})
+    Pi = rotation_matrix(ost.seed, ost.D, ost.rotation)
+    Kh, Vh = (decode_lt(ost, 2 * layer + k, Pi) for k in (0, 1))
+    q = host(Q)
+    for h in range(hq):
+        kv = oa.kv_head_of(h, hq, 4)
+        kt, vt = host(c.rows(0, kv, c.K)), host(c.rows(0, kv, c.V))
+        for i in range(n):
+            see = tail - n + i + 1
+            sp, sq = SCALE * Kh[kv] @ q[i, h], SCALE * kt[:see] @ q[i, h]
+            ref_l = np.log(np.exp(sp).sum())
+            assert abs(float(pl[i, h]) - ref_l) <= 1e-4 * (1 + abs(ref_l))
+            s = np.concatenate([sp, sq])
+            p = np.exp(s - s.max())
+            ref = (p[:, None] * np.concatenate([Vh[kv], vt[:see]])).sum(0) / p.sum()
+            A = (p[:, None] * np.abs(np.concatenate([Vh[kv], vt[:see]]))).sum(0) / p.sum()
+            big = max(np.abs(Vh[kv]).max(), np.abs(vt[:see]).max())
+            u = half_step(torch.bfloat16)
+            tol = u * np.abs(ref) + (u + 2.0 ** -14) * A + (1e-4 + 2e-4) * big + 1e-6
+            got = host(out)[i, h]
+            assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+            assert abs(float(L[i, h]) - (np.log(p.sum()) + s.max())) <= 2e-4 * (1 + abs(ref_l))
+    with pytest.raises(J.JoltError):
+        J.jolt_attention_lse(st, 3, Q, po, pl, SCALE)
+    with pytest.raises(ValueError):
+        J.jolt_attention_lse(st, 0, Q, po, pl[:, :1], SCALE)
 
 
 # ------------------------------------------------------------------ what the device refuses

@@ -55,6 +55,7 @@ def test_null_handles(J, untouched):
     d = J.BatchDesc(1, 1, 1, 1, p, p, p)
     calls = {
         "jolt_pages_status": lambda: L.jolt_pages_status(None, None),
+        "jolt_attention_lse": lambda: L.jolt_attention_lse(None, 0, p, 8, 1, 1.0, p, p, None),
         "jolt_qk_norm_rope": lambda: L.jolt_qk_norm_rope(None, None),
         "jolt_paged_append": lambda: L.jolt_paged_append(None, ctypes.addressof(d), bytes(J._NEW_ROWS.size), None),
         "jolt_paged_attention": lambda: L.jolt_paged_attention(None, ctypes.addressof(d), bytes(J._QUERIES.size), None),

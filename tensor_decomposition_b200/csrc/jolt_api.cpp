@@ -184,34 +184,40 @@ cudaError_t dev_malloc(T** ptr, size_t bytes) {
   return dev_malloc(reinterpret_cast<void**>(ptr), bytes);
 }
 
-cudaError_t pool_malloc(void** ptr, size_t bytes, cudaStream_t s) {
-  g_allocs.fetch_add(1, std::memory_order_relaxed);
+// The current device's pool, made at its first use (which cannot be captured in a CUDA graph); null for
+// a device beyond the table.
+cudaError_t device_pool(cudaMemPool_t* out) {
+  *out = nullptr;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kPoolDevices) return cudaMallocAsync(ptr, bytes, s);
-  cudaMemPool_t pool;
-  {
-    std::lock_guard<std::mutex> g(g_pool_mu);
-    if (!g_pools[dev]) {
-      cudaMemPoolProps props = {};
-      props.allocType = cudaMemAllocationTypePinned;
-      props.location.type = cudaMemLocationTypeDevice;
-      props.location.id = dev;
-      cudaMemPool_t np;
-      e = cudaMemPoolCreate(&np, &props);
-      if (e != cudaSuccess) return e;
-      uint64_t keep = UINT64_MAX;
-      e = cudaMemPoolSetAttribute(np, cudaMemPoolAttrReleaseThreshold, &keep);
-      if (e != cudaSuccess) {
-        cudaMemPoolDestroy(np);
-        return e;
-      }
-      g_pools[dev] = np;
+  if (e != cudaSuccess || dev < 0 || dev >= kPoolDevices) return e;
+  std::lock_guard<std::mutex> g(g_pool_mu);
+  if (!g_pools[dev]) {
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    cudaMemPool_t np;
+    e = cudaMemPoolCreate(&np, &props);
+    if (e != cudaSuccess) return e;
+    uint64_t keep = UINT64_MAX;
+    e = cudaMemPoolSetAttribute(np, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e != cudaSuccess) {
+      cudaMemPoolDestroy(np);
+      return e;
     }
-    pool = g_pools[dev];
+    g_pools[dev] = np;
   }
-  return cudaMallocFromPoolAsync(ptr, bytes, pool, s);
+  *out = g_pools[dev];
+  return cudaSuccess;
+}
+
+cudaError_t pool_malloc(void** ptr, size_t bytes, cudaStream_t s) {
+  g_allocs.fetch_add(1, std::memory_order_relaxed);
+  cudaMemPool_t pool;
+  const cudaError_t e = device_pool(&pool);
+  if (e != cudaSuccess) return e;
+  return pool ? cudaMallocFromPoolAsync(ptr, bytes, pool, s) : cudaMallocAsync(ptr, bytes, s);
 }
 template <typename T>
 cudaError_t pool_malloc(T** ptr, size_t bytes, cudaStream_t s) {
@@ -232,6 +238,10 @@ jolt_status host_fail(jolt_status st, const char* fmt, ...) {
 void host_clear_error() { g_err.clear(); }
 cudaError_t host_pool_malloc(void** ptr, size_t bytes, cudaStream_t s) { return pool_malloc(ptr, bytes, s); }
 cudaError_t host_dev_malloc(void** ptr, size_t bytes) { return dev_malloc(ptr, bytes); }
+cudaError_t host_pool_ready() {
+  cudaMemPool_t pool;
+  return device_pool(&pool);
+}
 void* host_prof_begin(const char* name, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> g(g_prof_mu);

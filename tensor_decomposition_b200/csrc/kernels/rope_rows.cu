@@ -7,9 +7,9 @@
 // to a part of a turn there, since a float32 angle of position 10^5 is off by 10^-2 rad.
 //
 // Each row is read and written once, which bounds the kernel for long inputs (HBM); short inputs
-// are bound by latency. A CTA takes a tile of tokens, about 80 rows, 16 lanes a row (16 bytes each) and
-// up to five rows a lane in flight at once: with one token a CTA the append of 16 rows a token ran at 1.4
-// TB/s, so it runs at 3.8. The tile's sines are computed once (a thread each, while the rows are on their
+// are bound by latency. A CTA takes a tile of tokens, up to 96 rows, 8 lanes a row (two 16-byte runs each) and
+// up to three rows a lane in flight at once: with one token a CTA the append of 16 rows a token ran at 1.4
+// TB/s, so it runs at 4.1. The tile's sines are computed once (a thread each, while the rows are on their
 // way) and used by all heads from shared memory; the append's page lookup is one parallel pass over the
 // batch's offsets instead of a search. (Persistent CTAs with a ring of asynchronous copies, and tiles of
 // two to four times the rows, were 8 to 25 % slower: the issue slots are 70 % busy as it is.)
@@ -24,11 +24,13 @@ namespace {
 using namespace f32x2;
 
 constexpr int kThreads = 256;
-constexpr int kSlots = kThreads / 16;   // rows at a time
-constexpr int kBatch = 5;               // rows a slot keeps in flight
+constexpr int kLanes = 8;               // of a row: 16 features each
+constexpr int kSlots = kThreads / kLanes;   // rows at a time
+constexpr int kBatch = 3;               // rows a slot keeps in flight
+constexpr int kCtas = 4;                // per SM
 constexpr int kMaxTile = 16;            // tokens of a tile
 
-// Four elements of a row, as two pairs.
+// Elements of a row, as pairs.
 __device__ __forceinline__ uint64_t wide(__nv_bfloat16, uint32_t v) {
   const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
   return pair_of(a.x, a.y);
@@ -50,13 +52,15 @@ __device__ __forceinline__ uint32_t narrow(__half, uint64_t p) {
   return *reinterpret_cast<const uint32_t*>(&a);
 }
 template <typename T>
-__device__ __forceinline__ void get4(T, const uint2& v, uint64_t* x) {
+__device__ __forceinline__ void get8(T, const uint4& v, uint64_t* x) {
   x[0] = wide(T(), v.x);
   x[1] = wide(T(), v.y);
+  x[2] = wide(T(), v.z);
+  x[3] = wide(T(), v.w);
 }
 template <typename T>
-__device__ __forceinline__ uint2 put4(T, const uint64_t* x) {
-  return make_uint2(narrow(T(), x[0]), narrow(T(), x[1]));
+__device__ __forceinline__ uint4 put8(T, const uint64_t* x) {
+  return make_uint4(narrow(T(), x[0]), narrow(T(), x[1]), narrow(T(), x[2]), narrow(T(), x[3]));
 }
 
 struct RowsArgs {
@@ -67,25 +71,25 @@ struct RowsArgs {
   int32_t tokens, tile;
 };
 
-// A lane holds two runs of four features of its row, o0 and o1, such that it has both members of
-// four rotated pairs (angles 4 l .. 4 l + 3) or eight features behind the rotated ones.
+// A lane holds two runs of eight features of its row, from o0 and o1 on, such that it has both members
+// of eight rotated pairs (angles 8 l .. 8 l + 7) or sixteen features behind the rotated ones.
 template <typename T, bool kPaged, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a) {
   extern __shared__ __align__(16) float trig[];        // [tile][2][64] cosines and sines of the pairs
   __shared__ __align__(16) float w_s[2][kD];           // norm weights
   __shared__ int64_t dst_s[kMaxTile];                  // append: page row in elements from the pages' base; < 0: none
   __shared__ int pos_s[kMaxTile], seq_s[kMaxTile];     // append: place in the cache, sequence (-1: none)
-  const int tid = threadIdx.x, slot = tid >> 4, l = tid & 15;
+  const int tid = threadIdx.x, slot = tid / kLanes, l = tid % kLanes;
   const int t0 = blockIdx.x * a.tile, nt = min(a.tile, a.tokens - t0);
   const int nA = a.A.heads, nR = a.A.heads + a.B.heads;
   const int step_t = kSlots / nR, step_r = kSlots % nR;
   const bool rot = a.r.inv_freq != nullptr;
   const bool normA = a.A.w != nullptr, normB = !kPaged && a.B.w != nullptr;
   const int h = a.r.rope_dim >> 1;
-  const bool turned = 8 * l < a.r.rope_dim;
-  const int o0 = kInterleaved || !turned ? 8 * l : 4 * l, o1 = kInterleaved || !turned ? 8 * l + 4 : 4 * l + h;
+  const bool turned = 16 * l < a.r.rope_dim;
+  const int o0 = kInterleaved || !turned ? 16 * l : 8 * l, o1 = kInterleaved || !turned ? 16 * l + 8 : 8 * l + h;
 
-  // rows slot, slot + 16, ...: token i of the tile, row r of the token
+  // rows slot, slot + kSlots, ...: token i of the tile, row r of the token
   int i = slot / nR, r = slot - i * nR;
   auto advance = [&](int& ti, int& tr) {
     ti += step_t;
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
       ++ti;
     }
   };
-  uint2 v[kBatch][2] = {};
+  uint4 v[kBatch][2] = {};
   auto load = [&](int ti, int tr) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -103,8 +107,8 @@ __global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
         const int t = t0 + ti;
         const T* src = tr < nA ? reinterpret_cast<const T*>(a.A.p) + (int64_t)t * a.A.ts + (int64_t)tr * a.A.hs
                                : reinterpret_cast<const T*>(a.B.p) + (int64_t)t * a.B.ts + (int64_t)(tr - nA) * a.B.hs;
-        v[k][0] = *reinterpret_cast<const uint2*>(src + o0);
-        v[k][1] = *reinterpret_cast<const uint2*>(src + o1);
+        v[k][0] = *reinterpret_cast<const uint4*>(src + o0);
+        v[k][1] = *reinterpret_cast<const uint4*>(src + o1);
       }
       advance(ti, tr);
     }
@@ -149,66 +153,70 @@ __global__ void __launch_bounds__(kThreads) k_rope_rows(const RowsArgs a) {
   }
   __syncthreads();
 
-  const uint32_t mask = 0xffffu << (tid & 16);   // the 16 lanes of a row, who take part in its sum
+  const uint32_t mask = 0xffu << (tid & 24);   // the lanes of a row, who take part in its sum
   for (;;) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (i >= nt) break;
       const bool isA = r < nA;
-      uint2 y0 = v[k][0], y1 = v[k][1];
+      uint4 y0 = v[k][0], y1 = v[k][1];
       if (!kPaged || isA) {     // values of the append go out as they are
-        uint64_t x[4];          // features o0, + 1; + 2, + 3; o1, + 1; + 2, + 3
-        get4(T(), y0, x);
-        get4(T(), y1, x + 2);
+        uint64_t x[8];          // features o0 .. o0 + 7, o1 .. o1 + 7
+        get8(T(), y0, x);
+        get8(T(), y1, x + 4);
         if (isA ? normA : normB) {
           uint64_t q2 = mul2(x[0], x[0]);
 #pragma unroll
-          for (int e = 1; e < 4; ++e) q2 = fma2(x[e], x[e], q2);
+          for (int e = 1; e < 8; ++e) q2 = fma2(x[e], x[e], q2);
           float q, qb;
           unpair(q2, q, qb);
           q += qb;
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(mask, q, o, 16);
+          for (int o = kLanes / 2; o > 0; o >>= 1) q += __shfl_xor_sync(mask, q, o, kLanes);
           const float f = rsqrtf(fmaf(q, 1.0f / kD, a.r.eps));
           const float* w = w_s[isA ? 0 : 1];
-          const float4 wa = *reinterpret_cast<const float4*>(w + o0), wb = *reinterpret_cast<const float4*>(w + o1);
           const uint64_t f2 = pair_of(f, f);
-          x[0] = mul2(x[0], mul2(f2, pair_of(wa.x, wa.y)));
-          x[1] = mul2(x[1], mul2(f2, pair_of(wa.z, wa.w)));
-          x[2] = mul2(x[2], mul2(f2, pair_of(wb.x, wb.y)));
-          x[3] = mul2(x[3], mul2(f2, pair_of(wb.z, wb.w)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 u = *reinterpret_cast<const float4*>(w + (e < 2 ? o0 : o1) + 4 * (e & 1));
+            x[2 * e] = mul2(x[2 * e], mul2(f2, pair_of(u.x, u.y)));
+            x[2 * e + 1] = mul2(x[2 * e + 1], mul2(f2, pair_of(u.z, u.w)));
+          }
         }
         if (turned) {
-          const float4 c = *reinterpret_cast<const float4*>(trig + i * kD + 4 * l);
-          const float4 s = *reinterpret_cast<const float4*>(trig + i * kD + 64 + 4 * l);
-          if (kInterleaved) {     // (u, v) -> (u, v) c + (-v, u) s
-            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float u, w;
-              unpair(x[e], u, w);
-              x[e] = fma2(pair_of(w, u), pair_of(-sn[e], sn[e]), mul2(x[e], pair_of(cs[e], cs[e])));
-            }
-          } else {
-            const uint64_t c2[2] = {pair_of(c.x, c.y), pair_of(c.z, c.w)}, s2[2] = {pair_of(s.x, s.y), pair_of(s.z, s.w)};
-            const uint64_t n2[2] = {pair_of(-s.x, -s.y), pair_of(-s.z, -s.w)};
+          for (int d = 0; d < 2; ++d) {   // four pairs at a time
+            const float4 c = *reinterpret_cast<const float4*>(trig + i * kD + 8 * l + 4 * d);
+            const float4 s = *reinterpret_cast<const float4*>(trig + i * kD + 64 + 8 * l + 4 * d);
+            if (kInterleaved) {     // (u, v) -> (u, v) c + (-v, u) s
+              const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint64_t u = x[e];
-              x[e] = fma2(x[2 + e], n2[e], mul2(u, c2[e]));
-              x[2 + e] = fma2(u, s2[e], mul2(x[2 + e], c2[e]));
+              for (int e = 0; e < 4; ++e) {
+                float u, w;
+                unpair(x[4 * d + e], u, w);
+                x[4 * d + e] = fma2(pair_of(w, u), pair_of(-sn[e], sn[e]), mul2(x[4 * d + e], pair_of(cs[e], cs[e])));
+              }
+            } else {
+              const uint64_t c2[2] = {pair_of(c.x, c.y), pair_of(c.z, c.w)}, s2[2] = {pair_of(s.x, s.y), pair_of(s.z, s.w)};
+              const uint64_t n2[2] = {pair_of(-s.x, -s.y), pair_of(-s.z, -s.w)};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint64_t u = x[2 * d + e], w = x[4 + 2 * d + e];
+                x[2 * d + e] = fma2(w, n2[e], mul2(u, c2[e]));
+                x[4 + 2 * d + e] = fma2(u, s2[e], mul2(w, c2[e]));
+              }
             }
           }
         }
-        y0 = put4(T(), x);
-        y1 = put4(T(), x + 2);
+        y0 = put8(T(), x);
+        y1 = put8(T(), x + 4);
       }
       if (!kPaged || dst_s[i] >= 0) {
         T* dst = reinterpret_cast<T*>(isA ? a.Ao.p : a.Bo.p) +
                  (kPaged ? dst_s[i] : (int64_t)(t0 + i) * (isA ? a.Ao.ts : a.Bo.ts)) +
                  (int64_t)(isA ? r : r - nA) * (isA ? a.Ao.hs : a.Bo.hs);
-        *reinterpret_cast<uint2*>(dst + o0) = y0;
-        *reinterpret_cast<uint2*>(dst + o1) = y1;
+        *reinterpret_cast<uint4*>(dst + o0) = y0;
+        *reinterpret_cast<uint4*>(dst + o1) = y1;
       }
       advance(i, r);
     }

@@ -120,6 +120,7 @@ jolt_status host_fail(jolt_status st, const char* fmt, ...);
 void host_clear_error();
 cudaError_t host_pool_malloc(void** ptr, size_t bytes, cudaStream_t s);
 cudaError_t host_dev_malloc(void** ptr, size_t bytes);
+cudaError_t host_pool_ready();   // makes the current device's pool, so that captured calls find it
 // Tracing of one phase on a stream: begin returns a token for end (null when tracing is off).
 void* host_prof_begin(const char* name, cudaStream_t s);
 void host_prof_end(void* token);

@@ -206,6 +206,7 @@ JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pag
     return host_fail(JOLT_ERR_CUDA, "jolt_pages_create: tensor map rejected");
   }
   cudaError_t e = cudaGetDevice(&p->device);
+  if (e == cudaSuccess) e = host_pool_ready();
   if (e == cudaSuccess) e = take_slot(p->device, &p->d_status);
   if (e == cudaSuccess) e = cudaMemsetAsync(p->d_status, 0, sizeof(int32_t), (cudaStream_t)cuda_stream);
   if (e != cudaSuccess) {

@@ -511,3 +511,79 @@ def test_binding_refuses(J):
 def test_row_blocks_of_every_fill(J, dtype, n):
     """Chunks whose last block of rows holds one to 256 of them, over one key tile, two, three and many."""
     _attend(J, Cache([n, n + 100, n + 256, n + 5000], [n] * 4, 1, 16, _t(dtype), seed=n), 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("seqs,heads,g,n,kv", [
+    (2, 8, 4, 5, 300),        # 16 items: clusters
+    (3, 8, 4, 8, 700),        # 24 items: shares
+    (40, 2, 16, 2, 90),       # 80 items, few keys: the kernel for many rows
+    (33, 2, 5, 4, 9000),      # 66 items, many keys: shares
+])
+def test_seventeen_to_thirty_two_rows(J, dtype, seqs, heads, g, n, kv):
+    c = Cache([max(n, kv - 7 * s) for s in range(seqs)], [n - s % 2 for s in range(seqs)], heads, 16, _t(dtype), seed=n, pad=3)
+    _attend(J, c, heads * g, max_q=n, prefix=True)
+
+
+@pytest.mark.parametrize("chunk,g", [(1, 2), (3, 12), (9, 8)])
+def test_more_sequences_than_threads(J, chunk, g):
+    """Batches that the kernels' threads have to go over more than once, long and short ones mixed."""
+    import torch
+    kv = [1 + (s * 37) % 150 for s in range(700)]
+    kv[650], kv[3] = 4000, 0
+    c = Cache(kv, [min(chunk, max(1, t)) for t in kv], 1, 16, torch.bfloat16, seed=chunk)
+    _attend(J, c, g, max_q=chunk)
+
+
+def test_one_page_for_two_sequences(J):
+    """Sequences that share pages of a common beginning."""
+    import torch
+    for chunks in ([1, 1], [40, 9]):
+        c = Cache([130, 100], chunks, 2, 16, torch.bfloat16, seed=8)
+        c.table[1, :5] = c.table[0, :5]
+        _attend(J, c, 8)
+
+
+def test_captured_without_a_first_call():
+    """The first calls of a process may be made while a graph is captured."""
+    import subprocess
+    import sys
+    code = """
+import torch, math, sys
+sys.path.insert(0, 'tests')
+from paged_common import Cache, check_attention
+from tensor_decomposition_b200 import jolt as J
+c = Cache([900, 40], [1, 1], 8, 16, torch.bfloat16, seed=1)
+d = Cache([900, 40], [70, 9], 8, 16, torch.bfloat16, seed=1)
+for x in (c, d):
+    Q = x.randn(x.total, 32, 128)
+    out = torch.full((x.total, 32, 128), math.nan, dtype=torch.bfloat16, device='cuda')
+    pages, batch = x.handles(J)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        J.jolt_qk_norm_rope(Q, Q)
+        J.jolt_paged_attention(pages, batch, Q, out, 0.1)
+    g.replay()
+    torch.cuda.synchronize()
+    J.jolt_pages_status(pages)
+    check_attention(x, Q, out, None, 0.1, True)
+print('fine')
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_results_do_not_depend_on_unread_memory(J):
+    """The same call over pages whose unused rows, unused pages and table entries hold other things."""
+    import torch
+    for chunks in ([1, 1, 1], [5, 5, 5], [70, 3, 129]):
+        outs = []
+        for fill in (float("nan"), 0.0, float("inf")):
+            c = Cache([200, 77, 129], chunks, 2, 16, torch.bfloat16, seed=14)
+            c.K[torch.isnan(c.K)] = fill
+            c.V[torch.isnan(c.V)] = fill
+            outs.append(_attend(J, c, 8)[3])
+        assert all(torch.equal(outs[0], o) for o in outs[1:])

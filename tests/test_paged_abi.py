@@ -105,3 +105,13 @@ def test_packed_structs_match_the_header(J):
         got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [J._NORM_ROPE.size - 4, J._NEW_ROWS.size - 4, J._QUERIES.size - 4, ctypes.sizeof(J.BatchDesc),
                    ctypes.sizeof(J.PageShape)]
+
+
+def test_the_codec_has_no_f16(J, untouched):
+    """The type of pages that the codec's caches do not have is refused there."""
+    with pytest.raises(J.JoltError) as e:
+        J.jolt_plan(2, 8, 64, 128, True, J.JOLT_F16, 10 ** 6, 1)
+    assert e.value.status == 1
+    keep, p = _buf()
+    d = ctypes.c_double()
+    assert J._lib.jolt_rel_frob_error(p, p, 16, J.JOLT_F16, None, ctypes.byref(d)) == 1

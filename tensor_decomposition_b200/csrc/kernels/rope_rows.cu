@@ -7,8 +7,8 @@
 // to a part of a turn there, since a float32 angle of position 10^5 is off by 10^-2 rad.
 //
 // Each row is read and written once, which bounds the kernel for long inputs (HBM); short inputs
-// are bound by latency. A CTA takes a tile of tokens, up to 96 rows, 8 lanes a row (two 16-byte runs each) and
-// up to three rows a lane in flight at once: with one token a CTA the append of 16 rows a token ran at 1.4
+// are bound by latency. A CTA takes a tile of tokens, up to 64 rows, 8 lanes a row (two 16-byte runs each) and
+// up to four rows a lane in flight at once: with one token a CTA the append of 16 rows a token ran at 1.4
 // TB/s, so it runs at 4.1. The tile's sines are computed once (a thread each, while the rows are on their
 // way) and used by all heads from shared memory; the append's page lookup is one parallel pass over the
 // batch's offsets instead of a search. (Persistent CTAs with a ring of asynchronous copies, and tiles of
@@ -23,11 +23,11 @@ namespace {
 
 using namespace f32x2;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kLanes = 8;               // of a row: 16 features each
 constexpr int kSlots = kThreads / kLanes;   // rows at a time
-constexpr int kBatch = 3;               // rows a slot keeps in flight
-constexpr int kCtas = 4;                // per SM
+constexpr int kBatch = 4;               // rows a slot keeps in flight
+constexpr int kCtas = 6;                // per SM
 constexpr int kMaxTile = 16;            // tokens of a tile
 
 // Elements of a row, as pairs.
@@ -115,8 +115,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
   };
   load(i, r);
 
+  static_assert(kThreads >= kD, "a thread a weight");
   if (normA && tid < kD) w_s[0][tid] = (float)reinterpret_cast<const T*>(a.A.w)[tid];
-  if (normB && tid >= kD) w_s[1][tid - kD] = (float)reinterpret_cast<const T*>(a.B.w)[tid - kD];
+  if (normB && tid < kD) w_s[1][tid] = (float)reinterpret_cast<const T*>(a.B.w)[tid];
   if (kPaged) {
     if (tid < kMaxTile) seq_s[tid] = -1;
     __syncthreads();

@@ -4,9 +4,9 @@
 // Two matrix products of 128 x 128 x 128 a tile of 128 keys and half block, and one exponential a
 // score: at 4 exponentials a cycle and sub-partition both take about 1000 cycles, so the tensor
 // pipe and the special function unit bound it alike. One persistent CTA an SM walks its share
-// of the units (128 keys of one item). Its warps: two softmax groups of eight, one for each half
-// block (two threads a row, 64 keys each, who agree on the maximum through shared memory: one thread a
-// row took 2350 cycles a tile against 2150, and twice as long to write its output); one that issues the MMAs (tcgen05, 128 x 128 accumulators in Tensor
+// of the units (128 keys of one item). Its warps: two softmax groups of four, one for each half
+// block (a thread a row; two threads a row, who have to agree on the maximum, took 3 to 4 % longer); one
+// that issues the MMAs (tcgen05, 128 x 128 accumulators in Tensor
 // Memory: scores and outputs of both halves fill its 512 columns); one that loads keys and values
 // by TMA, a box of up to 128 rows of a page at a time, into a ring of five 32 KB stages; two that gather
 // the query rows. While one half's scores are turned into weights, the tensor pipe works for the
@@ -31,9 +31,9 @@ constexpr int kBlockRows = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr uint32_t kTileBytes = kHalf * kD * 2;
 constexpr uint32_t kHalfTile = kTileBytes / 2;   // 128 rows x 64 features
-constexpr int kSoftmaxWarps = 16;
+constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
-constexpr int kRegsSoftmax = 104, kRegsOther = 64;   // 512 x 104 + 128 x 64 = the launch's 640 x 96
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;   // 256 x 200 + 128 x 104 = 384 x 168
 constexpr int kSmem = (2 + kStages) * kTileBytes;
 constexpr int kItem = 3;                     // what an item costs besides its tiles, in tiles
 constexpr float kFollow = 8.0f;
@@ -58,7 +58,6 @@ struct Piece {
   int s, h, m, M, t0, t1, T;
   SeqView v;
   int left;         // units of the CTA's share behind the piece
-  int more;         // whether there was one (told to the other warp of a pair)
 };
 // The piece of an item from its unit u on; false if the share ends before the item's first tile.
 __device__ __forceinline__ bool enter(Piece& p, int u, int g, bool causal) {
@@ -86,11 +85,8 @@ __device__ __forceinline__ bool next(Piece& p, const BatchView& b, int g, bool c
   return enter(p, 0, g, causal);
 }
 
-// Barrier of the two warps that share 32 rows.
+// Barrier of the two warps, one of each half, that have the same rows when the halves share an item.
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-
-// And of the four that share them when both halves have the same rows.
-__device__ __forceinline__ void quad_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Whether an item's rows fill one half only: the halves then take its tiles in turn, with the same
 // queries, and their outputs are joined at the end.
@@ -104,14 +100,6 @@ __device__ __forceinline__ bool next_of_warp(Piece& p, const BatchView& b, int g
   more = __shfl_sync(0xffffffffu, more, 0);
   __syncwarp();
   return more;
-}
-
-// The same for the two warps of a barrier.
-__device__ __forceinline__ bool next_of_pair(Piece& p, const BatchView& b, int g, bool causal, int id, bool first) {
-  pair_sync(id);
-  if (first) p.more = next(p, b, g, causal);
-  pair_sync(id);
-  return p.more;
 }
 
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
@@ -164,17 +152,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// The weights 2^(s scale2 + sub) of half a row, rounded to the type, written to Tensor Memory (tP); their
+// The weights 2^(s scale2 + sub) of a row, rounded to the type, written to Tensor Memory (tP); their
 // sum goes to l unrounded. The first half is announced while the second is made. (Making 1 or 2 of 8
 // exponentials by a polynomial on the multiply-add units, to spare the special function unit, gave 0 and
 // -8 % on a chunk of 2048 tokens over 32768 keys.)
 template <typename T>
-__device__ __forceinline__ void weights(const float (&s)[64], float scale2, float sub, float& l, uint32_t tP,
+__device__ __forceinline__ void weights(const float (&s)[kHalf], float scale2, float sub, float& l, uint32_t tP,
                                         uint64_t* lo, uint64_t* hi, int lane) {
   const uint64_t sc = pair_of(scale2, scale2), sb = pair_of(sub, sub);
   uint64_t sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < kHalf / 32; ++c) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -187,10 +175,12 @@ __device__ __forceinline__ void weights(const float (&s)[64], float scale2, floa
       w[i] = pack2(T(), x, y);
     }
     tmem_st16(tP + 16 * c, w);
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(c ? hi : lo);
+    if (c & 1) {
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c == 1 ? lo : hi);
+    }
   }
   float x, y;
   unpair(add2(sum[0], sum[1]), x, y);
@@ -239,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) Bars bar;
   __shared__ uint32_t tmem_s;
   __shared__ int gave_up;
-  __shared__ Piece piece_s[kSoftmaxWarps / 2 + 4];   // places on the line: the softmax pairs', the others'
+  __shared__ Piece piece_s[kSoftmaxWarps + 4];   // each warp's place on the line
   __shared__ bool any_s;
-  __shared__ __align__(8) float both_s[2][2][kHalf];   // what the two threads of a row tell each other
+  __shared__ float2 told_s[kHalf];         // what half 1 tells half 0
   __shared__ int64_t range_s[3];   // the end of this CTA's share, units of a share, shares with one more
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchView& b = a.b;
@@ -280,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = 0; m < M; ++m) n += tiles_of(v, g, m, causal) + kItem;
         return n * b.heads;
       },
-      kItem + 2, reinterpret_cast<int64_t*>(both_s));
+      kItem + 2, reinterpret_cast<int64_t*>(told_s));
   if ((int)blockIdx.x >= st.G) {
     if (tid == 0) ws.list[blockIdx.x].s = -1;
     if (warp == kSoftmaxWarps) tmem_dealloc(tmem_s, 512);
@@ -319,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kSoftmaxWarps) {
       // ---------------------------------------------------------------- MMA issue
       if (elect_one()) {
-        Piece& p = piece_s[kSoftmaxWarps / 2];
+        Piece& p = piece_s[warp];
         constexpr uint32_t id_qk = idesc<T>(), id_pv = idesc<T>() | (1u << 16);   // V: MN-major
         uint32_t kv = 0, queries[2] = {0, 0}, outputs[2] = {0, 0}, tiles[2] = {0, 0};
         bool ok = true;
@@ -339,15 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (first && !wait(&bar.o_empty[t], (outputs[t]++ & 1) ^ 1)) return false;
           tc_fence_after();
           const uint64_t B = desc_mnmajor_sw128(smem_u32(ring + (i % kStages) * kTileBytes), kHalfTile, 1024);
-          // 16 keys a step: the first 32 of each 64 are announced first
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const int k = (n & 1) | ((n & 2) << 1) | ((n & 4) >> 1);   // 0 1 4 5 2 3 6 7
-            if (n == 4) {
+          for (int k = 0; k < 8; ++k) {   // 16 keys a step: the first 64 are announced first
+            if (k == 4) {
               if (!wait(&bar.p_hi[t], tiles[t] & 1)) return false;
               tc_fence_after();
             }
-            umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, B + k * (2048 >> 4), id_pv, !first || n != 0);
+            umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, B + k * (2048 >> 4), id_pv, !first || k != 0);
           }
           ++tiles[t];
           return true;
@@ -414,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kSoftmaxWarps + 1) {
       // ---------------------------------------------------------------- keys and values
-      Piece& p = piece_s[warp - kSoftmaxWarps / 2];
+      Piece& p = piece_s[warp];
       uint32_t kv = 0, tails = 0;
       const int per = kHalf / box;           // boxes of a tile: one lane each
       prefetch_tensormap(&maps.K);
@@ -479,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---------------------------------------------------------------- queries: a warp a half block
-      Piece& p = piece_s[warp - kSoftmaxWarps / 2];
+      Piece& p = piece_s[warp];
       const int t = warp - kSoftmaxWarps - 2, c16 = lane & 15, r2 = lane >> 4;
       const int step_t = 2 / g, step_h = 2 % g;       // from a row to the one two further
       uint32_t pieces = 0;
@@ -515,21 +503,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       } while (next_of_warp(p, b, g, causal, lane));
     }
   } else {
-    // ------------------------------------------------------------------ softmax: two threads a row
+    // ------------------------------------------------------------------ softmax: a thread a row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    Piece& p = piece_s[4 * (warp >> 3) + (warp & 3)];
-    const int t = warp >> 3, side = (warp >> 2) & 1, wq = warp & 3;   // half block, half of the keys (features), rows
-    const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-    const uint32_t tS = tmem + t * kHalf + lanes + 64 * side;
-    const uint32_t tP = tmem + t * kHalf + lanes + 32 * side;
-    const uint32_t tO = tmem + (2 + t) * kHalf + lanes + 64 * side;
-    float* mine = &both_s[t][side][32 * wq + lane];
-    const float* other = &both_s[t][side ^ 1][32 * wq + lane];
+    Piece& p = piece_s[warp];
+    const int t = warp >> 2, wq = warp & 3;     // half block, 32 of its rows
+    const uint32_t tS = tmem + t * kHalf + ((uint32_t)(32 * wq) << 16), tO = tS + 2 * kHalf;
     const bool neg = a.scale < 0.0f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // not 0: a masked score times 0 is no number
     uint32_t tiles = 0, outputs[2] = {0, 0};
-    // A wait that gives up does not end this role: the barriers of a pair need both of its warps, and
-    // the other waits give up at once then. The result is reported as void.
+    // A wait that gives up does not end this role: a pair's barriers need both of its warps, and the other
+    // waits give up at once then. The result is reported as void.
     do {
       const bool alone = solo(p, g), began = p.t0 == 0, ends = p.t1 == p.T;
       const int R = p.v.n * g, r0 = p.m * kBlockRows + (alone ? 0 : t * kHalf);
@@ -555,31 +538,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        float s[64];
+        float s[kHalf];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+        for (int c = 0; c < kHalf / 32; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
         tmem_ld_wait();
         if (neg) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = -s[i];
+          for (int i = 0; i < kHalf; ++i) s[i] = -s[i];
         }
-        const int key0 = j * kHalf + 64 * side;
-        if (key0 + 63 > lim_warp) {
-          const int rel = lim - key0;
+        if (j * kHalf + kHalf - 1 > lim_warp) {
+          const int rel = lim - j * kHalf;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = i > rel ? -INFINITY : s[i];
+          for (int i = 0; i < kHalf; ++i) s[i] = i > rel ? -INFINITY : s[i];
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < 60; i += 8)
+        for (int i = 4; i < kHalf - 4; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
-        const float mh = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-        *mine = mh;
-        pair_sync(1 + 4 * t + wq);   // both have read their scores now: weights may overwrite them
-        const float mn = fmaxf(m, fmaxf(mh, *other) * scale2);
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[kHalf - 4 + k]);
+        const float mn = max3(m, max3(mx[0], mx[1], mx[2]) * scale2, mx[3] * scale2);
         if (j == t0) {
           m = mn;
         } else if (__any_sync(0xffffffffu, r < R && mn - m > kFollow)) {   // lanes behind the rows hold anything
@@ -588,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= f;
           // the scores being complete, so is every earlier product: the output is at rest
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kHalf / 16; ++c) {
             uint32_t o[16];
             tmem_ld16(tO + 16 * c, o);
             tmem_ld_wait();
@@ -598,9 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float sub = m == -INFINITY ? 0.0f : -m;
-        weights<T>(s, scale2, sub, l, tP, &bar.p_lo[t], &bar.p_hi[t], lane);
+        weights<T>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
-      // the products are in (so both warps are done with what they told each other)
+      // the products are in
       const bool used[2] = {true, !alone || p.t1 - p.t0 > 1};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -611,17 +590,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (used[k]) ++outputs[k];
       }
       tc_fence_after();
-      *mine = l;
-      pair_sync(1 + 4 * t + wq);
-      l = side ? *other + l : l + *other;
       float f0 = 1.0f, f1 = 0.0f;                 // weights of the two halves' outputs
       if (alone) {
         // half 1 tells half 0 its maximum and sum and is done; half 0 reads both outputs
-        pair_sync(1 + 4 * t + wq);
-        if (t == 1) *mine = side ? l : m;
-        quad_sync(9 + wq);
+        if (t == 1) told_s[32 * wq + lane] = make_float2(m, l);
+        pair_sync(1 + wq);
         if (t == 0) {
-          const float m1 = both_s[1][0][32 * wq + lane], l1 = both_s[1][1][32 * wq + lane], mn = fmaxf(m, m1);
+          const float m1 = told_s[32 * wq + lane].x, l1 = told_s[32 * wq + lane].y, mn = fmaxf(m, m1);
           if (mn != -INFINITY) {
             f0 = ex2(m - mn);
             f1 = ex2(m1 - mn);
@@ -629,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = mn;
           }
         }
-        quad_sync(9 + wq);
+        pair_sync(1 + wq);
         if (t == 1) continue;
       }
       const bool both = alone && used[1];
@@ -650,17 +625,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 *= inv * il;
         w *= il;
         // Four lanes (four rows) exchange their 16-byte blocks, so that a store writes 64 bytes of a row
-        const int64_t out_row = row * kD + 64 * side + 8 * (lane & 3);
+        const int64_t out_row = row * kD + 8 * (lane & 3);
         const uint32_t live = __ballot_sync(0xffffffffu, r < R);
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kD / 32; ++c) {
           uint32_t y[4][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[16];
             output16(tO + 32 * c + 16 * h, f0, both, f1, v);
             if (w > 0.0f) {
-              const float4* pre = reinterpret_cast<const float4*>(a.pre_out + row * kD + 64 * side + 32 * c + 16 * h);
+              const float4* pre = reinterpret_cast<const float4*>(a.pre_out + row * kD + 32 * c + 16 * h);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float4 x = pre[i];
@@ -682,14 +657,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + at) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
           }
         }
-        if (a.lse && side == 0 && r < R) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (a.lse && r < R) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
       } else {
         // parts: blocks of four features, rows next to one another
         const int64_t slot = (int64_t)blockIdx.x * 2 + (began ? 1 : 0);
         const int row_in = r - p.m * kBlockRows;
-        float4* dst = reinterpret_cast<float4*>(ws.o) + (slot * 32 + 16 * side) * kBlockRows + row_in;
+        float4* dst = reinterpret_cast<float4*>(ws.o) + slot * 32 * kBlockRows + row_in;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kD / 16; ++c) {
           float v[16];
           output16(tO + 16 * c, f0, both, f1, v);
           if (r < R) {
@@ -698,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[(4 * c + i) * kBlockRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (side == 0 && r < R) ws.ml[slot * kBlockRows + row_in] = make_float2(m, l);
+        if (r < R) ws.ml[slot * kBlockRows + row_in] = make_float2(m, l);
       }
       tc_fence_before();
       __syncwarp();
@@ -706,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar.o_empty[t]);
         if (both) mbar_arrive(&bar.o_empty[1]);   // for half 1, which went on
       }
-    } while (next_of_pair(p, b, g, causal, 1 + 4 * t + wq, side == 0 && lane == 0));
+    } while (next_of_warp(p, b, g, causal, lane));
   }
   tc_fence_before();
   __syncthreads();

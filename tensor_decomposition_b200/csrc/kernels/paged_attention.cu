@@ -28,6 +28,9 @@ __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, con
   const int g = a.Hq / a.b.heads, R = sp.rows;
   const int r = blockIdx.y * 4 + rw;
   if ((int)blockIdx.y * 4 >= R) return;
+  const int64_t row = (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g;
+  Prefix pre{};
+  if (r < R && sub == 0) pre = load_prefix(a, row, lane);
   float mx = -INFINITY, ls = 0.0f;
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (r < R) {
@@ -85,14 +88,16 @@ __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, con
       y.w = fmaf(x.w, f, y.w);
     }
   }
-  finish_row<T>(a, (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y, mn, ls);
+  finish_row<T>(a, row, lane, y, mn, ls, pre);
 }
 
 // The same for blocks of 256 rows, whose parts lie in blocks of four features with the rows next to one
-// another: a CTA takes 32 rows, a lane a row and its warp every fourth block of features, and the rows
+// another: a CTA takes 32 rows, a lane a row and its warp every eighth block of features, and the rows
 // come together in shared memory.
+constexpr int kBlockWarps = 8;
 template <typename T>
-__global__ void __launch_bounds__(128) k_attn_combine_blocks(const PagedAttnArgs a, const Workspace ws) {
+__global__ void __launch_bounds__(32 * kBlockWarps) k_attn_combine_blocks(const PagedAttnArgs a, const Workspace ws) {
+  constexpr int kN = 32 / kBlockWarps;   // blocks of features of a warp, and its rows
   __shared__ float4 y_s[32][33];
   grid_wait();
   const Split sp = ws.list[blockIdx.x];
@@ -102,23 +107,31 @@ __global__ void __launch_bounds__(128) k_attn_combine_blocks(const PagedAttnArgs
   if (rb >= R) return;
   const bool in = rb + lane < R;
   const float4* o = reinterpret_cast<const float4*>(ws.o);
+  int64_t row[kN];
+  Prefix pre[kN];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int r = sp.m * 256 + min(rb + warp + kBlockWarps * k, R - 1);
+    row[k] = (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g;
+    pre[k] = load_prefix(a, row[k], lane);
+  }
   float mx = -INFINITY, ls = 0.0f;
-  float4 y[8] = {};
-#pragma unroll 2
+  float4 y[kN] = {};
+#pragma unroll 4
   for (int c = 0; c < parts; ++c) {
     if (!in) break;
     const int64_t slot = (int64_t)(c0 + c) * 2 + (c == 0 ? sp.slot : 0);
     const float2 p = ws.ml[slot * 256 + rb + lane];
-    float4 x[8];
+    float4 x[kN];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = o[(slot * 32 + warp + 4 * k) * 256 + rb + lane];
+    for (int k = 0; k < kN; ++k) x[k] = o[(slot * 32 + warp + kBlockWarps * k) * 256 + rb + lane];
     const float mn = fmaxf(mx, p.x);
     if (mn == -INFINITY) continue;
     const float f0 = ex2(mx - mn), f = ex2(p.x - mn);
     mx = mn;
     ls = fmaf(ls, f0, p.y * f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kN; ++k) {
       y[k].x = fmaf(y[k].x, f0, x[k].x * f);
       y[k].y = fmaf(y[k].y, f0, x[k].y * f);
       y[k].z = fmaf(y[k].z, f0, x[k].z * f);
@@ -126,12 +139,13 @@ __global__ void __launch_bounds__(128) k_attn_combine_blocks(const PagedAttnArgs
     }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y_s[lane][warp + 4 * k] = y[k];
+  for (int k = 0; k < kN; ++k) y_s[lane][warp + kBlockWarps * k] = y[k];
   __syncthreads();
-  for (int i = warp; i < min(32, R - rb); i += 4) {
-    const int r = sp.m * 256 + rb + i;
-    finish_row<T>(a, (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g, lane, y_s[i][lane],
-                  __shfl_sync(0xffffffffu, mx, i), __shfl_sync(0xffffffffu, ls, i));
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int i = warp + kBlockWarps * k;
+    const float m1 = __shfl_sync(0xffffffffu, mx, i), l1 = __shfl_sync(0xffffffffu, ls, i);
+    if (rb + i < R) finish_row<T>(a, row[k], lane, y_s[i][lane], m1, l1, pre[k]);
   }
 }
 
@@ -139,7 +153,7 @@ template <typename T>
 cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid, p.decode ? (p.most + 3) / 4 : (p.most + 31) / 32);
-  cfg.blockDim = dim3(p.decode ? 512 : 128);
+  cfg.blockDim = dim3(p.decode ? 512 : 32 * kBlockWarps);
   cfg.stream = s;
   cudaLaunchAttribute at[1];   // placed while the parts are still computed; waits for them itself
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -129,22 +129,34 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units,
   return r;
 }
 
+// Four features of a row's prefix (lane i: 4 i ..) and its log-sum-exp, in units of log 2; -inf for none.
+// Loaded apart from finish_row, so that the loads run while a row's parts are summed.
+struct Prefix {
+  float4 x;
+  float lse;
+};
+__device__ __forceinline__ Prefix load_prefix(const PagedAttnArgs& a, int64_t row, int lane) {
+  Prefix p{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY};
+  if (a.pre_lse) {
+    p.lse = a.pre_lse[row] * kLog2e;
+    p.x = *reinterpret_cast<const float4*>(a.pre_out + row * kD + 4 * lane);
+  }
+  return p;
+}
+
 // Four output features of one row, from the unscaled sum o, maximum m (units of log 2) and sum l:
 // joined with the prefix, scaled, rounded and stored; lane 0 stores the log-sum-exp.
 template <typename T>
-__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, int64_t row, int lane, float4 o, float m, float l) {
-  if (a.pre_lse) {
-    const float p = a.pre_lse[row] * kLog2e, mx = fmaxf(m, p);
-    if (mx != -INFINITY) {
-      const float4 x = *reinterpret_cast<const float4*>(a.pre_out + row * kD + 4 * lane);
-      const float f = ex2(m - mx), w = ex2(p - mx);
-      l = fmaf(l, f, w);
-      o.x = p == -INFINITY ? o.x * f : fmaf(o.x, f, w * x.x);
-      o.y = p == -INFINITY ? o.y * f : fmaf(o.y, f, w * x.y);
-      o.z = p == -INFINITY ? o.z * f : fmaf(o.z, f, w * x.z);
-      o.w = p == -INFINITY ? o.w * f : fmaf(o.w, f, w * x.w);
-      m = mx;
-    }
+__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, int64_t row, int lane, float4 o, float m, float l,
+                                           const Prefix& p) {
+  if (p.lse != -INFINITY) {
+    const float mx = fmaxf(m, p.lse), f = ex2(m - mx), w = ex2(p.lse - mx);
+    l = fmaf(l, f, w);
+    o.x = fmaf(o.x, f, w * p.x.x);
+    o.y = fmaf(o.y, f, w * p.x.y);
+    o.z = fmaf(o.z, f, w * p.x.z);
+    o.w = fmaf(o.w, f, w * p.x.w);
+    m = mx;
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   T y[4] = {(T)(o.x * inv), (T)(o.y * inv), (T)(o.z * inv), (T)(o.w * inv)};

@@ -579,6 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = m == -INFINITY ? 0.0f : -m;
         weights<T>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
+      const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g + (rc - tok * g);
+      if (a.pre_lse && r < R) {   // what the end needs of the prefix, while the last products are made
+        prefetch_l2(a.pre_out + row * kD, kD * 4);
+      }
       // the products are in
       const bool used[2] = {true, !alone || p.t1 - p.t0 > 1};
 #pragma unroll
@@ -608,7 +612,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t == 1) continue;
       }
       const bool both = alone && used[1];
-      const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g + (rc - tok * g);
       if (began && ends) {
         float inv = 1.0f, w = 0.0f;
         if (a.pre_lse) {
@@ -635,10 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[16];
             output16(tO + 32 * c + 16 * h, f0, both, f1, v);
             if (w > 0.0f) {
-              const float4* pre = reinterpret_cast<const float4*>(a.pre_out + row * kD + 32 * c + 16 * h);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float4 x = pre[i];
+                const float4 x = reinterpret_cast<const float4*>(a.pre_out + row * kD + 32 * c + 16 * h)[i];
                 v[4 * i] = fmaf(w, x.x, v[4 * i]);
                 v[4 * i + 1] = fmaf(w, x.y, v[4 * i + 1]);
                 v[4 * i + 2] = fmaf(w, x.z, v[4 * i + 2]);

@@ -371,6 +371,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
         __syncthreads();
         for (int rr = warp; rr < min(16, R - 16 * t); rr += kSlices) {
           const int r = 16 * t + rr;
+          const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
+          Prefix pre{};
+          if (!kTeam && whole) pre = load_prefix(a, row, lane);
           float mx = -INFINITY, ls = 0.0f;
 #pragma unroll
           for (int w = 0; w < kSlices; ++w) mx = fmaxf(mx, ml_s[w][r].x);
@@ -387,8 +390,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
             *reinterpret_cast<float4*>(sm + kSmem<kT> + r * (4 * kD) + 16 * lane) = y;
             if (lane == 0) team_ml[r] = make_float2(mx, ls);
           } else if (whole) {
-            const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
-            finish_row<T>(a, row, lane, y, mx, ls);
+            finish_row<T>(a, row, lane, y, mx, ls, pre);
           } else {
             const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * ws.rows + r;
             *reinterpret_cast<float4*>(ws.o + at * kD + 4 * lane) = y;
@@ -420,8 +422,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
   // the cluster's parts: CTA k finishes the rows k, k + 8, ..., a warp each
   if (count == 0 && tid < kRows) team_ml[tid] = make_float2(-INFINITY, 0.0f);
   const cooperative_groups::cluster_group team = cooperative_groups::this_cluster();
-  team.sync();
   const int r = blockIdx.x % kTeamCtas + kTeamCtas * warp;
+  const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
+  Prefix pre{};
+  if (r < cc.v.n * g) pre = load_prefix(a, row, lane);
+  team.sync();
   if (r < cc.v.n * g) {
     float2 p[kTeamCtas];
     float4 x[kTeamCtas], y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
       y.z = fmaf(x[c].z, f, y.z);
       y.w = fmaf(x[c].w, f, y.w);
     }
-    finish_row<T>(a, (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g, lane, y, mx, ls);
+    finish_row<T>(a, row, lane, y, mx, ls, pre);
   }
   team.sync();   // no CTA leaves while another reads from it
 }

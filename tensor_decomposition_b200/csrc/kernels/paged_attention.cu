@@ -186,9 +186,9 @@ AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)a.b.max_q * (a.Hq / a.b.heads);
   const int64_t items = (int64_t)a.b.heads * a.b.num_seqs;
   p.decode = rows <= 16 || (rows <= 32 && (items <= kFewItems || tokens >= kFewTokens));
-  p.rows = !p.decode ? 256 : rows <= 16 ? 16 : 32;
+  p.rows = !p.decode ? 256 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   p.most = (int)std::max<int64_t>(1, std::min<int64_t>(rows, p.rows));
-  const int fit = p.rows == 16 ? kTeamItems : kTeamItems / 2;   // two CTAs an SM, or one
+  const int fit = p.rows <= 16 ? kTeamItems : kTeamItems / 2;   // two CTAs an SM, or one
   if (p.decode && items <= fit && (tokens <= kTeamTokens || items >= fit - fit / 8)) {
     p.team = 1;
     p.grid = (int)items * 8;
@@ -197,7 +197,7 @@ AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   const int unit = p.decode ? 64 : 128;
   const int64_t units = std::max<int64_t>(1, (tokens + unit - 1) / unit) * std::max<int64_t>(1, (rows + p.rows - 1) / p.rows) *
                         a.b.heads * a.b.num_seqs;
-  p.grid = (int)std::min<int64_t>((p.rows == 16 ? 3 : p.rows == 32 ? 2 : 1) * (int64_t)sms, units);
+  p.grid = (int)std::min<int64_t>((p.rows <= 16 ? 3 : p.rows == 32 ? 2 : 1) * (int64_t)sms, units);
   p.bytes = o_bytes(p) + ml_bytes(p) + up256(p.grid * sizeof(Split));
   return p;
 }

@@ -15,6 +15,8 @@
 // outputs). A warp for each block on a common ring, with a barrier a unit, ran at half the speed.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "paged_attention.cuh"
 
 namespace jolt {
@@ -29,18 +31,21 @@ constexpr int kTile = kKeys * kD * 2;     // bytes of a slice's keys (or values)
 constexpr int kMinUnits = 1;
 constexpr int kTeamCtas = 8;
 constexpr int kThreads = 32 * kSlices;
-// kT: blocks of 16 query rows. CTAs per SM and stages of a ring: what registers and shared memory allow.
+// kT: blocks of 16 query rows, 0 for up to 8 rows. CTAs per SM and stages of a ring: what registers and
+// shared memory allow.
 template <int kT>
-constexpr int kCtas = kT == 1 ? 3 : 2;
+constexpr int kCtas = kT <= 1 ? 3 : 2;
 template <int kT>
-constexpr int kStages = kT == 1 ? 2 : 3;
+constexpr int kStages = kT <= 1 ? 2 : 3;
+template <int kT>
+constexpr int kRowsOf = kT == 0 ? 8 : 16 * kT;
 // Shared memory: the rings, the queries (kT = 2), a team's part.
 template <int kT>
 constexpr int kRing = kSlices * kStages<kT> * 2 * kTile;
 template <int kT>
 constexpr int kSmem = kRing<kT> + (kT > 1 ? 16 * kT * kD * 2 : 0);
 template <int kT>
-constexpr int kTeamSmem = kSmem<kT> + 16 * kT * kD * 4;
+constexpr int kTeamSmem = kSmem<kT> + kRowsOf<kT> * kD * 4;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -103,12 +108,300 @@ __device__ __forceinline__ void advance(Cursor& c, const BatchView& b) {
   } while (c.U == 0);
 }
 
+// What one warp holds of an item, for blocks of 16 rows: queries as A fragments (read from shared memory
+// each time for two blocks), outputs, running maxima (in units of log 2) and sums; lane: rows quad and
+// quad + 8 of a block.
+template <typename T, int kT>
+struct Blocks16 {
+  static constexpr int blocks = kT, per = 16, rows = 16 * kT;
+  uint32_t q[8][4];
+  float o[kT][16][4], m[kT][2], l[kT][2];
+  int lim[kT][2];
+
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const SeqView& v, int h, int g, uint8_t* qs, int tid) {
+    const int lane = tid & 31, quad = lane >> 2, pair = lane & 3, R = v.n * g;
+    const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)v.q0 * a.q_ts + (int64_t)h * g * a.q_hs;
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = 16 * t + quad + 8 * k;
+        const int tok = r / g;
+        lim[t][k] = r < R ? (a.causal ? v.len - v.n + tok : v.len - 1) : -1;
+        if (kT == 1) {
+          const T* p = Q + (int64_t)tok * a.q_ts + (int64_t)(r % g) * a.q_hs + 2 * pair;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            q[j][k] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j) : 0u;
+            q[j][k + 2] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j + 8) : 0u;
+          }
+        }
+        m[t][k] = -INFINITY;
+        l[t][k] = 0.0f;
+      }
+    if (kT > 1) {   // no warp reads the queries before: the last item's end was a barrier
+      for (int u = tid; u < rows * 16; u += kThreads) {
+        const int r = u >> 4, c = u & 15, tok = r / g;
+        const uint4 x = r < R ? *reinterpret_cast<const uint4*>(Q + (int64_t)tok * a.q_ts + (int64_t)(r - tok * g) * a.q_hs + 8 * c)
+                              : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(qs + r * (2 * kD) + ((c ^ (r & 7)) << 4)) = x;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][j][e] = 0.0f;
+  }
+
+  // A unit's 16 keys: scores of 16 rows x 16 keys, weights, weighted values.
+  __device__ __forceinline__ void unit(uint32_t Ks, uint32_t Vs, uint32_t Qs, int key0, bool edge, float scale2, int lane) {
+    const int pair = lane & 3;
+      // scores of 16 rows x 16 keys: matrices (keys 0-7, 8-15) x (features 0-7, 8-15) of each k-step
+      float s[kT][2][4] = {};
+      const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = (lane >> 3) & 1, vrow = lane & 15, vcol = lane >> 4;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t k4[4];
+        ldsm4(Ks + (j >> 2) * (kTile / 2) + mrow * 128 + (((2 * (j & 3) + mcol) ^ (mrow & 7)) << 4), k4);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          if (kT > 1) ldsm4(Qs + (16 * t + vrow) * (2 * kD) + (((2 * j + vcol) ^ (vrow & 7)) << 4), q[j]);
+          mma(T(), s[t][0], q[j], k4[0], k4[1]);
+          mma(T(), s[t][1], q[j], k4[2], k4[3]);
+        }
+      }
+      // running softmax in units of log 2; lane: rows quad and quad + 8, keys 2 pair, + 1 of each block of 8
+      uint32_t hi[kT][4], lo[kT][4];
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        float mn[2] = {m[t][0], m[t][1]};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = s[t][n][e] * scale2;
+            if (edge && key0 + 8 * n + 2 * pair + (e & 1) > lim[t][e >> 1]) x = -INFINITY;
+            s[t][n][e] = x;
+            mn[e >> 1] = fmaxf(mn[e >> 1], x);
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 1));
+          mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 2));
+        }
+        if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1])) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float f = mn[k] == -INFINITY ? 1.0f : ex2(m[t][k] - mn[k]);
+            m[t][k] = mn[k];
+            l[t][k] *= f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              o[t][j][2 * k] *= f;
+              o[t][j][2 * k + 1] *= f;
+            }
+          }
+        }
+        const float sub[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0], m[t][1] == -INFINITY ? 0.0f : m[t][1]};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[t][n][e] = ex2(s[t][n][e] - sub[e >> 1]);
+            l[t][e >> 1] += s[t][n][e];
+          }
+        split2(T(), s[t][0][0], s[t][0][1], hi[t][0], lo[t][0]);
+        split2(T(), s[t][0][2], s[t][0][3], hi[t][1], lo[t][1]);
+        split2(T(), s[t][1][0], s[t][1][1], hi[t][2], lo[t][2]);
+        split2(T(), s[t][1][2], s[t][1][3], hi[t][3], lo[t][3]);
+      }
+      // weighted values: matrices (keys 0-7, 8-15) x (8 features), transposed
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t v4[4];
+        ldsm4t(Vs + (j >> 2) * (kTile / 2) + vrow * 128 + (((2 * (j & 3) + vcol) ^ (vrow & 7)) << 4), v4);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          mma(T(), o[t][2 * j], hi[t], v4[0], v4[1]);
+          mma(T(), o[t][2 * j + 1], hi[t], v4[2], v4[3]);
+        }
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          mma(T(), o[t][2 * j], lo[t], v4[0], v4[1]);
+          mma(T(), o[t][2 * j + 1], lo[t], v4[2], v4[3]);
+        }
+      }
+  }
+
+  __device__ __forceinline__ void sums(float2* ml, int lane) {
+    const int quad = lane >> 2, pair = lane & 3;
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 1);
+        l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 2);
+        if (pair == 0) ml[16 * t + quad + 8 * k] = make_float2(m[t][k], l[t][k]);
+      }
+  }
+  // Block t's outputs relative to the maxima over all warps (ml), rows of 128 floats, 16-byte blocks
+  // swizzled by the row.
+  template <class ML>
+  __device__ __forceinline__ void put(int t, float* so, const ML& ml, int lane) {
+    const int quad = lane >> 2, pair = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = quad + 8 * k;
+      float mx = ml[0][16 * t + r].x;
+#pragma unroll
+      for (int w = 1; w < kSlices; ++w) mx = fmaxf(mx, ml[w][16 * t + r].x);
+      const float f = mx == -INFINITY ? 0.0f : ex2(m[t][k] - mx);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int blk = (2 * j + (pair >> 1)) ^ ((r & 7) << 1);
+        *reinterpret_cast<float2*>(so + r * kD + 4 * blk + 2 * (pair & 1)) =
+            make_float2(o[t][j][2 * k] * f, o[t][j][2 * k + 1] * f);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The same for up to 8 rows, with the products turned: keys (and features) are the 16 rows of an MMA and
+// the queries its 8 columns, so half the MMAs do. Lane: queries 2 pair and 2 pair + 1; of the scores
+// keys quad and quad + 8, of the output features quad and quad + 8 of each 16.
+template <typename T>
+struct Block8 {
+  static constexpr int blocks = 1, per = 8;
+  uint32_t q[8][2];
+  float o[8][4], m[2], l[2];
+  int lim[2];
+
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const SeqView& v, int h, int g, uint8_t*, int tid) {
+    const int lane = tid & 31, quad = lane >> 2, pair = lane & 3, R = v.n * g;
+    const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)v.q0 * a.q_ts + (int64_t)h * g * a.q_hs;
+    const T* p = Q + (int64_t)(quad / g) * a.q_ts + (int64_t)(quad % g) * a.q_hs + 2 * pair;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      q[j][0] = quad < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j) : 0u;
+      q[j][1] = quad < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j + 8) : 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * pair + e;
+      lim[e] = r < R ? (a.causal ? v.len - v.n + r / g : v.len - 1) : -1;
+      m[e] = -INFINITY;
+      l[e] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+  }
+
+  __device__ __forceinline__ void unit(uint32_t Ks, uint32_t Vs, uint32_t, int key0, bool edge, float scale2, int lane) {
+    const int quad = lane >> 2;
+    const int arow = lane & 15, acol = lane >> 4, trow = (lane & 7) + ((lane >> 4) << 3), tcol = (lane >> 3) & 1;
+    float sa[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t k4[4];
+      ldsm4(Ks + (j >> 2) * (kTile / 2) + arow * 128 + (((2 * (j & 3) + acol) ^ (arow & 7)) << 4), k4);
+      mma(T(), sa[j & 1], k4, q[j][0], q[j][1]);
+    }
+    float s[4], mn[2] = {m[0], m[1]};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x = (sa[0][e] + sa[1][e]) * scale2;
+      if (edge && key0 + quad + 8 * (e >> 1) > lim[e & 1]) x = -INFINITY;
+      s[e] = x;
+      mn[e & 1] = fmaxf(mn[e & 1], x);
+    }
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], w));
+    if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = mn[e] == -INFINITY ? 1.0f : ex2(m[e] - mn[e]);
+        m[e] = mn[e];
+        l[e] *= f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j][e] *= f;
+          o[j][2 + e] *= f;
+        }
+      }
+    }
+    const float sub[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[e] = ex2(s[e] - sub[e & 1]);
+      l[e & 1] += s[e];
+    }
+    uint32_t hi[2], lo[2];
+    split2(T(), s[0], s[1], hi[0], lo[0]);
+    split2(T(), s[2], s[3], hi[1], lo[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {   // keys x queries to queries x keys
+      hi[k] = turn8x8(hi[k]);
+      lo[k] = turn8x8(lo[k]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t v4[4];
+      ldsm4t(Vs + (j >> 2) * (kTile / 2) + trow * 128 + (((2 * (j & 3) + tcol) ^ (trow & 7)) << 4), v4);
+      mma(T(), o[j], v4, hi[0], hi[1]);
+      mma(T(), o[j], v4, lo[0], lo[1]);
+    }
+  }
+
+  __device__ __forceinline__ void sums(float2* ml, int lane) {
+    const int quad = lane >> 2, pair = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], w);
+      if (quad == 0) ml[2 * pair + e] = make_float2(m[e], l[e]);
+    }
+  }
+  template <class ML>
+  __device__ __forceinline__ void put(int, float* so, const ML& ml, int lane) {
+    const int quad = lane >> 2, pair = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * pair + e;
+      float mx = ml[0][r].x;
+#pragma unroll
+      for (int w = 1; w < kSlices; ++w) mx = fmaxf(mx, ml[w][r].x);
+      const float f = mx == -INFINITY ? 0.0f : ex2(m[e] - mx);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int d = 16 * j + 8 * k + quad;
+          so[r * kD + 4 * ((d >> 2) ^ (r << 1)) + (d & 3)] = o[j][2 * k + e] * f;
+        }
+    }
+  }
+};
+
 // kTeam: instead of a share of the line a CTA takes an eighth of the item of its cluster, and the cluster's
 // CTAs combine through one another's shared memory: one launch and no scratch.
 template <typename T, int kT, bool kTeam>
 __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     k_attn_decode(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws) {
-  constexpr int kRows = 16 * kT, kDeep = kStages<kT>;
+  using Held = std::conditional_t<kT == 0, Block8<T>, Blocks16<T, kT == 0 ? 1 : kT>>;
+  constexpr int kRows = kRowsOf<kT>, kDeep = kStages<kT>;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ __align__(8) uint64_t full_s[kSlices][kStages<kT>];
   __shared__ int valid_s[kSlices][kStages<kT>];      // rows of a stage that hold keys
@@ -116,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
   __shared__ float2 ml_s[kSlices][kRows];
   __shared__ float2 team_ml[kTeam ? kRows : 1];
   __shared__ int64_t scan_s[kSlices + 3];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, pair = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchView& b = a.b;
   const int g = a.Hq / b.heads;
   const float scale2 = a.scale * kLog2e;
@@ -193,9 +486,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
 #pragma unroll
   for (int i = 0; i < kDeep - 1; ++i) issue(i);
 
-  uint32_t q[8][4];          // queries, A fragments: of the item (kT = 1) or of the block at work
-  float o[kT][16][4], m[kT][2], l[kT][2];
-  int lim[kT][2];
+  Held held;
   bool fresh = true;         // the next unit begins an item (or this CTA's part of one)
   bool began = cc.u == 0;    // the current item began in this CTA's range
   Split split;
@@ -208,41 +499,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     issue((i + kDeep - 1) % kDeep);
     if (fresh) {
       fresh = false;
-      const int R = cc.v.n * g;
-      const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)cc.v.q0 * a.q_ts + (int64_t)cc.h * g * a.q_hs;
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = 16 * t + quad + 8 * k;
-          const int tok = r / g;
-          lim[t][k] = r < R ? (a.causal ? cc.v.len - cc.v.n + tok : cc.v.len - 1) : -1;
-          if (kT == 1) {
-            const T* p = Q + (int64_t)tok * a.q_ts + (int64_t)(r % g) * a.q_hs + 2 * pair;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              q[j][k] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j) : 0u;
-              q[j][k + 2] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j + 8) : 0u;
-            }
-          }
-          m[t][k] = -INFINITY;
-          l[t][k] = 0.0f;
-        }
-      if (kT > 1) {   // no warp reads the queries before: the last item's end was a barrier
-        for (int u = tid; u < kRows * 16; u += kThreads) {
-          const int r = u >> 4, c = u & 15, tok = r / g;
-          const uint4 x = r < R ? *reinterpret_cast<const uint4*>(Q + (int64_t)tok * a.q_ts + (int64_t)(r - tok * g) * a.q_hs + 8 * c)
-                                : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sm + kRing<kT> + r * (2 * kD) + ((c ^ (r & 7)) << 4)) = x;
-        }
-        __syncthreads();
-      }
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[t][j][e] = 0.0f;
+      held.begin(a, cc.v, cc.h, g, sm + kRing<kT>, tid);
     }
     const uint32_t Ks = smem_u32(ring + stage * 2 * kTile), Vs = Ks + kTile;
     const int key0 = cc.u * kUnit + warp * kKeys;
@@ -258,119 +515,24 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
         fence_async_shared();   // before the stage's next copy
         __syncwarp();
       }
-      // scores of 16 rows x 16 keys: matrices (keys 0-7, 8-15) x (features 0-7, 8-15) of each k-step
-      float s[kT][2][4] = {};
-      const int mrow = (lane & 7) + ((lane >> 4) << 3), mcol = (lane >> 3) & 1, vrow = lane & 15, vcol = lane >> 4;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t k4[4];
-        ldsm4(Ks + (j >> 2) * (kTile / 2) + mrow * 128 + (((2 * (j & 3) + mcol) ^ (mrow & 7)) << 4), k4);
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          if (kT > 1) ldsm4(smem_u32(sm + kRing<kT>) + (16 * t + vrow) * (2 * kD) + (((2 * j + vcol) ^ (vrow & 7)) << 4), q[j]);
-          mma(T(), s[t][0], q[j], k4[0], k4[1]);
-          mma(T(), s[t][1], q[j], k4[2], k4[3]);
-        }
-      }
-      // running softmax in units of log 2; lane: rows quad and quad + 8, keys 2 pair, + 1 of each block of 8
       const bool edge = key0 + kKeys - 1 > (a.causal ? cc.v.len - cc.v.n : cc.v.len - 1) || cc.v.n * g < kRows;
-      uint32_t hi[kT][4], lo[kT][4];
-#pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        float mn[2] = {m[t][0], m[t][1]};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = s[t][n][e] * scale2;
-            if (edge && key0 + 8 * n + 2 * pair + (e & 1) > lim[t][e >> 1]) x = -INFINITY;
-            s[t][n][e] = x;
-            mn[e >> 1] = fmaxf(mn[e >> 1], x);
-          }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 1));
-          mn[k] = fmaxf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 2));
-        }
-        if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1])) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float f = mn[k] == -INFINITY ? 1.0f : ex2(m[t][k] - mn[k]);
-            m[t][k] = mn[k];
-            l[t][k] *= f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              o[t][j][2 * k] *= f;
-              o[t][j][2 * k + 1] *= f;
-            }
-          }
-        }
-        const float sub[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0], m[t][1] == -INFINITY ? 0.0f : m[t][1]};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[t][n][e] = ex2(s[t][n][e] - sub[e >> 1]);
-            l[t][e >> 1] += s[t][n][e];
-          }
-        split2(T(), s[t][0][0], s[t][0][1], hi[t][0], lo[t][0]);
-        split2(T(), s[t][0][2], s[t][0][3], hi[t][1], lo[t][1]);
-        split2(T(), s[t][1][0], s[t][1][1], hi[t][2], lo[t][2]);
-        split2(T(), s[t][1][2], s[t][1][3], hi[t][3], lo[t][3]);
-      }
-      // weighted values: matrices (keys 0-7, 8-15) x (8 features), transposed
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t v4[4];
-        ldsm4t(Vs + (j >> 2) * (kTile / 2) + vrow * 128 + (((2 * (j & 3) + vcol) ^ (vrow & 7)) << 4), v4);
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          mma(T(), o[t][2 * j], hi[t], v4[0], v4[1]);
-          mma(T(), o[t][2 * j + 1], hi[t], v4[2], v4[3]);
-        }
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          mma(T(), o[t][2 * j], lo[t], v4[0], v4[1]);
-          mma(T(), o[t][2 * j + 1], lo[t], v4[2], v4[3]);
-        }
-      }
+      held.unit(Ks, Vs, smem_u32(sm + kRing<kT>), key0, edge, scale2, lane);
     }
     const bool ends = cc.u + 1 == cc.U;
     if (ends || i + 1 == count) {
       // join the four warps: maxima and sums first, then the outputs, a block of rows at a time, each warp's
-      // in its own stage that was just read (rows of 128 floats; 16-byte blocks swizzled by the row)
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 1);
-          l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 2);
-          if (pair == 0) ml_s[warp][16 * t + quad + 8 * k] = make_float2(m[t][k], l[t][k]);
-        }
+      // in its own stage that was just read
+      held.sums(ml_s[warp], lane);
       const int R = cc.v.n * g;
       const bool whole = ends && began;
       const int slot = began ? 1 : 0;
 #pragma unroll
-      for (int t = 0; t < kT; ++t) {
+      for (int t = 0; t < Held::blocks; ++t) {
         __syncthreads();
-        float* so = reinterpret_cast<float*>(ring + stage * 2 * kTile);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = quad + 8 * k;
-          float mx = ml_s[0][16 * t + r].x;
-#pragma unroll
-          for (int w = 1; w < kSlices; ++w) mx = fmaxf(mx, ml_s[w][16 * t + r].x);
-          const float f = mx == -INFINITY ? 0.0f : ex2(m[t][k] - mx);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int blk = (2 * j + (pair >> 1)) ^ ((r & 7) << 1);
-            *reinterpret_cast<float2*>(so + r * kD + 4 * blk + 2 * (pair & 1)) =
-                make_float2(o[t][j][2 * k] * f, o[t][j][2 * k + 1] * f);
-          }
-        }
+        held.put(t, reinterpret_cast<float*>(ring + stage * 2 * kTile), ml_s, lane);
         __syncthreads();
-        for (int rr = warp; rr < min(16, R - 16 * t); rr += kSlices) {
-          const int r = 16 * t + rr;
+        for (int rr = warp; rr < min(Held::per, R - Held::per * t); rr += kSlices) {
+          const int r = Held::per * t + rr;
           const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
           Prefix pre{};
           if (!kTeam && whole) pre = load_prefix(a, row, lane);
@@ -488,8 +650,10 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
 }  // namespace
 
 cudaError_t attn_decode(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s) {
-  if (p.rows == 16) return a.dtype == JOLT_BF16 ? launch<__nv_bfloat16, 1>(a, p, w, s) : launch<__half, 1>(a, p, w, s);
-  return a.dtype == JOLT_BF16 ? launch<__nv_bfloat16, 2>(a, p, w, s) : launch<__half, 2>(a, p, w, s);
+  const bool b = a.dtype == JOLT_BF16;
+  if (p.rows == 8) return b ? launch<__nv_bfloat16, 0>(a, p, w, s) : launch<__half, 0>(a, p, w, s);
+  if (p.rows == 16) return b ? launch<__nv_bfloat16, 1>(a, p, w, s) : launch<__half, 1>(a, p, w, s);
+  return b ? launch<__nv_bfloat16, 2>(a, p, w, s) : launch<__half, 2>(a, p, w, s);
 }
 
 }  // namespace jolt

@@ -20,6 +20,7 @@ template <typename T>
 __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, const Workspace ws) {
   __shared__ float4 y_s[4][kSubs][32];
   __shared__ float2 ml_s[4][kSubs];
+  grid_release();
   grid_wait();
   const Split sp = ws.list[blockIdx.x];
   if (sp.s < 0) return;
@@ -99,6 +100,7 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kBlockWarps) k_attn_combine_blocks(const PagedAttnArgs a, const Workspace ws) {
   constexpr int kN = 32 / kBlockWarps;   // blocks of features of a warp, and its rows
   __shared__ float4 y_s[32][33];
+  grid_release();
   grid_wait();
   const Split sp = ws.list[blockIdx.x];
   if (sp.s < 0) return;
@@ -151,19 +153,8 @@ __global__ void __launch_bounds__(32 * kBlockWarps) k_attn_combine_blocks(const 
 
 template <typename T>
 cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, p.decode ? (p.most + 3) / 4 : (p.most + 31) / 32);
-  cfg.blockDim = dim3(p.decode ? 512 : 32 * kBlockWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];   // placed while the parts are still computed; waits for them itself
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, p.decode ? k_attn_combine<T> : k_attn_combine_blocks<T>, a, w);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
+  if (p.decode) return launch_early(k_attn_combine<T>, dim3(p.grid, (p.most + 3) / 4), dim3(512), 0, 1, s, a, w);
+  return launch_early(k_attn_combine_blocks<T>, dim3(p.grid, (p.most + 31) / 32), dim3(32 * kBlockWarps), 0, 1, s, a, w);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

@@ -201,11 +201,6 @@ struct Waits {
   }
 };
 
-// Wait for the kernels before this one in the stream (a launch that was let start early).
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Let the next kernel of the stream be placed now; it waits for this one's end by itself.
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 }  // namespace pattn
 
 // The two kernels.

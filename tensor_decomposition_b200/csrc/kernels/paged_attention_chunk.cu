@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&tmem_s, 512);
     tmem_relinquish();
   }
+  grid_wait();
   const Start st = find_start<kThreads>(
       b.num_seqs,
       [&](int s) {
@@ -701,9 +702,7 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
   static SmemFlags allowed;
   cudaError_t e = allow_smem(k_attn_chunk<T>, kSmem, a.device, allowed);
   if (e != cudaSuccess) return e;
-  k_attn_chunk<T><<<p.grid, kThreads, kSmem, s>>>(a, maps, w, box);
-  note_launch();
-  return cudaGetLastError();
+  return launch_early(k_attn_chunk<T>, dim3(p.grid), dim3(kThreads), kSmem, 1, s, a, maps, w, box);
 }
 
 }  // namespace

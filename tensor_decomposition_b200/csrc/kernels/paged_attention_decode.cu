@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
   const BatchView& b = a.b;
   const int g = a.Hq / b.heads;
   const float scale2 = a.scale * kLog2e;
+  grid_release();
   if (tid < kSlices * kDeep) mbar_init(&full_s[0][0] + tid, 1);
   if (tid == 0) {
     gave_up = 0;
@@ -420,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     prefetch_tensormap(&maps.K);
     prefetch_tensormap(&maps.V);
   }
+  grid_wait();
   Start st{};
   Cursor lc;
   if (kTeam) {
@@ -433,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     st.hi = (int64_t)(rank + 1) * lc.U / kTeamCtas;
     lc.u = (int)st.lo;
   } else {
-    grid_release();
     st = find_start<kThreads>(
         b.num_seqs, [&](int s) { return (int64_t)units_of(seq_view(b, s)) * b.heads; }, kMinUnits, scan_s);
     if ((int)blockIdx.x >= st.G) {
@@ -625,26 +626,11 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
   if (p.team) {
     e = allow_smem(k_attn_decode<T, kT, true>, kTeamSmem<kT>, a.device, allowed_team);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kTeamSmem<kT>;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kTeamCtas;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_attn_decode<T, kT, true>, a, maps, w);
-  } else {
-    e = allow_smem(k_attn_decode<T, kT, false>, kSmem<kT>, a.device, allowed);
-    if (e != cudaSuccess) return e;
-    k_attn_decode<T, kT, false><<<p.grid, kThreads, kSmem<kT>, s>>>(a, maps, w);
+    return launch_early(k_attn_decode<T, kT, true>, dim3(p.grid), dim3(kThreads), kTeamSmem<kT>, kTeamCtas, s, a, maps, w);
   }
+  e = allow_smem(k_attn_decode<T, kT, false>, kSmem<kT>, a.device, allowed);
   if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
+  return launch_early(k_attn_decode<T, kT, false>, dim3(p.grid), dim3(kThreads), kSmem<kT>, 1, s, a, maps, w);
 }
 
 }  // namespace

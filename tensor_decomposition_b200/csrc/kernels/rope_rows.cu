@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
   __shared__ __align__(16) float w_s[2][kD];           // norm weights
   __shared__ int64_t dst_s[kMaxTile];                  // append: page row in elements from the pages' base; < 0: none
   __shared__ int pos_s[kMaxTile], seq_s[kMaxTile];     // append: place in the cache, sequence (-1: none)
+  grid_release();
+  grid_wait();
   const int tid = threadIdx.x, slot = tid / kLanes, l = tid % kLanes;
   const int t0 = blockIdx.x * a.tile, nt = min(a.tile, a.tokens - t0);
   const int nA = a.A.heads, nR = a.A.heads + a.B.heads;
@@ -238,9 +240,7 @@ cudaError_t launch(jolt_dtype t, int tokens, RowsArgs a, int sms, cudaStream_t s
   const int grid = (tokens + a.tile - 1) / a.tile, bytes = a.tile * kD * (int)sizeof(float);
   auto kernel = t == JOLT_BF16 ? (a.r.interleaved ? k_rope_rows<__nv_bfloat16, kPaged, true> : k_rope_rows<__nv_bfloat16, kPaged, false>)
                                : (a.r.interleaved ? k_rope_rows<__half, kPaged, true> : k_rope_rows<__half, kPaged, false>);
-  kernel<<<grid, kThreads, bytes, s>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_early(kernel, dim3(grid), dim3(kThreads), bytes, 1, s, a);
 }
 
 }  // namespace

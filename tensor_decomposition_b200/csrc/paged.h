@@ -6,6 +6,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <utility>
 
 #include "jolt_internal.h"
 
@@ -68,6 +69,35 @@ inline cudaError_t allow_smem(K* kernel, int bytes, int device, SmemFlags& done)
   if (e == cudaSuccess) done.on[device].store(true, std::memory_order_release);
   return e;
 }
+
+// Launches that may be placed before the kernel ahead of them in the stream has ended, where that one allows
+// it: the kernel itself waits for it (grid_wait) before it touches memory, and lets the one behind it be
+// placed (grid_release) at its start. What goes before the wait, and the launch, overlaps.
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s,
+                                A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
 
 // Rows of 128 elements of a tensor [tokens][heads][128]; element strides.
 struct RowsIn {

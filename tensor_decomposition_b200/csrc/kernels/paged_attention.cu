@@ -52,14 +52,13 @@ __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, con
       float mn = mx;
 #pragma unroll
       for (int i = 0; i < 8; ++i) mn = fmaxf(mn, p[i].x);
-      if (mn == -INFINITY) continue;
-      const float f0 = ex2(mx - mn);
+      const float f0 = rescale(mx, mn);
       mx = mn;
       ls *= f0;
       y.x *= f0; y.y *= f0; y.z *= f0; y.w *= f0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float f = ex2(p[i].x - mn);
+        const float f = rescale(p[i].x, mn);
         ls = fmaf(p[i].y, f, ls);
         y.x = fmaf(x[i].x, f, y.x);
         y.y = fmaf(x[i].y, f, y.y);
@@ -77,17 +76,15 @@ __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, con
   for (int i = 1; i < kSubs; ++i) mn = fmaxf(mn, ml_s[rw][i].x);
   y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   ls = 0.0f;
-  if (mn != -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < kSubs; ++i) {
-      const float f = ex2(ml_s[rw][i].x - mn);
-      const float4 x = y_s[rw][i][lane];
-      ls = fmaf(ml_s[rw][i].y, f, ls);
-      y.x = fmaf(x.x, f, y.x);
-      y.y = fmaf(x.y, f, y.y);
-      y.z = fmaf(x.z, f, y.z);
-      y.w = fmaf(x.w, f, y.w);
-    }
+  for (int i = 0; i < kSubs; ++i) {
+    const float f = rescale(ml_s[rw][i].x, mn);
+    const float4 x = y_s[rw][i][lane];
+    ls = fmaf(ml_s[rw][i].y, f, ls);
+    y.x = fmaf(x.x, f, y.x);
+    y.y = fmaf(x.y, f, y.y);
+    y.z = fmaf(x.z, f, y.z);
+    y.w = fmaf(x.w, f, y.w);
   }
   finish_row<T>(a, row, lane, y, mn, ls, pre);
 }
@@ -128,8 +125,7 @@ __global__ void __launch_bounds__(32 * kBlockWarps) k_attn_combine_blocks(const 
 #pragma unroll
     for (int k = 0; k < kN; ++k) x[k] = o[(slot * 32 + warp + kBlockWarps * k) * 256 + rb + lane];
     const float mn = fmaxf(mx, p.x);
-    if (mn == -INFINITY) continue;
-    const float f0 = ex2(mx - mn), f = ex2(p.x - mn);
+    const float f0 = rescale(mx, mn), f = rescale(p.x, mn);
     mx = mn;
     ls = fmaf(ls, f0, p.y * f);
 #pragma unroll

@@ -135,6 +135,14 @@ struct Prefix {
   float4 x;
   float lse;
 };
+// 1 / l and the log-sum-exp of a row of maximum m (units of log 2) and sum l; 0 and -inf without keys (l is
+// 1 at least where there are any, or no number).
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+// What weights of maximum m are scaled by to be relative to mx >= m: 0 where there are none, as ex2(-inf) is. A
+// row whose scores are no numbers has m = -inf and l = NaN, which 0 keeps.
+__device__ __forceinline__ float rescale(float m, float mx) { return mx == -INFINITY ? 0.0f : ex2(m - mx); }
+
 __device__ __forceinline__ Prefix load_prefix(const PagedAttnArgs& a, int64_t row, int lane) {
   Prefix p{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY};
   if (a.pre_lse) {
@@ -150,7 +158,7 @@ template <typename T>
 __device__ __forceinline__ void finish_row(const PagedAttnArgs& a, int64_t row, int lane, float4 o, float m, float l,
                                            const Prefix& p) {
   if (p.lse != -INFINITY) {
-    const float mx = fmaxf(m, p.lse), f = ex2(m - mx), w = ex2(p.lse - mx);
+    const float mx = fmaxf(m, p.lse), f = rescale(m, mx), w = ex2(p.lse - mx);
     l = fmaf(l, f, w);
     o.x = fmaf(o.x, f, w * p.x.x);
     o.y = fmaf(o.y, f, w * p.x.y);
@@ -158,10 +166,10 @@ __device__ __forceinline__ void finish_row(const PagedAttnArgs& a, int64_t row, 
     o.w = fmaf(o.w, f, w * p.x.w);
     m = mx;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = inverse_sum(l);
   T y[4] = {(T)(o.x * inv), (T)(o.y * inv), (T)(o.z * inv), (T)(o.w * inv)};
   *reinterpret_cast<uint2*>(reinterpret_cast<T*>(a.out) + row * kD + 4 * lane) = *reinterpret_cast<const uint2*>(y);
-  if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (a.lse && lane == 0) a.lse[row] = log_sum(m, l);
 }
 
 // Tensor maps of the pages.

@@ -602,12 +602,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         pair_sync(1 + wq);
         if (t == 0) {
           const float m1 = told_s[32 * wq + lane].x, l1 = told_s[32 * wq + lane].y, mn = fmaxf(m, m1);
-          if (mn != -INFINITY) {
-            f0 = ex2(m - mn);
-            f1 = ex2(m1 - mn);
-            l = l * f0 + l1 * f1;
-            m = mn;
-          }
+          f0 = rescale(m, mn);
+          f1 = rescale(m1, mn);
+          l = l * f0 + l1 * f1;
+          m = mn;
         }
         pair_sync(1 + wq);
         if (t == 1) continue;
@@ -617,14 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float inv = 1.0f, w = 0.0f;
         if (a.pre_lse) {
           const float pl = a.pre_lse[row] * kLog2e, mn = fmaxf(m, pl);
-          if (mn != -INFINITY) {
-            inv = ex2(m - mn);
-            w = ex2(pl - mn);
-            l = fmaf(l, inv, w);
-            m = mn;
-          }
+          inv = rescale(m, mn);
+          w = rescale(pl, mn);
+          l = fmaf(l, inv, w);
+          m = mn;
         }
-        const float il = l > 0.0f ? 1.0f / l : 0.0f;
+        const float il = inverse_sum(l);
         f0 *= inv * il;
         f1 *= inv * il;
         w *= il;
@@ -638,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             float v[16];
             output16(tO + 32 * c + 16 * h, f0, both, f1, v);
-            if (w > 0.0f) {
+            if (a.pre_lse && w != 0.0f) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float4 x = reinterpret_cast<const float4*>(a.pre_out + row * kD + 32 * c + 16 * h)[i];
@@ -660,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + at) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
           }
         }
-        if (a.lse && r < R) a.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (a.lse && r < R) a.lse[row] = log_sum(m, l);
       } else {
         // parts: blocks of four features, rows next to one another
         const int64_t slot = (int64_t)blockIdx.x * 2 + (began ? 1 : 0);

@@ -258,7 +258,7 @@ struct Blocks16 {
       float mx = ml[0][16 * t + r].x;
 #pragma unroll
       for (int w = 1; w < kSlices; ++w) mx = fmaxf(mx, ml[w][16 * t + r].x);
-      const float f = mx == -INFINITY ? 0.0f : ex2(m[t][k] - mx);
+      const float f = rescale(m[t][k], mx);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int blk = (2 * j + (pair >> 1)) ^ ((r & 7) << 1);
@@ -383,7 +383,7 @@ struct Block8 {
       float mx = ml[0][r].x;
 #pragma unroll
       for (int w = 1; w < kSlices; ++w) mx = fmaxf(mx, ml[w][r].x);
-      const float f = mx == -INFINITY ? 0.0f : ex2(m[e] - mx);
+      const float f = rescale(m[e], mx);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
 #pragma unroll
           for (int w = 0; w < kSlices; ++w) {
             const float2 p = ml_s[w][r];
-            ls += mx == -INFINITY ? 0.0f : p.y * ex2(p.x - mx);
+            ls = fmaf(p.y, rescale(p.x, mx), ls);
             const float4 x = *reinterpret_cast<const float4*>(
                 reinterpret_cast<const float*>(sm + (w * kDeep + stage) * 2 * kTile) + rr * kD + 4 * (lane ^ ((rr & 7) << 1)));
             y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
@@ -603,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     for (int c = 0; c < kTeamCtas; ++c) mx = fmaxf(mx, p[c].x);
 #pragma unroll
     for (int c = 0; c < kTeamCtas; ++c) {
-      if (p[c].x == -INFINITY) continue;   // no keys, and perhaps no output written
-      const float f = ex2(p[c].x - mx);
+      if (p[c].y == 0.0f) continue;   // no keys, and perhaps no output written
+      const float f = rescale(p[c].x, mx);
       ls = fmaf(p[c].y, f, ls);
       y.x = fmaf(x[c].x, f, y.x);
       y.y = fmaf(x[c].y, f, y.y);

@@ -587,3 +587,34 @@ def test_results_do_not_depend_on_unread_memory(J):
             c.V[torch.isnan(c.V)] = fill
             outs.append(_attend(J, c, 8)[3])
         assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+@pytest.mark.parametrize("kv,chunks,heads,g", [
+    ([300, 40], [1, 1], 2, 4),               # clusters
+    ([30000, 40], [1, 1], 2, 4),             # up to 8 rows, items in many shares
+    ([30000, 40], [3, 2], 2, 4),             # up to 16
+    ([30000, 40], [7, 2], 2, 4),             # up to 32
+    ([30000, 40], [30, 20], 2, 4),           # a chunk of half a block, in many shares
+    ([30000, 140], [100, 140], 2, 4),        # whole blocks, in many shares
+    ([256] * 80, [256] * 80, 2, 2),          # many more blocks than CTAs
+])
+def test_queries_that_are_no_numbers(J, kv, chunks, heads, g, prefix):
+    """Such a row's output and log-sum-exp are none either, however its keys are divided; the other rows'
+    are as they should be."""
+    import torch
+    c = Cache(kv, chunks, heads, 16, torch.bfloat16, seed=5)
+    pages, batch, Q, good, L0 = _attend(J, c, heads * g)
+    po = pl = None
+    if prefix:
+        po, pl = c.randn(c.total, heads * g, D, dtype=torch.float32), c.randn(c.total, heads * g, dtype=torch.float32)
+    rows, hd = [0, c.total // 2, c.total - 1], [0, 3, heads * g - 1]
+    bad = Q.clone()
+    bad[rows, hd, 77] = math.nan
+    out, L = torch.zeros_like(good), torch.zeros_like(L0)
+    J.jolt_paged_attention(pages, batch, bad, out, SCALE, lse=L, prefix_out=po, prefix_lse=pl)
+    J.jolt_pages_status(pages)
+    assert torch.isnan(out[rows, hd].float()).all() and torch.isnan(L[rows, hd]).all()
+    J.jolt_paged_attention(pages, batch, Q, good, SCALE, lse=L0, prefix_out=po, prefix_lse=pl)
+    out[rows, hd], L[rows, hd] = good[rows, hd], L0[rows, hd]
+    check_attention(c, Q, out, L, SCALE, True, po, pl)

@@ -225,7 +225,7 @@ JOLT_API jolt_status jolt_attention_lse(jolt_stream_t stream, int32_t layer, con
  * followed (its keys count as zeros in attention and are not written by append). Entries behind
  * the pages of kv_len tokens are not read and may hold anything, and so may the rows of the last
  * page behind kv_len; the rows before kv_len have to be finite.
- * Supported: head_dim 128, page_size a multiple of 16, BF16 and F16.
+ * Supported: head_dim 128, page_size a multiple of 16 below 2^24, BF16 and F16.
  */
 typedef struct jolt_pages_s* jolt_pages_t;
 
@@ -247,7 +247,8 @@ typedef struct {
 /*
  * jolt_pages_create - describe a page set to the library. K_pages, V_pages: device, 16-byte
  *   aligned. The device that is current becomes the set's; calls on it need that device current.
- *   Not to be captured. Errors: INVALID_ARG, OOM, CUDA, UNSUPPORTED (dtype, page_size).
+ *   Synchronises `cuda_stream`; not to be captured. Errors: INVALID_ARG, OOM, CUDA, UNSUPPORTED
+ *   (dtype, page_size).
  */
 JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pages, void* V_pages,
                                        void* cuda_stream, jolt_pages_t* out);

@@ -170,7 +170,7 @@ constexpr int kFewItems = 64, kFewTokens = 8192;
 constexpr int kTeamTokens = 4096, kTeamItems = 32;
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   AttnPlan p;
-  const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)a.b.max_q * (a.Hq / a.b.heads);
+  const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)std::min(a.b.max_q, a.b.total_q) * (a.Hq / a.b.heads);
   const int64_t items = (int64_t)a.b.heads * a.b.num_seqs;
   p.decode = rows <= 16 || (rows <= 32 && (items <= kFewItems || tokens >= kFewTokens));
   p.rows = !p.decode ? 256 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
@@ -182,9 +182,9 @@ AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
     return p;
   }
   const int unit = p.decode ? 64 : 128;
-  const int64_t units = std::max<int64_t>(1, (tokens + unit - 1) / unit) * std::max<int64_t>(1, (rows + p.rows - 1) / p.rows) *
-                        a.b.heads * a.b.num_seqs;
-  p.grid = (int)std::min<int64_t>((p.rows <= 16 ? 3 : p.rows == 32 ? 2 : 1) * (int64_t)sms, units);
+  const int64_t per_item = std::max<int64_t>(1, (tokens + unit - 1) / unit) * std::max<int64_t>(1, (rows + p.rows - 1) / p.rows);
+  const int64_t most = (p.rows <= 16 ? 3 : p.rows == 32 ? 2 : 1) * (int64_t)sms;
+  p.grid = (int)std::min(most, std::min(most, per_item) * items);
   p.bytes = o_bytes(p) + ml_bytes(p) + up256(p.grid * sizeof(Split));
   return p;
 }

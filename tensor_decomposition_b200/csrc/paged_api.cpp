@@ -1,4 +1,5 @@
 // Host side of the growing cache (include/jolt.h): page sets, argument checks and launches.
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <new>
@@ -125,6 +126,8 @@ jolt_status check_batch(const char* what, const jolt_pages_s* pg, const jolt_bat
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: null q_start, kv_len or page_table", what);
   if ((int64_t)b->max_pages * pg->shape.page_size > INT32_MAX - 1024)
     return host_fail(JOLT_ERR_UNSUPPORTED, "%s: page tables of more than 2^31 tokens", what);
+  if ((int64_t)b->num_seqs * pg->shape.heads > INT32_MAX)
+    return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 sequences times heads", what);
   return JOLT_OK;
 }
 
@@ -180,8 +183,8 @@ JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pag
     return host_fail(JOLT_ERR_INVALID_ARG, "jolt_pages_create: head_dim %d unsupported (supported: 128)", sh.head_dim);
   if (sh.dtype != JOLT_BF16 && sh.dtype != JOLT_F16)
     return host_fail(JOLT_ERR_UNSUPPORTED, "jolt_pages_create: pages are bf16 or f16");
-  if (sh.page_size % 16 || sh.page_size > (1 << 24))
-    return host_fail(JOLT_ERR_UNSUPPORTED, "jolt_pages_create: page_size %d is not a multiple of 16 up to 2^24",
+  if (sh.page_size % 16 || sh.page_size >= (1 << 24))   // a head's stride fits 32 bits
+    return host_fail(JOLT_ERR_UNSUPPORTED, "jolt_pages_create: page_size %d is not a multiple of 16 below 2^24",
                      sh.page_size);
   if ((int64_t)sh.heads * sh.page_size * (2 * kD) >= (1ll << 40))
     return host_fail(JOLT_ERR_UNSUPPORTED, "jolt_pages_create: a page of 2^40 bytes or more");
@@ -209,6 +212,7 @@ JOLT_API jolt_status jolt_pages_create(const jolt_page_shape* shape, void* K_pag
   if (e == cudaSuccess) e = host_pool_ready();
   if (e == cudaSuccess) e = take_slot(p->device, &p->d_status);
   if (e == cudaSuccess) e = cudaMemsetAsync(p->d_status, 0, sizeof(int32_t), (cudaStream_t)cuda_stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)cuda_stream);   // the set is used on any stream
   if (e != cudaSuccess) {
     if (p->d_status) give_slot(p->device, p->d_status);
     delete p;
@@ -324,6 +328,12 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   if (!q.out) return host_fail(JOLT_ERR_INVALID_ARG, "%s: null out", what);
   if (!aligned16(q.out) || !aligned16(q.prefix_out))
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: out and prefix_out must be 16-byte aligned", what);
+  // a KV head's blocks of rows times tiles of keys are counted in 32 bits
+  const int64_t tokens = (int64_t)batch->max_pages * pages->shape.page_size;
+  const int64_t rows = (int64_t)std::min(batch->max_q, batch->total_q) * (q.q_heads / pages->shape.heads);
+  if ((rows / 256 + 1) * (tokens / 128 + 4) > INT32_MAX)
+    return host_fail(JOLT_ERR_UNSUPPORTED, "%s: chunks of %d tokens over page tables of %lld tokens", what,
+                     (int)std::min(batch->max_q, batch->total_q), (long long)tokens);
   st = check_device(what, pages);
   if (st != JOLT_OK) return st;
   PagedAttnArgs a{};

@@ -618,3 +618,24 @@ def test_queries_that_are_no_numbers(J, kv, chunks, heads, g, prefix):
     J.jolt_paged_attention(pages, batch, Q, good, SCALE, lse=L0, prefix_out=po, prefix_lse=pl)
     out[rows, hd], L[rows, hd] = good[rows, hd], L0[rows, hd]
     check_attention(c, Q, out, L, SCALE, True, po, pl)
+
+
+def test_sizes_that_pass_32_bits(J):
+    """max_q bounds the chunks from above, however far; what the kernels could not count is refused."""
+    import ctypes
+    import torch
+    _attend(J, Cache([900, 40], [1, 1], 2, 16, torch.bfloat16, seed=2), 8, max_q=2 ** 31 - 1)
+    c = Cache([900, 400], [300, 9], 2, 16, torch.bfloat16, seed=2)
+    pages, batch, Q, out, _ = _attend(J, c, 8, max_q=2 ** 31 - 1)
+
+    def call(num_seqs, total, max_q, max_pages):
+        d = J.BatchDesc(num_seqs, total, max_q, max_pages, *(x.data_ptr() for x in (c.q_start, c.kv_len, c.table)))
+        q = J._QUERIES.pack(Q.data_ptr(), 8 * D, D, 0, 0, out.data_ptr(), 0, 8, 1, SCALE)
+        return J._lib.jolt_paged_attention(pages.handle, ctypes.addressof(d), q, None)
+
+    before = J.jolt_launch_count()
+    assert call(2, 309, 309, 1 << 27) == 9              # a table of 2^31 tokens
+    assert call(1 << 30, 309, 309, 57) == 9             # 2^31 items
+    assert call(2, 1 << 23, 1 << 23, 1 << 22) == 9      # 2^17 blocks of rows by 2^19 tiles of keys
+    assert call(2, 1 << 28, 1, 57) == 9                 # 2^31 query rows
+    assert J.jolt_launch_count() == before

@@ -115,3 +115,10 @@ def test_the_codec_has_no_f16(J, untouched):
     keep, p = _buf()
     d = ctypes.c_double()
     assert J._lib.jolt_rel_frob_error(p, p, 16, J.JOLT_F16, None, ctypes.byref(d)) == 1
+
+
+def test_pages_whose_head_stride_is_beyond_32_bits(J, untouched):
+    keep, p = _buf()
+    h = ctypes.c_void_p()
+    sh = J.PageShape(1, 1, 1 << 24, 128, 0)
+    assert J._lib.jolt_pages_create(ctypes.byref(sh), p, p, None, ctypes.byref(h)) == 9 and not h.value

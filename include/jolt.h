@@ -224,7 +224,8 @@ JOLT_API jolt_status jolt_attention_lse(jolt_stream_t stream, int32_t layer, con
  * outside [0, max_pages * page_size]) is skipped, a table entry that is no page of the set is never
  * followed (its keys count as zeros in attention and are not written by append). Entries behind
  * the pages of kv_len tokens are not read and may hold anything, and so may the rows of the last
- * page behind kv_len; the rows before kv_len have to be finite.
+ * page behind kv_len. A key or value that is no finite number shows in the rows that see it alone
+ * (a value in its feature, as an infinity or NaN).
  * Supported: head_dim 128, page_size a multiple of 16 below 2^24, BF16 and F16.
  */
 typedef struct jolt_pages_s* jolt_pages_t;

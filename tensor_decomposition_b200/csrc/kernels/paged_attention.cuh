@@ -172,6 +172,66 @@ __device__ __forceinline__ void finish_row(const PagedAttnArgs& a, int64_t row, 
   if (a.lse && lane == 0) a.lse[row] = log_sum(m, l);
 }
 
+// Values that some rows of a block see and others do not (causal) may be no numbers, which a weight of zero
+// does not hide in a matrix product. A warp looks for them in a tile in shared memory (two halves of 128-byte
+// rows, `half` apart) and zeroes them there; the rows that see them look them up in the pages at the end
+// (hidden16) and show NaN in their features. x 0 + sum is 0 until an x is no finite number.
+__device__ __forceinline__ uint32_t times_0(__nv_bfloat16, uint32_t x, uint32_t sum) {
+  const __nv_bfloat162 y = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(0.0f, 0.0f),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&sum));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t times_0(__half, uint32_t x, uint32_t sum) {
+  const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(0.0f, 0.0f),
+                            *reinterpret_cast<const __half2*>(&sum));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ constexpr uint32_t exponent(__nv_bfloat16) { return 0x7f80; }
+__device__ __forceinline__ constexpr uint32_t exponent(__half) { return 0x7c00; }
+// Whether all is finite in rows ra .. rb - 1 of the tile.
+template <typename T, int kAhead>
+__device__ __forceinline__ bool finite(const uint8_t* tile, uint32_t half, int ra, int rb, int lane) {
+  uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll kAhead
+  for (int u = 2 * ra + (lane >> 3); u < 2 * rb; u += 4) {   // a half row each
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + (u & 1) * half + (u >> 1) * 128 + (lane & 7) * 16);
+    sum[0] = times_0(T(), v.x, sum[0]);
+    sum[1] = times_0(T(), v.y, sum[1]);
+    sum[2] = times_0(T(), v.z, sum[2]);
+    sum[3] = times_0(T(), v.w, sum[3]);
+  }
+  return !__any_sync(0xffffffffu, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0);
+}
+// Zeroes in them what is not.
+template <typename T>
+__device__ __forceinline__ void hide(uint8_t* tile, uint32_t half, int ra, int rb, int lane) {
+  const uint32_t e = exponent(T());
+#pragma unroll 1
+  for (int u = 64 * ra + lane; u < 64 * rb; u += 32) {   // two elements each
+    uint32_t* w = reinterpret_cast<uint32_t*>(tile + ((u >> 5) & 1) * half + (u >> 6) * 128) + (u & 31);
+    uint32_t x = *w;
+    if ((x & e) == e) x &= 0xffff0000u;
+    if (((x >> 16) & e) == e) x &= 0xffffu;
+    *w = x;
+  }
+}
+// Which of the features d0 .. d0 + 15 of the keys from .. to of a sequence are no finite numbers.
+template <typename T>
+__device__ __forceinline__ uint32_t hidden16(const PagedAttnArgs& a, int s, int h, int from, int to, int d0) {
+  uint32_t found = 0;
+#pragma unroll 1
+  for (int key = max(from, 0); key <= to; ++key) {
+    const int page = page_of(a.b, s, key);
+    if (page < 0) continue;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(a.V) +
+                        (((int64_t)page * a.b.heads + h) * a.b.page_size + key % a.b.page_size) * kD + d0;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if ((v[i] & exponent(T())) == exponent(T())) found |= 1u << i;
+  }
+  return found;
+}
+
 // Tensor maps of the pages.
 struct Maps {
   CUtensorMap K, V;

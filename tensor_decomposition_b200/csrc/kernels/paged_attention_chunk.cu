@@ -222,6 +222,26 @@ __device__ __forceinline__ void output16(uint32_t t0, float f0, bool both, float
   }
 }
 
+// Rare, so kept out of the kernel's code: what one warp does to hide values, and to show NaN where a row of
+// the piece that sees the keys up to lim sees one: in out (blocks of one feature) or a part (blocks of four).
+template <typename T>
+__device__ __noinline__ void hide_values(uint8_t* tile, int ra, int rb, bool* hid) {
+  hide<T>(tile, kHalfTile, ra, rb, threadIdx.x & 31);
+  *hid = true;
+}
+template <typename T>
+__device__ __noinline__ void show_values(const PagedAttnArgs& a, const Piece& p, int lim, T* out, float* part) {
+  const int g = a.Hq / a.b.heads;
+  for (int d0 = 0; d0 < kD; d0 += 16) {
+    const uint32_t found = hidden16<T>(a, p.s, p.h, p.v.len - p.v.n + p.m * kBlockRows / g + 1, lim, d0);
+    for (int d = d0; d < d0 + 16; ++d) {
+      if (!((found >> (d - d0)) & 1)) continue;
+      if (out) out[d] = (T)NAN;
+      else part[(d >> 2) * (4 * kBlockRows) + (d & 3)] = NAN;
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_chunk(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws, int box) {
@@ -231,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int gave_up;
   __shared__ Piece piece_s[kSoftmaxWarps + 4];   // each warp's place on the line
   __shared__ bool any_s;
+  __shared__ bool hid_s[8];                // whether a piece's values hold what was hidden: the last pieces'
   __shared__ float2 told_s[kHalf];         // what half 1 tells half 0
   __shared__ int64_t range_s[3];   // the end of this CTA's share, units of a share, shares with one more
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -404,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kSoftmaxWarps + 1) {
       // ---------------------------------------------------------------- keys and values
       Piece& p = piece_s[warp];
-      uint32_t kv = 0, tails = 0;
+      uint32_t kv = 0, tails = 0, pieces = 0;
       const int per = kHalf / box;           // boxes of a tile: one lane each
       prefetch_tensormap(&maps.K);
       prefetch_tensormap(&maps.V);
@@ -412,6 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       do {
         const int t0 = p.t0, nt = p.t1 - t0, len = p.v.len, h = p.h, seq = p.s;
         const bool alone = solo(p, g);
+        const int seen = causal ? len - p.v.n + p.m * kBlockRows / g : len - 1;   // the last key that all rows see
+        // (the ring holds the tiles of three pieces at most, and the softmax is at most two behind those)
+        bool* hid = &hid_s[pieces++ & 7];
+        if (lane == 0) *hid = false;
         for (int x = 0; x < 2 * nt && ok; ++x, ++kv) {
             // K0 V0 K1 V1 ..., or as the halves take them in turn K0 K1 V0 K2 V1 K3 ... V(nt - 2) V(nt - 1)
             int kind = x & 1, j = x >> 1;
@@ -433,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A tile with rows that hold no keys: values there are zeroed, since a weight of zero
             // does not hide what lies in the page (keys are hidden by the mask on their scores);
             // rows of a bad page are zeroed for both. Such a tile lands on a barrier of its own first.
-            const bool fix = !whole || (kind == 1 && ends);
+            const bool some = kind == 1 && min((j + 1) * kHalf, len) - 1 > seen;   // values that not all rows see
+            const bool fix = !whole || (kind == 1 && ends) || some;
             uint64_t* fb = fix ? &bar.tail : &bar.kv_full[s];
             uint8_t* dst = ring + s * kTileBytes;
             if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(good) * box * kD * 2);
@@ -455,6 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *reinterpret_cast<uint4*>(dst + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
                   *reinterpret_cast<uint4*>(dst + kHalfTile + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
                 }
+              }
+              if (some) {
+                const int from = max(0, seen + 1 - j * kHalf), to = min(kHalf, len - j * kHalf);
+                if (!finite<T, 2>(dst, kHalfTile, from, to, lane)) hide_values<T>(dst, from, to, hid);
               }
               fence_async_shared();
               __syncwarp();
@@ -511,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + t * kHalf + ((uint32_t)(32 * wq) << 16), tO = tS + 2 * kHalf;
     const bool neg = a.scale < 0.0f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // not 0: a masked score times 0 is no number
-    uint32_t tiles = 0, outputs[2] = {0, 0};
+    uint32_t tiles = 0, outputs[2] = {0, 0}, pieces = 0;
     // A wait that gives up does not end this role: a pair's barriers need both of its warps, and the other
     // waits give up at once then. The result is reported as void.
     do {
@@ -595,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (used[k]) ++outputs[k];
       }
       tc_fence_after();
+      const bool hid = *(volatile bool*)&hid_s[pieces++ & 7];
       float f0 = 1.0f, f1 = 0.0f;                 // weights of the two halves' outputs
       if (alone) {
         // half 1 tells half 0 its maximum and sum and is done; half 0 reads both outputs
@@ -657,6 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (a.lse && r < R) a.lse[row] = log_sum(m, l);
+        if (hid) {
+          __syncwarp();   // other lanes stored the row
+          if (r < R) show_values<T>(a, p, lim, reinterpret_cast<T*>(a.out) + row * kD, nullptr);
+        }
       } else {
         // parts: blocks of four features, rows next to one another
         const int64_t slot = (int64_t)blockIdx.x * 2 + (began ? 1 : 0);
@@ -673,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (r < R) ws.ml[slot * kBlockRows + row_in] = make_float2(m, l);
+        if (hid && r < R) show_values<T>(a, p, lim, nullptr, reinterpret_cast<float*>(dst));
       }
       tc_fence_before();
       __syncwarp();

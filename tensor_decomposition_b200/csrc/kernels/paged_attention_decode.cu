@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
   __shared__ __align__(8) uint64_t full_s[kSlices][kStages<kT>];
   __shared__ int valid_s[kSlices][kStages<kT>];      // rows of a stage that hold keys
   __shared__ int gave_up;
+  __shared__ bool hid_s[kSlices];                    // whether the item's values hold what was hidden
   __shared__ float2 ml_s[kSlices][kRows];
   __shared__ float2 team_ml[kTeam ? kRows : 1];
   __shared__ int64_t scan_s[kSlices + 3];
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     issue((i + kDeep - 1) % kDeep);
     if (fresh) {
       fresh = false;
+      if (lane == 0) hid_s[warp] = false;
       held.begin(a, cc.v, cc.h, g, sm + kRing<kT>, tid);
     }
     const uint32_t Ks = smem_u32(ring + stage * 2 * kTile), Vs = Ks + kTile;
@@ -515,6 +517,17 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
         }
         fence_async_shared();   // before the stage's next copy
         __syncwarp();
+      }
+      const int seen = cc.v.len - cc.v.n;   // the last key that all rows see
+      if (a.causal && key0 + valid - 1 > seen) {
+        uint8_t* values = ring + stage * 2 * kTile + kTile;
+        const int from = max(0, seen + 1 - key0);
+        if (!finite<T, 1>(values, kTile / 2, from, valid, lane)) {
+          hide<T>(values, kTile / 2, from, valid, lane);
+          if (lane == 0) hid_s[warp] = true;
+          fence_async_shared();
+          __syncwarp();
+        }
       }
       const bool edge = key0 + kKeys - 1 > (a.causal ? cc.v.len - cc.v.n : cc.v.len - 1) || cc.v.n * g < kRows;
       held.unit(Ks, Vs, smem_u32(sm + kRing<kT>), key0, edge, scale2, lane);
@@ -548,6 +561,14 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
             const float4 x = *reinterpret_cast<const float4*>(
                 reinterpret_cast<const float*>(sm + (w * kDeep + stage) * 2 * kTile) + rr * kD + 4 * (lane ^ ((rr & 7) << 1)));
             y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+          }
+          if (hid_s[0] | hid_s[1] | hid_s[2] | hid_s[3]) {
+            const int seen = cc.v.len - cc.v.n;
+            const uint32_t found = hidden16<T>(a, cc.s, cc.h, seen + 1, seen + r / g, (4 * lane) & ~15) >> ((4 * lane) & 15);
+            if (found & 1) y.x = NAN;
+            if (found & 2) y.y = NAN;
+            if (found & 4) y.z = NAN;
+            if (found & 8) y.w = NAN;
           }
           if (kTeam) {
             *reinterpret_cast<float4*>(sm + kSmem<kT> + r * (4 * kD) + 16 * lane) = y;

@@ -128,6 +128,7 @@ struct PagedAttnArgs {
   jolt_dtype dtype;
   int32_t device;
   const CUtensorMap* maps;     // host: K and V with boxes of gcd(page_size, 128) rows, K and V with 16 rows
+  const void* V;               // the value pages
   const void* Q;
   int64_t q_ts, q_hs;          // element strides of Q
   int32_t Hq;

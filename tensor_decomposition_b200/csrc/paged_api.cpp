@@ -341,6 +341,7 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   a.dtype = pages->shape.dtype;
   a.device = pages->device;
   a.maps = pages->maps;
+  a.V = pages->V;
   a.Q = q.Q; a.q_ts = q.q_token_stride; a.q_hs = q.q_head_stride; a.Hq = q.q_heads;
   a.scale = q.scale; a.causal = q.causal != 0;
   a.pre_out = q.prefix_out; a.pre_lse = q.prefix_lse;

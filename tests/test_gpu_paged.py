@@ -639,3 +639,58 @@ def test_sizes_that_pass_32_bits(J):
     assert call(2, 1 << 23, 1 << 23, 1 << 22) == 9      # 2^17 blocks of rows by 2^19 tiles of keys
     assert call(2, 1 << 28, 1, 57) == 9                 # 2^31 query rows
     assert J.jolt_launch_count() == before
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kv,chunks,heads,g", [
+    ([300, 40, 2], [2, 3, 2], 2, 2),         # up to 8 rows, clusters
+    ([30000, 40], [2, 2], 2, 4),             # in many shares
+    ([30000, 77], [4, 3], 2, 4),             # up to 16
+    ([300, 5], [7, 5], 2, 4),                # up to 32, clusters
+    ([30000, 140], [7, 8], 2, 4),
+    ([30000, 40], [30, 40], 2, 4),           # chunks of half a block and less, in many shares
+    ([30000, 140], [100, 140], 2, 4),        # whole blocks, in many shares
+    ([100, 300], [130, 300], 3, 1),          # more tokens than the cache holds
+    ([256] * 80, [256] * 80, 2, 2),          # many more blocks than CTAs
+])
+def test_values_that_are_no_numbers_where_they_are_not_seen(J, dtype, kv, chunks, heads, g):
+    """Tokens of a chunk whose keys and values are no numbers (a padded chunk, say): the rows before them are
+    as they should be, and the rows that see such a value show it, in its feature alone: as no finite number, which
+    of them is open (a weight enters the product as a rounded part and a remainder that may be 0 or negative,
+    and inf * hi + inf * lo is then inf + NaN or inf - inf)."""
+    import torch
+    c = Cache(kv, chunks, heads, 16, _t(dtype), seed=6)
+    Q = c.randn(c.total, heads * g, D, scale=2.0)
+    pages, batch = c.handles(J)
+    seen = torch.zeros((c.total, heads * g, D), device="cuda")         # what every output is to show
+    K0, V0 = c.K.clone(), c.V.clone()
+    for s, (T, n) in enumerate(zip(kv, chunks)):
+        for back, h, f, x in ((0, 0, 0, math.nan), (1, heads - 1, 50, math.inf), (n // 2, 0, 127, -math.inf)):
+            t = T - 1 - back                                            # seen by the chunk's last 1 + back tokens
+            c.V[c.table[s, t // 16].long(), h, t % 16, f] = x
+            V0[c.table[s, t // 16].long(), h, t % 16, f] = 0.0
+            seen[c.starts[s + 1] - 1 - back:c.starts[s + 1], h * g:(h + 1) * g, f] += x
+    out = torch.zeros((c.total, heads * g, D), dtype=c.dtype, device="cuda")
+    L = torch.zeros((c.total, heads * g), device="cuda")
+    J.jolt_paged_attention(pages, batch, Q, out, SCALE, lse=L)
+    J.jolt_pages_status(pages)
+    bad = seen != 0                                                     # (a NaN is unequal to 0)
+    assert not torch.isfinite(out[bad].float()).any()
+    clean = Cache(kv, chunks, heads, 16, _t(dtype), seed=6)
+    clean.V = V0
+    ref = attention_ref(clean, Q, SCALE, True)[0]
+    out[bad] = ref[bad].to(c.dtype)
+    check_attention(clean, Q, out, L, SCALE, True)
+
+    # the chunk's last token, keys too: it alone is no number, and so is its row
+    c.V.copy_(V0)
+    for s, T in enumerate(kv):
+        c.K[c.table[s, (T - 1) // 16].long(), :, (T - 1) % 16] = math.nan
+        c.V[c.table[s, (T - 1) // 16].long(), :, (T - 1) % 16] = math.inf
+    J.jolt_paged_attention(pages, batch, Q, out, SCALE, lse=L)
+    J.jolt_pages_status(pages)
+    last = torch.tensor(c.starts[1:], device="cuda") - 1
+    assert torch.isnan(out[last].float()).all() and torch.isnan(L[last]).all()
+    ro, rl = attention_ref(clean, Q, SCALE, True)[:2]
+    out[last], L[last] = ro[last].to(c.dtype), rl[last].float()
+    check_attention(clean, Q, out, L, SCALE, True)

@@ -26,10 +26,11 @@ __global__ void __launch_bounds__(512) k_attn_combine(const PagedAttnArgs a, con
   if (sp.s < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & 3, rw = warp >> 2;
   const int c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
-  const int g = a.Hq / a.b.heads, R = sp.rows;
+  const int g = a.g.d, R = sp.rows;
   const int r = blockIdx.y * 4 + rw;
   if ((int)blockIdx.y * 4 >= R) return;
-  const int64_t row = (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g;
+  const int tok = a.g.quot(r);
+  const int64_t row = (int64_t)(sp.q0 + tok) * a.Hq + sp.h * g + r - tok * g;
   Prefix pre{};
   if (r < R && sub == 0) pre = load_prefix(a, row, lane);
   float mx = -INFINITY, ls = 0.0f;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(32 * kBlockWarps) k_attn_combine_blocks(const 
   const Split sp = ws.list[blockIdx.x];
   if (sp.s < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x, parts = sp.c_last - c0 + 1;
-  const int g = a.Hq / a.b.heads, rb = blockIdx.y * 32, R = sp.rows;
+  const int g = a.g.d, rb = blockIdx.y * 32, R = sp.rows;
   if (rb >= R) return;
   const bool in = rb + lane < R;
   const float4* o = reinterpret_cast<const float4*>(ws.o);
@@ -111,7 +112,8 @@ __global__ void __launch_bounds__(32 * kBlockWarps) k_attn_combine_blocks(const 
 #pragma unroll
   for (int k = 0; k < kN; ++k) {
     const int r = sp.m * 256 + min(rb + warp + kBlockWarps * k, R - 1);
-    row[k] = (int64_t)(sp.q0 + r / g) * a.Hq + sp.h * g + r % g;
+    const int tok = a.g.quot(r);
+    row[k] = (int64_t)(sp.q0 + tok) * a.Hq + sp.h * g + r - tok * g;
     pre[k] = load_prefix(a, row[k], lane);
   }
   float mx = -INFINITY, ls = 0.0f;

@@ -83,7 +83,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sm, int64_t& t
   return v + before;   // inclusive
 }
 
-// This CTA's share of the line: work(s) is the units of sequence s; a CTA takes min_units at least.
+// This CTA's share of the line: work(s) is the units of sequence s, 0 behind the last; a CTA takes min_units at least.
 // Called by all NT threads (NT a multiple of 32); sm: NT / 32 + 3 words of shared memory, free again on
 // return and a barrier.
 template <int NT, class F>
@@ -91,8 +91,8 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units,
   int64_t &base_s = sm[NT / 32], &units_s = sm[NT / 32 + 1], &seq_s = sm[NT / 32 + 2];
   Start r{};
   const int tid = threadIdx.x;
-  int64_t mine = tid < num_seqs ? work(tid) : 0, sum = mine;
-  for (int s = tid + NT; s < num_seqs; s += NT) sum += work(s);
+  int64_t mine = work(tid), sum = mine;
+  for (int s0 = NT; s0 < num_seqs; s0 += NT) sum += work(s0 + tid);
   int64_t total, base = 0;
   int64_t incl = block_scan<NT>(sum, sm, total);
   const int64_t most = quot(total + min_units - 1, min_units);
@@ -111,7 +111,7 @@ __device__ __forceinline__ Start find_start(int num_seqs, F work, int min_units,
     __syncthreads();
   } else {
     for (int s0 = 0; s0 < num_seqs; s0 += NT) {
-      const int64_t v = s0 + tid < num_seqs ? work(s0 + tid) : 0;
+      const int64_t v = work(s0 + tid);
       incl = base + block_scan<NT>(v, sm, total);
       if (incl > r.lo && incl - v <= r.lo) {
         base_s = incl - v;
@@ -224,7 +224,7 @@ __device__ __forceinline__ uint32_t hidden16(const PagedAttnArgs& a, int s, int 
     const int page = page_of(a.b, s, key);
     if (page < 0) continue;
     const uint16_t* v = reinterpret_cast<const uint16_t*>(a.V) +
-                        (((int64_t)page * a.b.heads + h) * a.b.page_size + key % a.b.page_size) * kD + d0;
+                        (((int64_t)page * a.b.heads + h) * a.b.page_size + key - a.b.by_page.quot(key) * a.b.page_size) * kD + d0;
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
       if ((v[i] & exponent(T())) == exponent(T())) found |= 1u << i;

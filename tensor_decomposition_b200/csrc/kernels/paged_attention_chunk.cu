@@ -44,11 +44,13 @@ struct Bars {
   uint64_t tail;
 };
 
-__device__ __forceinline__ int blocks_of(const SeqView& v, int g) { return (v.n * g + kBlockRows - 1) / kBlockRows; }
+__device__ __forceinline__ int blocks_of(const SeqView& v, const Divisor& g) {
+  return (v.n * (int)g.d + kBlockRows - 1) / kBlockRows;
+}
 // Tiles of keys that block m of the sequence's rows sees (one at least, so that empty rows are written).
-__device__ __forceinline__ int tiles_of(const SeqView& v, int g, int m, bool causal) {
+__device__ __forceinline__ int tiles_of(const SeqView& v, const Divisor& g, int m, bool causal) {
   int seen = v.len;
-  if (causal) seen += (int)((uint32_t)(min(v.n * g, (m + 1) * kBlockRows) - 1) / (uint32_t)g) + 1 - v.n;
+  if (causal) seen += g.quot(min(v.n * (int)g.d, (m + 1) * kBlockRows) - 1) + 1 - v.n;
   return max(1, (seen + kHalf - 1) / kHalf);
 }
 
@@ -60,7 +62,7 @@ struct Piece {
   int left;         // units of the CTA's share behind the piece
 };
 // The piece of an item from its unit u on; false if the share ends before the item's first tile.
-__device__ __forceinline__ bool enter(Piece& p, int u, int g, bool causal) {
+__device__ __forceinline__ bool enter(Piece& p, int u, const Divisor& g, bool causal) {
   p.T = tiles_of(p.v, g, p.m, causal);
   const int take = min(p.T + kItem - u, p.left);
   p.left -= take;
@@ -69,7 +71,7 @@ __device__ __forceinline__ bool enter(Piece& p, int u, int g, bool causal) {
   return p.t1 > p.t0;
 }
 // The next piece of the share; false behind the last.
-__device__ __forceinline__ bool next(Piece& p, const BatchView& b, int g, bool causal) {
+__device__ __forceinline__ bool next(Piece& p, const BatchView& b, const Divisor& g, bool causal) {
   if (p.left <= 0) return false;
   if (++p.m == p.M) {
     p.m = 0;
@@ -90,10 +92,10 @@ __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 6
 
 // Whether an item's rows fill one half only: the halves then take its tiles in turn, with the same
 // queries, and their outputs are joined at the end.
-__device__ __forceinline__ bool solo(const Piece& p, int g) { return p.v.n * g - p.m * kBlockRows <= kHalf; }
+__device__ __forceinline__ bool solo(const Piece& p, const Divisor& g) { return p.v.n * (int)g.d - p.m * kBlockRows <= kHalf; }
 
 // A warp's common place moved on by its first lane.
-__device__ __forceinline__ bool next_of_warp(Piece& p, const BatchView& b, int g, bool causal, int lane) {
+__device__ __forceinline__ bool next_of_warp(Piece& p, const BatchView& b, const Divisor& g, bool causal, int lane) {
   __syncwarp();
   bool more = false;
   if (lane == 0) more = next(p, b, g, causal);
@@ -225,15 +227,15 @@ __device__ __forceinline__ void output16(uint32_t t0, float f0, bool both, float
 // Rare, so kept out of the kernel's code: what one warp does to hide values, and to show NaN where a row of
 // the piece that sees the keys up to lim sees one: in out (blocks of one feature) or a part (blocks of four).
 template <typename T>
-__device__ __noinline__ void hide_values(uint8_t* tile, int ra, int rb, bool* hid) {
+__device__ __forceinline__ void hide_values(uint8_t* tile, int ra, int rb, bool* hid) {
   hide<T>(tile, kHalfTile, ra, rb, threadIdx.x & 31);
   *hid = true;
 }
 template <typename T>
 __device__ __noinline__ void show_values(const PagedAttnArgs& a, const Piece& p, int lim, T* out, float* part) {
-  const int g = a.Hq / a.b.heads;
+  const Divisor& g = a.g;
   for (int d0 = 0; d0 < kD; d0 += 16) {
-    const uint32_t found = hidden16<T>(a, p.s, p.h, p.v.len - p.v.n + p.m * kBlockRows / g + 1, lim, d0);
+    const uint32_t found = hidden16<T>(a, p.s, p.h, p.v.len - p.v.n + g.quot(p.m * kBlockRows) + 1, lim, d0);
     for (int d = d0; d < d0 + 16; ++d) {
       if (!((found >> (d - d0)) & 1)) continue;
       if (out) out[d] = (T)NAN;
@@ -249,14 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) Bars bar;
   __shared__ uint32_t tmem_s;
   __shared__ int gave_up;
-  __shared__ Piece piece_s[kSoftmaxWarps + 4];   // each warp's place on the line
+  __shared__ Piece first_s, piece_s[kSoftmaxWarps + 4];   // the share's begin, each warp's place on the line
   __shared__ bool any_s;
   __shared__ bool hid_s[8];                // whether a piece's values hold what was hidden: the last pieces'
   __shared__ float2 told_s[kHalf];         // what half 1 tells half 0
   __shared__ int64_t range_s[3];   // the end of this CTA's share, units of a share, shares with one more
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchView& b = a.b;
-  const int g = a.Hq / b.heads;
+  const Divisor& g = a.g;
   const bool causal = a.causal;
   grid_release();
   if (tid == 0) {
@@ -276,6 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.tail, 1);
     gave_up = 0;
     fence_barrier_init();
+    prefetch_tensormap(&maps.K);
+    prefetch_tensormap(&maps.V);
   }
   if (warp == kSoftmaxWarps) {
     tmem_alloc(&tmem_s, 512);
@@ -284,12 +288,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_wait();
   const Start st = find_start<kThreads>(
       b.num_seqs,
-      [&](int s) {
-        const SeqView v = seq_view(b, s);
+      [&](int s) {   // of a warp's 32 sequences at once, those of more than four blocks one by one
+        SeqView v{0, 0, 0};
+        if (s < b.num_seqs) v = seq_view(b, s);
         const int M = blocks_of(v, g);
         int64_t n = 0;
-#pragma unroll 4
-        for (int m = 0; m < M; ++m) n += tiles_of(v, g, m, causal) + kItem;
+        if (M <= 4)
+          for (int m = 0; m < M; ++m) n += tiles_of(v, g, m, causal) + kItem;
+        for (uint32_t more = __ballot_sync(0xffffffffu, M > 4); more; more &= more - 1) {
+          const int from = __ffs(more) - 1, blocks = __shfl_sync(0xffffffffu, M, from);
+          const SeqView w{0, __shfl_sync(0xffffffffu, v.n, from), __shfl_sync(0xffffffffu, v.len, from)};
+          int64_t sum = 0;
+          for (int m = lane; m < blocks; m += 32) sum += tiles_of(w, g, m, causal) + kItem;
+#pragma unroll
+          for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == from) n = sum;
+        }
         return n * b.heads;
       },
       kItem + 2, reinterpret_cast<int64_t*>(told_s));
@@ -298,28 +312,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kSoftmaxWarps) tmem_dealloc(tmem_s, 512);
     return;
   }
-  if (tid == 0) {
+  if (warp == 0) {   // the share's first piece
     Piece p;
     p.s = st.s;
     p.v = seq_view(b, p.s);
     p.M = blocks_of(p.v, g);
-    const int64_t per = quot(st.units, b.heads), from = st.lo - st.base;   // (a head's units fit 32 bits)
+    const int64_t per = quot(st.units, b.heads), from = st.lo - st.base;   // (a head's units fit 31 bits)
     p.h = (int)quot(from, (uint32_t)per);
     int at = (int)(from - p.h * per);
-    p.m = 0;
-    for (int n; at >= (n = tiles_of(p.v, g, p.m, causal) + kItem); at -= n) ++p.m;
-    p.left = (int)(st.hi - st.lo);
-    any_s = enter(p, at, g, causal);   // a share can lie in an item's first units only
-    for (Piece& q : piece_s) q = p;
-    range_s[0] = st.hi;
-    range_s[1] = st.each;
-    range_s[2] = st.more;
-    ws.list[blockIdx.x].s = -1;
+    for (p.m = 0; p.m < p.M; p.m += 32) {   // 32 blocks at a time
+      const int n = p.m + lane < p.M ? tiles_of(p.v, g, p.m + lane, causal) + kItem : 0;
+      int to = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += y;
+      }
+      const uint32_t in = __ballot_sync(0xffffffffu, at < to);
+      const int k = in ? __ffs(in) - 1 : 31;
+      at -= __shfl_sync(0xffffffffu, in ? to - n : to, k);
+      if (in) {
+        p.m += k;
+        break;
+      }
+    }
+    if (lane == 0) {
+      p.left = (int)(st.hi - st.lo);
+      any_s = enter(p, at, g, causal);   // a share can lie in an item's first units only
+      first_s = p;
+      range_s[0] = st.hi;
+      range_s[1] = st.each;
+      range_s[2] = st.more;
+      ws.list[blockIdx.x].s = -1;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
+  if (lane < (int)(sizeof(Piece) / 4))
+    reinterpret_cast<int32_t*>(&piece_s[warp])[lane] = reinterpret_cast<const int32_t*>(&first_s)[lane];
+  __syncwarp();
   const Waits wait{&gave_up, b.status};
   uint8_t* Qs = sm;
   uint8_t* ring = sm + 2 * kTileBytes;
@@ -426,14 +459,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- keys and values
       Piece& p = piece_s[warp];
       uint32_t kv = 0, tails = 0, pieces = 0;
-      const int per = kHalf / box;           // boxes of a tile: one lane each
-      prefetch_tensormap(&maps.K);
-      prefetch_tensormap(&maps.V);
+      const int box_log = 31 - __clz(box), per_log = 7 - box_log, per = 1 << per_log;   // boxes of a tile: one lane each
+      // Pages are looked up for 32 boxes at once: lane i has that of box i % per of tile pg_j + i / per.
+      const int tile_l = lane >> per_log, box_l = lane & (per - 1), ahead = 32 >> per_log;
+      int pg = -1, pg_s = -1, pg_j = 0;
       bool ok = true;
       do {
         const int t0 = p.t0, nt = p.t1 - t0, len = p.v.len, h = p.h, seq = p.s;
         const bool alone = solo(p, g);
-        const int seen = causal ? len - p.v.n + p.m * kBlockRows / g : len - 1;   // the last key that all rows see
+        const int seen = causal ? len - p.v.n + g.quot(p.m * kBlockRows) : len - 1;   // the last key that all rows see
         // (the ring holds the tiles of three pieces at most, and the softmax is at most two behind those)
         bool* hid = &hid_s[pieces++ & 7];
         if (lane == 0) *hid = false;
@@ -446,9 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             j += t0;
             const int key = j * kHalf + lane * box;     // this lane's box
-            int page = -1;
+            if (seq != pg_s || j < pg_j || j >= pg_j + ahead) {
+              pg_s = seq;
+              pg_j = max(j - 1, 0);          // the halves' turns go back by one
+              const int64_t k = (int64_t)(pg_j + tile_l) * kHalf + box_l * box;
+              pg = k < len ? page_of(b, seq, (int)k) : -1;
+            }
             const bool mine = lane < per && key < len;
-            if (mine) page = page_of(b, seq, key);
+            int page = __shfl_sync(0xffffffffu, pg, ((j - pg_j) << per_log) + box_l);
+            if (!mine) page = -1;
             const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
             const bool whole = __all_sync(0xffffffffu, !mine || page >= 0);
             const bool ends = (j + 1) * kHalf > len;
@@ -466,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (page >= 0) {
               const CUtensorMap* map = kind ? &maps.V : &maps.K;
-              const int row = key % b.page_size;
+              const int row = key - b.by_page.quot(key) * b.page_size;
               tma_load_4d(dst + lane * box * 128, map, fb, 0, row, h, page);
               tma_load_4d(dst + kHalfTile + lane * box * 128, map, fb, 64, row, h, page);
             }
@@ -475,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++tails;
               if (!ok) break;
               for (int r = lane; r < kHalf; r += 32) {
-                if (((good >> (r / box)) & 1) && j * kHalf + r < len) continue;
+                if (((good >> (r >> box_log)) & 1) && j * kHalf + r < len) continue;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                   *reinterpret_cast<uint4*>(dst + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
@@ -500,17 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- queries: a warp a half block
       Piece& p = piece_s[warp];
       const int t = warp - kSoftmaxWarps - 2, c16 = lane & 15, r2 = lane >> 4;
-      const int step_t = 2 / g, step_h = 2 % g;       // from a row to the one two further
+      const int step_t = g.quot(2), step_h = 2 - step_t * g.d;       // from a row to the one two further
       uint32_t pieces = 0;
       bool ok = true;
       do {
-        const int R = p.v.n * g, r0 = p.m * kBlockRows + t * kHalf;
+        const int R = p.v.n * g.d, r0 = p.m * kBlockRows + t * kHalf;
         if (r0 >= R) continue;
         ok = __all_sync(0xffffffffu, wait(&bar.q_empty[t], (pieces & 1) ^ 1));
         if (!ok) break;
         ++pieces;
-        int tok = (r0 + r2) / g, hd = (r0 + r2) - tok * g;
-        const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g * a.q_hs + 8 * c16;
+        int tok = g.quot(r0 + r2), hd = (r0 + r2) - tok * g.d;
+        const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)p.v.q0 * a.q_ts + (int64_t)p.h * g.d * a.q_hs + 8 * c16;
         const uint32_t dst = smem_u32(Qs + t * kTileBytes + (c16 >> 3) * kHalfTile);
         const int pairs = (min(kHalf, R - r0) + 1) / 2;   // what lies behind the last row does not matter
 #pragma unroll 4
@@ -523,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "memory");
           tok += step_t;
           hd += step_h;
-          if (hd >= g) {
-            hd -= g;
+          if (hd >= (int)g.d) {
+            hd -= g.d;
             ++tok;
           }
         }
@@ -546,14 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // waits give up at once then. The result is reported as void.
     do {
       const bool alone = solo(p, g), began = p.t0 == 0, ends = p.t1 == p.T;
-      const int R = p.v.n * g, r0 = p.m * kBlockRows + (alone ? 0 : t * kHalf);
+      const int R = p.v.n * g.d, r0 = p.m * kBlockRows + (alone ? 0 : t * kHalf);
       if (tid == 0 && began && !ends)   // the share's last piece
         ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[0] + (p.T - p.t1) - 1, range_s[1], range_s[2]), 1,
                                     p.v.q0, min(kBlockRows, R - p.m * kBlockRows)};
       const int t1 = p.t1, every = alone ? 2 : 1, t0 = p.t0 + (alone ? t : 0);   // this half's tiles
       const bool rows = r0 + 32 * wq < R;         // whether the warp has any
       const int r = r0 + 32 * wq + lane;
-      const int rc = min(r, R - 1), tok = rc / g;
+      const int rc = min(r, R - 1), tok = g.quot(rc);
       const int lim = causal ? p.v.len - p.v.n + tok : p.v.len - 1;
       const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);      // the least of the warp's rows
       float m = -INFINITY, l = 0.0f;
@@ -610,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = m == -INFINITY ? 0.0f : -m;
         weights<T>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
-      const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g + (rc - tok * g);
+      const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g.d + (rc - tok * g.d);
       if (a.pre_lse && r < R) {   // what the end needs of the prefix, while the last products are made
         prefetch_l2(a.pre_out + row * kD, kD * 4);
       }

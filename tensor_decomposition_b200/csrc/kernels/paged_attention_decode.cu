@@ -118,18 +118,18 @@ struct Blocks16 {
   float o[kT][16][4], m[kT][2], l[kT][2];
   int lim[kT][2];
 
-  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const SeqView& v, int h, int g, uint8_t* qs, int tid) {
-    const int lane = tid & 31, quad = lane >> 2, pair = lane & 3, R = v.n * g;
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const SeqView& v, int h, uint8_t* qs, int tid) {
+    const int g = a.g.d, lane = tid & 31, quad = lane >> 2, pair = lane & 3, R = v.n * g;
     const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)v.q0 * a.q_ts + (int64_t)h * g * a.q_hs;
 #pragma unroll
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = 16 * t + quad + 8 * k;
-        const int tok = r / g;
+        const int tok = a.g.quot(r);
         lim[t][k] = r < R ? (a.causal ? v.len - v.n + tok : v.len - 1) : -1;
         if (kT == 1) {
-          const T* p = Q + (int64_t)tok * a.q_ts + (int64_t)(r % g) * a.q_hs + 2 * pair;
+          const T* p = Q + (int64_t)tok * a.q_ts + (int64_t)(r - tok * g) * a.q_hs + 2 * pair;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             q[j][k] = r < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j) : 0u;
@@ -141,7 +141,7 @@ struct Blocks16 {
       }
     if (kT > 1) {   // no warp reads the queries before: the last item's end was a barrier
       for (int u = tid; u < rows * 16; u += kThreads) {
-        const int r = u >> 4, c = u & 15, tok = r / g;
+        const int r = u >> 4, c = u & 15, tok = a.g.quot(r);
         const uint4 x = r < R ? *reinterpret_cast<const uint4*>(Q + (int64_t)tok * a.q_ts + (int64_t)(r - tok * g) * a.q_hs + 8 * c)
                               : make_uint4(0, 0, 0, 0);
         *reinterpret_cast<uint4*>(qs + r * (2 * kD) + ((c ^ (r & 7)) << 4)) = x;
@@ -285,10 +285,10 @@ struct Block8 {
   float o[8][4], m[2], l[2];
   int lim[2];
 
-  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const SeqView& v, int h, int g, uint8_t*, int tid) {
-    const int lane = tid & 31, quad = lane >> 2, pair = lane & 3, R = v.n * g;
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const SeqView& v, int h, uint8_t*, int tid) {
+    const int g = a.g.d, lane = tid & 31, quad = lane >> 2, pair = lane & 3, R = v.n * g, tok = a.g.quot(quad);
     const T* Q = reinterpret_cast<const T*>(a.Q) + (int64_t)v.q0 * a.q_ts + (int64_t)h * g * a.q_hs;
-    const T* p = Q + (int64_t)(quad / g) * a.q_ts + (int64_t)(quad % g) * a.q_hs + 2 * pair;
+    const T* p = Q + (int64_t)tok * a.q_ts + (int64_t)(quad - tok * g) * a.q_hs + 2 * pair;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       q[j][0] = quad < R ? *reinterpret_cast<const uint32_t*>(p + 16 * j) : 0u;
@@ -297,7 +297,7 @@ struct Block8 {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 2 * pair + e;
-      lim[e] = r < R ? (a.causal ? v.len - v.n + r / g : v.len - 1) : -1;
+      lim[e] = r < R ? (a.causal ? v.len - v.n + a.g.quot(r) : v.len - 1) : -1;
       m[e] = -INFINITY;
       l[e] = 0.0f;
     }
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
   __shared__ int64_t scan_s[kSlices + 3];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchView& b = a.b;
-  const int g = a.Hq / b.heads;
+  const int g = a.g.d;
   const float scale2 = a.scale * kLog2e;
   grid_release();
   if (tid < kSlices * kDeep) mbar_init(&full_s[0][0] + tid, 1);
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     lc.u = (int)st.lo;
   } else {
     st = find_start<kThreads>(
-        b.num_seqs, [&](int s) { return (int64_t)units_of(seq_view(b, s)) * b.heads; }, kMinUnits, scan_s);
+        b.num_seqs, [&](int s) { return s < b.num_seqs ? (int64_t)units_of(seq_view(b, s)) * b.heads : 0; }, kMinUnits, scan_s);
     if ((int)blockIdx.x >= st.G) {
       if (tid == 0) ws.list[blockIdx.x].s = -1;
       return;
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
       uint64_t* bar = &full_s[warp][stage];
       valid_s[warp][stage] = page < 0 ? 0 : min(kKeys, lc.v.len - key0);
       if (page >= 0) {
-        const int row = key0 % b.page_size;
+        const int row = key0 - b.by_page.quot(key0) * b.page_size;
         uint8_t* dst = ring + stage * 2 * kTile;
         mbar_arrive_expect_tx(bar, 2 * kTile);
         tma_load_4d(dst, &maps.K, bar, 0, row, lc.h, page);
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     if (fresh) {
       fresh = false;
       if (lane == 0) hid_s[warp] = false;
-      held.begin(a, cc.v, cc.h, g, sm + kRing<kT>, tid);
+      held.begin(a, cc.v, cc.h, sm + kRing<kT>, tid);
     }
     const uint32_t Ks = smem_u32(ring + stage * 2 * kTile), Vs = Ks + kTile;
     const int key0 = cc.u * kUnit + warp * kKeys;
@@ -547,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
         __syncthreads();
         for (int rr = warp; rr < min(Held::per, R - Held::per * t); rr += kSlices) {
           const int r = Held::per * t + rr;
-          const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
+          const int tok = a.g.quot(r);
+          const int64_t row = (int64_t)(cc.v.q0 + tok) * a.Hq + cc.h * g + r - tok * g;
           Prefix pre{};
           if (!kTeam && whole) pre = load_prefix(a, row, lane);
           float mx = -INFINITY, ls = 0.0f;
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
           }
           if (hid_s[0] | hid_s[1] | hid_s[2] | hid_s[3]) {
             const int seen = cc.v.len - cc.v.n;
-            const uint32_t found = hidden16<T>(a, cc.s, cc.h, seen + 1, seen + r / g, (4 * lane) & ~15) >> ((4 * lane) & 15);
+            const uint32_t found = hidden16<T>(a, cc.s, cc.h, seen + 1, seen + tok, (4 * lane) & ~15) >> ((4 * lane) & 15);
             if (found & 1) y.x = NAN;
             if (found & 2) y.y = NAN;
             if (found & 4) y.z = NAN;
@@ -607,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
   if (count == 0 && tid < kRows) team_ml[tid] = make_float2(-INFINITY, 0.0f);
   const cooperative_groups::cluster_group team = cooperative_groups::this_cluster();
   const int r = blockIdx.x % kTeamCtas + kTeamCtas * warp;
-  const int64_t row = (int64_t)(cc.v.q0 + r / g) * a.Hq + cc.h * g + r % g;
+  const int tok = a.g.quot(r);
+  const int64_t row = (int64_t)(cc.v.q0 + tok) * a.Hq + cc.h * g + r - tok * g;
   Prefix pre{};
   if (r < cc.v.n * g) pre = load_prefix(a, row, lane);
   team.sync();

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
       int64_t d = -1;
       if (s >= 0 && pos_s[t] >= 0) {
         const int pg = page_of(a.b, s, pos_s[t]);
-        if (pg >= 0) d = ((int64_t)pg * a.b.heads * a.b.page_size + pos_s[t] % a.b.page_size) * kD;
+        if (pg >= 0) d = ((int64_t)pg * a.b.heads * a.b.page_size + pos_s[t] - a.b.by_page.quot(pos_s[t]) * a.b.page_size) * kD;
       }
       dst_s[t] = d;
     }

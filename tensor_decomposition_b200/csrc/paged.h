@@ -15,6 +15,23 @@ namespace jolt {
 // Bits of a page set's status word (OR-ed by kernels, read and cleared by jolt_pages_status).
 enum : int32_t { PST_BAD_BATCH = 1, PST_BAD_PAGE = 2, PST_TIMEOUT = 4 };
 
+// A divisor d that the host knows: the quotient of 0 <= n < 2^31 is floor(n m / 2^(31 + s)) with s = ceil(log2 d)
+// and m = ceil(2^(31 + s) / d) < 2^32, which is n / d and less than 1 / d too much (Granlund and Montgomery's
+// division by an invariant). The kernels divide on their way to the first copy, where a division costs 0.1 us.
+struct Divisor {
+  uint32_t d = 1, m = 1u << 31, s = 0;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quot(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
+#endif
+};
+inline Divisor divisor(uint32_t d) {
+  Divisor r;
+  r.d = d;
+  while ((1u << r.s) < d && r.s < 31) ++r.s;
+  r.m = (uint32_t)(((1ull << (31 + r.s)) + d - 1) / d);
+  return r;
+}
+
 // One batch of sequences (device arrays; see jolt_batch in jolt.h) over one page set.
 struct BatchView {
   int32_t num_seqs, total_q, max_q, max_pages;
@@ -22,6 +39,7 @@ struct BatchView {
   const int32_t* kv_len;       // [num_seqs]
   const int32_t* page_table;   // [num_seqs][max_pages]
   int32_t num_pages, heads, page_size;
+  Divisor by_page;             // page_size
   int32_t* status;
 };
 
@@ -49,7 +67,7 @@ __device__ __forceinline__ SeqView seq_view(const BatchView& b, int s) {
 // Page that holds token `pos` (0 <= pos < len) of sequence s, or -1 (flagged) when the table's
 // entry is no page of the set.
 __device__ __forceinline__ int page_of(const BatchView& b, int s, int pos) {
-  const int p = b.page_table[(int64_t)s * b.max_pages + pos / b.page_size];
+  const int p = b.page_table[(int64_t)s * b.max_pages + b.by_page.quot(pos)];
   if (p < 0 || p >= b.num_pages) {
     atomicOr(b.status, PST_BAD_PAGE);
     return -1;
@@ -132,6 +150,7 @@ struct PagedAttnArgs {
   const void* Q;
   int64_t q_ts, q_hs;          // element strides of Q
   int32_t Hq;
+  Divisor g;                   // query heads a KV head
   float scale;
   int32_t causal;
   const float *pre_out, *pre_lse;   // [total_q][Hq][128], [total_q][Hq], or null

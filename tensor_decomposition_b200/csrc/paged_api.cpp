@@ -153,6 +153,7 @@ BatchView view_of(const jolt_pages_s* pg, const jolt_batch* b) {
   v.num_pages = pg->shape.num_pages;
   v.heads = pg->shape.heads;
   v.page_size = pg->shape.page_size;
+  v.by_page = divisor(v.page_size);
   v.status = pg->d_status;
   return v;
 }
@@ -343,6 +344,7 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
   a.maps = pages->maps;
   a.V = pages->V;
   a.Q = q.Q; a.q_ts = q.q_token_stride; a.q_hs = q.q_head_stride; a.Hq = q.q_heads;
+  a.g = divisor(q.q_heads / pages->shape.heads);
   a.scale = q.scale; a.causal = q.causal != 0;
   a.pre_out = q.prefix_out; a.pre_lse = q.prefix_lse;
   a.out = q.out; a.lse = q.lse;

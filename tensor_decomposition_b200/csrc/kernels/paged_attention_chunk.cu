@@ -47,23 +47,27 @@ struct Bars {
 __device__ __forceinline__ int blocks_of(const SeqView& v, const Divisor& g) {
   return (v.n * (int)g.d + kBlockRows - 1) / kBlockRows;
 }
-// Tiles of keys that block m of the sequence's rows sees (one at least, so that empty rows are written).
+// Keys that block m of the sequence's rows sees (none where it is not positive), and their tiles (one at least,
+// so that empty rows are written).
+__device__ __forceinline__ int seen_of(const SeqView& v, const Divisor& g, int m, bool causal) {
+  return causal ? v.len + g.quot(min(v.n * (int)g.d, (m + 1) * kBlockRows) - 1) + 1 - v.n : v.len;
+}
 __device__ __forceinline__ int tiles_of(const SeqView& v, const Divisor& g, int m, bool causal) {
-  int seen = v.len;
-  if (causal) seen += g.quot(min(v.n * (int)g.d, (m + 1) * kBlockRows) - 1) + 1 - v.n;
-  return max(1, (seen + kHalf - 1) / kHalf);
+  return max(1, (seen_of(v, g, m, causal) + kHalf - 1) / kHalf);
 }
 
 // A part of an item: tiles t0 .. t1 - 1 of its T. On the line an item takes kItem units (its begin and
 // end: queries in, output out) and one for each tile after them.
 struct Piece {
   int s, h, m, M, t0, t1, T;
+  int upto;         // keys that the block sees
   SeqView v;
   int left;         // units of the CTA's share behind the piece
 };
 // The piece of an item from its unit u on; false if the share ends before the item's first tile.
 __device__ __forceinline__ bool enter(Piece& p, int u, const Divisor& g, bool causal) {
-  p.T = tiles_of(p.v, g, p.m, causal);
+  p.upto = max(0, seen_of(p.v, g, p.m, causal));
+  p.T = max(1, (p.upto + kHalf - 1) / kHalf);
   const int take = min(p.T + kItem - u, p.left);
   p.left -= take;
   p.t0 = max(u - kItem, 0);
@@ -157,7 +161,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The weights 2^(s scale2 + sub) of a row, rounded to the type, written to Tensor Memory (tP); their
 // sum goes to l unrounded. The first half is announced while the second is made. (Making 1 or 2 of 8
 // exponentials by a polynomial on the multiply-add units, to spare the special function unit, gave 0 and
-// -8 % on a chunk of 2048 tokens over 32768 keys.)
+// -8 % on a chunk of 2048 tokens over 32768 keys. Leaving out those of 32 keys that no row of the warp sees,
+// by a branch, made items of one or two tiles 5 % faster and prompts 4 % slower.)
 template <typename T>
 __device__ __forceinline__ void weights(const float (&s)[kHalf], float scale2, float sub, float& l, uint32_t tP,
                                         uint64_t* lo, uint64_t* hi, int lane) {
@@ -224,13 +229,8 @@ __device__ __forceinline__ void output16(uint32_t t0, float f0, bool both, float
   }
 }
 
-// Rare, so kept out of the kernel's code: what one warp does to hide values, and to show NaN where a row of
-// the piece that sees the keys up to lim sees one: in out (blocks of one feature) or a part (blocks of four).
-template <typename T>
-__device__ __forceinline__ void hide_values(uint8_t* tile, int ra, int rb, bool* hid) {
-  hide<T>(tile, kHalfTile, ra, rb, threadIdx.x & 31);
-  *hid = true;
-}
+// Rare, so kept out of the kernel's code: NaN where a row of the piece that sees the keys up to lim sees a value
+// that is no finite number, in out (blocks of one feature) or a part (blocks of four).
 template <typename T>
 __device__ __noinline__ void show_values(const PagedAttnArgs& a, const Piece& p, int lim, T* out, float* part) {
   const Divisor& g = a.g;
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int pg = -1, pg_s = -1, pg_j = 0;
       bool ok = true;
       do {
-        const int t0 = p.t0, nt = p.t1 - t0, len = p.v.len, h = p.h, seq = p.s;
+        const int t0 = p.t0, nt = p.t1 - t0, len = p.v.len, upto = p.upto, h = p.h, seq = p.s;
         const bool alone = solo(p, g);
         const int seen = causal ? len - p.v.n + g.quot(p.m * kBlockRows) : len - 1;   // the last key that all rows see
         // (the ring holds the tiles of three pieces at most, and the softmax is at most two behind those)
@@ -486,20 +486,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int64_t k = (int64_t)(pg_j + tile_l) * kHalf + box_l * box;
               pg = k < len ? page_of(b, seq, (int)k) : -1;
             }
-            const bool mine = lane < per && key < len;
+            const bool mine = lane < per && key < upto;
             int page = __shfl_sync(0xffffffffu, pg, ((j - pg_j) << per_log) + box_l);
             if (!mine) page = -1;
             const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
             const bool whole = __all_sync(0xffffffffu, !mine || page >= 0);
-            const bool ends = (j + 1) * kHalf > len;
             const uint32_t s = kv % kStages;
             ok = __all_sync(0xffffffffu, wait(&bar.kv_empty[s], ((kv / kStages) & 1) ^ 1));
             if (!ok) break;
-            // A tile with rows that hold no keys: values there are zeroed, since a weight of zero
-            // does not hide what lies in the page (keys are hidden by the mask on their scores);
-            // rows of a bad page are zeroed for both. Such a tile lands on a barrier of its own first.
-            const bool some = kind == 1 && min((j + 1) * kHalf, len) - 1 > seen;   // values that not all rows see
-            const bool fix = !whole || (kind == 1 && ends) || some;
+            // A tile that is looked over when it has landed, on a barrier of its own: values that no
+            // row sees are zeroed, since a weight of zero does not hide what lies in the page (keys
+            // are hidden by the mask on their scores), rows of a bad page for both, and values that not all
+            // rows see where they are no numbers.
+            const int here = upto - j * kHalf;
+            const bool some = kind == 1 && j * kHalf + min(here, kHalf) - 1 > seen;
+            const bool fix = !whole || (kind == 1 && here < kHalf) || some;
             uint64_t* fb = fix ? &bar.tail : &bar.kv_full[s];
             uint8_t* dst = ring + s * kTileBytes;
             if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(good) * box * kD * 2);
@@ -514,17 +515,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = __all_sync(0xffffffffu, wait(&bar.tail, tails & 1));
               ++tails;
               if (!ok) break;
-              for (int r = lane; r < kHalf; r += 32) {
-                if (((good >> (r >> box_log)) & 1) && j * kHalf + r < len) continue;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  *reinterpret_cast<uint4*>(dst + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                  *reinterpret_cast<uint4*>(dst + kHalfTile + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                }
+              for (int r = (whole ? max(0, here) : 0) + (lane >> 3); r < kHalf; r += 4) {   // eight lanes a row
+                if (((good >> (r >> box_log)) & 1) && r < here) continue;
+                *reinterpret_cast<uint4*>(dst + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(dst + kHalfTile + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
               }
               if (some) {
-                const int from = max(0, seen + 1 - j * kHalf), to = min(kHalf, len - j * kHalf);
-                if (!finite<T, 2>(dst, kHalfTile, from, to, lane)) hide_values<T>(dst, from, to, hid);
+                const int from = max(0, seen + 1 - j * kHalf), to = min(kHalf, here);
+                if (!finite<T, 2>(dst, kHalfTile, from, to, lane)) {
+                  hide<T>(dst, kHalfTile, from, to, lane);
+                  *hid = true;
+                }
               }
               fence_async_shared();
               __syncwarp();

@@ -9,10 +9,10 @@
 // Each row is read and written once, which bounds the kernel for long inputs (HBM); short inputs
 // are bound by latency. A CTA takes a tile of tokens, up to 64 rows, 8 lanes a row (two 16-byte runs each) and
 // up to four rows a lane in flight at once: with one token a CTA the append of 16 rows a token ran at 1.4
-// TB/s, so it runs at 4.1. The tile's sines are computed once (a thread each, while the rows are on their
+// TB/s, so it runs at 4.3 (tokens of 80 rows, a CTA each, at 5.5). The tile's sines are computed once (a thread each, while the rows are on their
 // way) and used by all heads from shared memory; the append's page lookup is one parallel pass over the
 // batch's offsets instead of a search. (Persistent CTAs with a ring of asynchronous copies, and tiles of
-// two to four times the rows, were 8 to 25 % slower: the issue slots are 70 % busy as it is.)
+// two to four times the rows, were 8 to 25 % slower.)
 #include <algorithm>
 
 #include "../paged.h"
@@ -26,7 +26,12 @@ using namespace f32x2;
 constexpr int kThreads = 128;
 constexpr int kLanes = 8;               // of a row: 16 features each
 constexpr int kSlots = kThreads / kLanes;   // rows at a time
-constexpr int kBatch = 4;               // rows a slot keeps in flight
+// Rows a slot keeps in flight. Where a tile has more rows than the slots hold at once (a token of more than 64
+// rows), the next row is loaded as soon as one is taken up, and three do; else all are loaded first and used
+// (16384 tokens of 80 rows: 121 us that way and 132 the other; 64 tokens of 40 rows: 4.4 and 3.3 us).
+template <bool kLong>
+constexpr int kBatch = kLong ? 3 : 4;
+constexpr int kRows = kSlots * kBatch<false>;   // of a tile, unless one token has more
 constexpr int kCtas = 6;                // per SM
 constexpr int kMaxTile = 16;            // tokens of a tile
 
@@ -73,7 +78,7 @@ struct RowsArgs {
 
 // A lane holds two runs of eight features of its row, from o0 and o1 on, such that it has both members
 // of eight rotated pairs (angles 8 l .. 8 l + 7) or sixteen features behind the rotated ones.
-template <typename T, bool kPaged, bool kInterleaved>
+template <typename T, bool kPaged, bool kInterleaved, bool kLong>
 __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a) {
   extern __shared__ __align__(16) float trig[];        // [tile][2][64] cosines and sines of the pairs
   __shared__ __align__(16) float w_s[2][kD];           // norm weights
@@ -101,21 +106,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
       ++ti;
     }
   };
-  uint4 v[kBatch][2] = {};
-  auto load = [&](int ti, int tr) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (ti < nt) {
-        const int t = t0 + ti;
-        const T* src = tr < nA ? reinterpret_cast<const T*>(a.A.p) + (int64_t)t * a.A.ts + (int64_t)tr * a.A.hs
-                               : reinterpret_cast<const T*>(a.B.p) + (int64_t)t * a.B.ts + (int64_t)(tr - nA) * a.B.hs;
-        v[k][0] = *reinterpret_cast<const uint4*>(src + o0);
-        v[k][1] = *reinterpret_cast<const uint4*>(src + o1);
-      }
-      advance(ti, tr);
-    }
+  uint4 v[kBatch<kLong>][2] = {};
+  int li = i, lr = r;        // the next row to load
+  auto load = [&](uint4* x) {
+    if (li >= nt) return;
+    const int t = t0 + li;
+    const T* src = lr < nA ? reinterpret_cast<const T*>(a.A.p) + (int64_t)t * a.A.ts + (int64_t)lr * a.A.hs
+                           : reinterpret_cast<const T*>(a.B.p) + (int64_t)t * a.B.ts + (int64_t)(lr - nA) * a.B.hs;
+    x[0] = *reinterpret_cast<const uint4*>(src + o0);
+    x[1] = *reinterpret_cast<const uint4*>(src + o1);
+    advance(li, lr);
   };
-  load(i, r);
+#pragma unroll
+  for (int k = 0; k < kBatch<kLong>; ++k) load(v[k]);
 
   static_assert(kThreads >= kD, "a thread a weight");
   if (normA && tid < kD) w_s[0][tid] = (float)reinterpret_cast<const T*>(a.A.w)[tid];
@@ -159,10 +162,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
   const uint32_t mask = 0xffu << (tid & 24);   // the lanes of a row, who take part in its sum
   for (;;) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (i >= nt) break;
+    for (int k = 0; k < kBatch<kLong>; ++k) {
+      if (i >= nt) return;
       const bool isA = r < nA;
       uint4 y0 = v[k][0], y1 = v[k][1];
+      if (kLong) load(v[k]);
       if (!kPaged || isA) {     // values of the append go out as they are
         uint64_t x[8];          // features o0 .. o0 + 7, o1 .. o1 + 7
         get8(T(), y0, x);
@@ -223,8 +227,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
       }
       advance(i, r);
     }
-    if (i >= nt) return;
-    load(i, r);
+    if (!kLong) return;
   }
 }
 
@@ -236,11 +239,15 @@ cudaError_t launch(jolt_dtype t, int tokens, RowsArgs a, int sms, cudaStream_t s
   const int nR = (int)nR64;
   // as many tokens as a tile's rows hold, fewer where that would leave the GPU without work
   a.tokens = tokens;
-  a.tile = std::max(1, std::min({kMaxTile, kSlots * kBatch / nR, tokens / (2 * sms)}));
+  a.tile = std::max(1, std::min({kMaxTile, kRows / nR, tokens / (2 * sms)}));
   const int grid = (tokens + a.tile - 1) / a.tile, bytes = a.tile * kD * (int)sizeof(float);
-  auto kernel = t == JOLT_BF16 ? (a.r.interleaved ? k_rope_rows<__nv_bfloat16, kPaged, true> : k_rope_rows<__nv_bfloat16, kPaged, false>)
-                               : (a.r.interleaved ? k_rope_rows<__half, kPaged, true> : k_rope_rows<__half, kPaged, false>);
-  return launch_early(kernel, dim3(grid), dim3(kThreads), bytes, 1, s, a);
+  auto go = [&](auto kernel) { return launch_early(kernel, dim3(grid), dim3(kThreads), bytes, 1, s, a); };
+  const bool bf16 = t == JOLT_BF16, turn = a.r.interleaved;
+  if (nR > kRows)
+    return bf16 ? (turn ? go(k_rope_rows<__nv_bfloat16, kPaged, true, true>) : go(k_rope_rows<__nv_bfloat16, kPaged, false, true>))
+                : (turn ? go(k_rope_rows<__half, kPaged, true, true>) : go(k_rope_rows<__half, kPaged, false, true>));
+  return bf16 ? (turn ? go(k_rope_rows<__nv_bfloat16, kPaged, true, false>) : go(k_rope_rows<__nv_bfloat16, kPaged, false, false>))
+              : (turn ? go(k_rope_rows<__half, kPaged, true, false>) : go(k_rope_rows<__half, kPaged, false, false>));
 }
 
 }  // namespace

@@ -694,3 +694,10 @@ def test_values_that_are_no_numbers_where_they_are_not_seen(J, dtype, kv, chunks
     ro, rl = attention_ref(clean, Q, SCALE, True)[:2]
     out[last], L[last] = ro[last].to(c.dtype), rl[last].float()
     check_attention(clean, Q, out, L, SCALE, True)
+
+
+@pytest.mark.parametrize("hq,hk", [(65, 0), (60, 5), (40, 40), (200, 3)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_tokens_of_many_rows(J, hq, hk, inter):
+    """Tokens of one row more than a CTA takes at once, and of several times as many."""
+    test_norm_rope(J, "bf16", 5, hq, hk, True, 128, inter, 4000)

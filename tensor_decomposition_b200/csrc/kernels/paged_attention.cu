@@ -161,20 +161,21 @@ size_t ml_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * 
 
 }  // namespace
 
-// Up to 16 rows of a chunk reading one KV head run in the kernel for few rows; 17 to 32 do where there are
-// few items or long caches (16 x 8 items of 20 rows: 21, 31, 53, 121 and 384 us for 128, 512, 2048, 8192 and
-// 32768 keys, in the other kernel 16, 23, 52, 144 and 533; 4 x 8 items: 12, 16, 24, 47, 114 and 16, 21, 24,
-// 53, 148). Where clusters of 8 CTAs, one for each item, all run at once (33 and more do not: 9.0 us
-// instead of 5.9) and their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0
+// Up to 8 rows of a chunk reading one KV head run in the kernel for few rows; 9 to 32 do where there are few
+// items and short caches, whose fewer steps to the first output count (32 items of 16 rows: 8.7, 9.3, 14.3, 32.7
+// and 98 us for 128, 512, 2048, 8192 and 32768 keys, in the other kernel 15.2, 16.7, 18.7, 35.7 and 93; of 20
+// rows: 12.1, 15.6, 23.7, 47, 120 and 15.3, 17.0, 18.8, 37, 95; 128 items of 16 rows: 17.5, 26.7, 43, 102, 338
+// and 16.6, 18.1, 35, 93, 326). Where clusters of 8 CTAs, one for each item, all run at once (33 and more
+// do not: 9.0 us instead of 5.9) and their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0
 // instead of 7.7 us at 1024 keys, 11.9 and 10.9 at 4096, 19.3 and 13.5 at 8192; 32 items: 26 instead of 32
 // at 8192).
-constexpr int kFewItems = 64, kFewTokens = 8192;
+constexpr int kFewItems = 32, kFewTokens16 = 8192, kFewTokens32 = 512;
 constexpr int kTeamTokens = 4096, kTeamItems = 32;
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   AttnPlan p;
   const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)std::min(a.b.max_q, a.b.total_q) * (a.Hq / a.b.heads);
   const int64_t items = (int64_t)a.b.heads * a.b.num_seqs;
-  p.decode = rows <= 16 || (rows <= 32 && (items <= kFewItems || tokens >= kFewTokens));
+  p.decode = rows <= 8 || (rows <= 32 && items <= kFewItems && tokens <= (rows <= 16 ? kFewTokens16 : kFewTokens32));
   p.rows = !p.decode ? 256 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   p.most = (int)std::max<int64_t>(1, std::min<int64_t>(rows, p.rows));
   const int fit = p.rows <= 16 ? kTeamItems : kTeamItems / 2;   // two CTAs an SM, or one

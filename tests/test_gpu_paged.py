@@ -701,3 +701,15 @@ def test_values_that_are_no_numbers_where_they_are_not_seen(J, dtype, kv, chunks
 def test_tokens_of_many_rows(J, hq, hk, inter):
     """Tokens of one row more than a CTA takes at once, and of several times as many."""
     test_norm_rope(J, "bf16", 5, hq, hk, True, 128, inter, 4000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("seqs,heads,g,n,kv", [
+    (2, 8, 4, 4, 400), (2, 8, 4, 4, 7000), (3, 8, 4, 3, 7900), (4, 8, 4, 4, 8000), (4, 8, 4, 4, 9000), (9, 8, 4, 4, 300),
+    (1, 8, 5, 4, 300), (2, 8, 4, 8, 500), (3, 8, 4, 8, 500), (4, 8, 4, 7, 510), (4, 8, 4, 7, 600), (5, 8, 4, 6, 200),
+])
+def test_nine_to_thirty_two_rows(J, dtype, seqs, heads, g, n, kv):
+    """Either side of the sizes where the kernel for few rows gives way to the other one."""
+    c = Cache([max(n, kv - 7 * s) for s in range(seqs)], [n - s % 2 for s in range(seqs)], heads, 16, _t(dtype), seed=n, pad=2)
+    _attend(J, c, heads * g, max_q=n)
+    _attend(J, c, heads * g, max_q=n, prefix=True, causal=False)

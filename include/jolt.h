@@ -195,7 +195,8 @@ JOLT_API jolt_status jolt_attention(jolt_stream_t stream, const void* Q, int32_t
  *   each row's sum of exponentials, as jolt_paged_attention takes them for a prefix: a model whose
  *   context is a compressed stream followed by tokens in pages attends to both with one call each.
  * Q: device bf16 [n_queries][q_heads][head_dim] of layer `layer`; out: device float32, same shape;
- *   lse: device float32 [n_queries][q_heads]. Otherwise as jolt_attention.
+ *   lse: device float32 [n_queries][q_heads]. Otherwise as jolt_attention: the queries are bf16 beside
+ *   pages of F16 too, and have to be rounded for it there.
  */
 JOLT_API jolt_status jolt_attention_lse(jolt_stream_t stream, int32_t layer, const void* Q, int32_t q_heads,
                                         int32_t n_queries, float scale, float* out, float* lse, void* cuda_stream);

@@ -167,8 +167,9 @@ class Plan:
 
 
 class Stream:
-    def __init__(self, handle, plan=None, keep=()):
+    def __init__(self, handle, plan=None, keep=(), layers=None):
         self.handle, self.plan, self._keep = handle, plan, keep
+        self.layers = plan.shape.layers if plan is not None else layers
 
     def __del__(self):
         if getattr(self, "handle", None):
@@ -245,7 +246,7 @@ def jolt_stream_from_host(data: bytes, cuda_stream=None) -> Stream:
     h = ctypes.c_void_p()
     buf = ctypes.create_string_buffer(data, len(data))
     _check(_lib.jolt_stream_from_host(buf, len(data), _stream_ptr(cuda_stream), ctypes.byref(h)))
-    return Stream(h)
+    return Stream(h, layers=struct.unpack_from("<i", data, 16)[0])   # of the header that was just checked
 
 
 def jolt_export_debug(stream: Stream, what: int, lt: int = 0) -> np.ndarray:
@@ -310,18 +311,33 @@ def jolt_selftest_eig_dense(A, R, V, lam, cuda_stream=None):
                                         _stream_ptr(cuda_stream)))
 
 
+def _attention_tensors(Q, out, lse=None):
+    """Bf16 queries and float32 results, rows of 128, on the current device: the library reads and writes them as
+    these whatever they are."""
+    import torch
+    _here(Q.get_device(), torch)
+    if Q.shape[-1] != 128:
+        raise ValueError("the rows of Q must have 128 features")
+    _array(Q, "Q", Q.shape, torch.bfloat16, Q.get_device())
+    _array(out, "out", Q.shape, torch.float32, Q.get_device())
+    _array(lse, "lse", Q.shape[:2], torch.float32, Q.get_device())
+
+
 def jolt_attention(stream: Stream, Q, out, scale: float, cuda_stream=None):
     """Q: bf16 CUDA tensor [layers][q_heads][n][head_dim]; out: float32 CUDA tensor of the same shape."""
-    if Q.dim() != 4 or tuple(out.shape) != tuple(Q.shape):
+    if Q.dim() != 4 or tuple(out.shape) != tuple(Q.shape) or Q.shape[0] != stream.layers:
         raise ValueError("Q and out must be [layers][q_heads][n][head_dim] of the same shape")
+    _attention_tensors(Q, out)
     _check(_lib.jolt_attention(stream.handle, _dptr(Q), int(Q.shape[1]), int(Q.shape[2]), float(scale), _dptr(out),
                                _stream_ptr(cuda_stream)))
 
 
 def jolt_attention_lse(stream: Stream, layer: int, Q, out, lse, scale: float, cuda_stream=None):
-    """Q: bf16 CUDA tensor [n][q_heads][head_dim] of one layer; out: float32, same shape; lse: float32 [n][q_heads]."""
+    """Q: bf16 CUDA tensor [n][q_heads][head_dim] of one layer; out: float32, same shape; lse: float32 [n][q_heads].
+    (The queries of fp16 pages have to be rounded to bf16 for it.)"""
     if Q.dim() != 3 or tuple(out.shape) != tuple(Q.shape) or tuple(lse.shape) != tuple(Q.shape[:2]):
         raise ValueError("Q and out must be [n][q_heads][head_dim] of the same shape and lse [n][q_heads]")
+    _attention_tensors(Q, out, lse)
     _check(_lib.jolt_attention_lse(stream.handle, int(layer), _dptr(Q), int(Q.shape[1]), int(Q.shape[0]), float(scale),
                                    _dptr(out), _dptr(lse), _stream_ptr(cuda_stream)))
 

@@ -44,7 +44,7 @@ constexpr float kFollow = 8.0f;
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full[2], q_empty[2], s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
-  uint64_t tail;
+  uint64_t tail, drain;
 };
 
 __device__ __forceinline__ int blocks_of(const SeqView& v, const Divisor& g) {
@@ -247,6 +247,19 @@ __device__ __noinline__ void show_values(const PagedAttnArgs& a, const Piece& p,
   }
 }
 
+// Where a wait gave up, copies and products in flight end before the CTA's memory and its Tensor Memory are given
+// up; never in a run that ends well, so kept out of the kernel's code. Copies: those of the ring's last stages, and of
+// a tile that was to be looked over.
+__device__ __noinline__ void land(uint64_t* full, uint32_t kv, uint64_t* tail, uint32_t tails) {
+  if (tails) mbar_wait(tail, (tails - 1) & 1, 1u << 20);
+  const uint32_t n = min(kv, (uint32_t)kStages);
+  for (uint32_t i = kv - n; i < kv; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1, 1u << 20);
+}
+__device__ __noinline__ void drain(uint64_t* bar) {
+  umma_commit(bar);
+  mbar_wait(bar, 0, 1u << 20);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_chunk(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws, int box) {
@@ -279,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.o_empty[t], kSoftmaxWarps / 2);
     }
     mbar_init(&bar.tail, 1);
+    mbar_init(&bar.drain, 1);
     gave_up = 0;
     fence_barrier_init();
     prefetch_tensormap(&maps.K);
@@ -457,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } while (ok && next(p, b, g, causal));
+        if (!ok) drain(&bar.drain);
       }
     } else if (warp == kSoftmaxWarps + 1) {
       // ---------------------------------------------------------------- keys and values
@@ -536,10 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       } while (ok && next_of_warp(p, b, g, causal, lane));
-      if (!ok) {   // copies in flight land before the CTA's memory is given up
-        const uint32_t n = min(kv, (uint32_t)kStages);
-        for (uint32_t i = kv - n; i < kv; ++i) mbar_wait(&bar.kv_full[i % kStages], (i / kStages) & 1, 1u << 20);
-      }
+      if (!ok) land(bar.kv_full, kv, &bar.tail, tails);
     } else {
       // ---------------------------------------------------------------- queries: a warp a half block
       Piece& p = piece_s[warp];

@@ -398,6 +398,12 @@ struct Block8 {
   }
 };
 
+// The fills from .. to - 1 of a ring's stages, waited for once more; never in a run that ends well, so kept out of the
+// kernel's registers.
+__device__ __noinline__ void land(uint64_t* full, int stages, int from, int to) {
+  for (int k = from; k < to; ++k) mbar_wait(&full[k % stages], (k / stages) & 1, 1u << 20);
+}
+
 // kTeam: instead of a share of the line a CTA takes an eighth of the item of its cluster, and the cluster's
 // CTAs combine through one another's shared memory: one launch and no scratch.
 template <typename T, int kT, bool kTeam>
@@ -418,7 +424,10 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
   const int g = a.g.d;
   const float scale2 = a.scale * kLog2e;
   grid_release();
-  if (tid < kSlices * kDeep) mbar_init(&full_s[0][0] + tid, 1);
+  if (tid < kSlices * kDeep) {
+    mbar_init(&full_s[0][0] + tid, 1);
+    (&valid_s[0][0])[tid] = kKeys;     // also of a stage that is never filled, when a wait has given up
+  }
   if (tid == 0) {
     gave_up = 0;
     fence_barrier_init();
@@ -499,8 +508,12 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
 
   for (int i = 0; i < count; ++i) {
     const int stage = i % kDeep;
-    wait(&full_s[warp][stage], (i / kDeep) & 1);   // void results are reported where it gives up
-    __syncwarp();
+    // Where a wait gives up, the warp's copies in flight land (or are waited for as long again) and no stage is filled
+    // after it: the result is void, and reported. The barriers of the items' ends need the warp all the same.
+    if (!__all_sync(0xffffffffu, wait(&full_s[warp][stage], (i / kDeep) & 1))) {
+      land(full_s[warp], kDeep, i, issued);
+      issued = count;
+    }
     issue((i + kDeep - 1) % kDeep);
     if (fresh) {
       fresh = false;
@@ -601,8 +614,6 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
     }
     if (i + 1 < count) advance(cc, b);
   }
-  if (*wait.gave_up)   // copies in flight land before the CTA's memory is given up
-    for (int i = max(0, count - kDeep); i < count; ++i) mbar_wait(&full_s[warp][i % kDeep], (i / kDeep) & 1, 1u << 20);
   if (!kTeam) {
     if (tid == 0) ws.list[blockIdx.x] = split;
     return;

@@ -222,7 +222,8 @@ JOLT_API jolt_status jolt_attention_lse(jolt_stream_t stream, int32_t layer, con
  *
  * What the host cannot check is checked on the device and reported by jolt_pages_status: a sequence
  * whose bounds do not fit (offsets that fall or leave [0, total_q], more than max_q tokens, kv_len
- * outside [0, max_pages * page_size]) is skipped, a table entry that is no page of the set is never
+ * outside [0, max_pages * page_size]) is skipped (a token that others then claim together is appended for
+ * the last of them, and its attention is void), a table entry that is no page of the set is never
  * followed (its keys count as zeros in attention and are not written by append). Entries behind
  * the pages of kv_len tokens are not read and may hold anything, and so may the rows of the last
  * page behind kv_len. A key or value that is no finite number shows in the rows that see it alone

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
   extern __shared__ __align__(16) float trig[];        // [tile][2][64] cosines and sines of the pairs
   __shared__ __align__(16) float w_s[2][kD];           // norm weights
   __shared__ int64_t dst_s[kMaxTile];                  // append: page row in elements from the pages' base; < 0: none
-  __shared__ int pos_s[kMaxTile], seq_s[kMaxTile];     // append: place in the cache, sequence (-1: none)
+  __shared__ int seq_s[kMaxTile];                      // append: sequence (-1: none)
   grid_release();
   grid_wait();
   const int tid = threadIdx.x, slot = tid / kLanes, l = tid % kLanes;
@@ -123,6 +123,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
   static_assert(kThreads >= kD, "a thread a weight");
   if (normA && tid < kD) w_s[0][tid] = (float)reinterpret_cast<const T*>(a.A.w)[tid];
   if (normB && tid < kD) w_s[1][tid] = (float)reinterpret_cast<const T*>(a.B.w)[tid];
+  // place in its sequence's cache of token t of the tile, below 0 for none (the arrays are in L1 by then)
+  auto place = [&](int t) {
+    const int s = seq_s[t];
+    return s < 0 ? -1 : a.b.kv_len[s] - (a.b.q_start[s + 1] - (t0 + t));
+  };
   if (kPaged) {
     if (tid < kMaxTile) seq_s[tid] = -1;
     __syncthreads();
@@ -131,18 +136,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
       if (q0 >= t0 + nt || q1 <= t0) continue;
       const SeqView sv = seq_view(a.b, s);
       if (sv.n == 0) continue;
-      for (int t = max(q0, t0); t < min(q1, t0 + nt); ++t) {
-        seq_s[t - t0] = s;
-        pos_s[t - t0] = sv.len - (q1 - t);
-      }
+      // offsets that fall let several sequences claim a token: the last has it, and its place comes from that one alone
+      for (int t = max(q0, t0); t < min(q1, t0 + nt); ++t) atomicMax(&seq_s[t - t0], s);
     }
     __syncthreads();
     if (tid >= kThreads - nt) {   // not the first threads: they have angles to make
-      const int t = tid - (kThreads - nt), s = seq_s[t];
+      const int t = tid - (kThreads - nt), pos = place(t);
       int64_t d = -1;
-      if (s >= 0 && pos_s[t] >= 0) {
-        const int pg = page_of(a.b, s, pos_s[t]);
-        if (pg >= 0) d = ((int64_t)pg * a.b.heads * a.b.page_size + pos_s[t] - a.b.by_page.quot(pos_s[t]) * a.b.page_size) * kD;
+      if (pos >= 0) {
+        const int pg = page_of(a.b, seq_s[t], pos);
+        if (pg >= 0) d = ((int64_t)pg * a.b.heads * a.b.page_size + pos - a.b.by_page.quot(pos) * a.b.page_size) * kD;
       }
       dst_s[t] = d;
     }
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
   if (rot) {
     for (int u = tid; u < nt * h; u += kThreads) {
       const int t = u / h, f = u - t * h;
-      const int pos = kPaged && !a.r.positions ? (seq_s[t] >= 0 ? pos_s[t] : 0) : a.r.positions[t0 + t];
+      const int pos = kPaged && !a.r.positions ? place(t) : a.r.positions[t0 + t];
       // parts of a turn, in float64 up to the last whole turn
       double turn = (double)pos * ((double)a.r.inv_freq[f] * 0.15915494309189533577);
       turn -= rint(turn);

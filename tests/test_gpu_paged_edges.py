@@ -1,0 +1,73 @@
+"""Where the growing cache's operators can go wrong without a shape that looks odd: bad offsets that fall, reports made
+while another stream works, weights far below the largest, prefixes that hold no number, precision. Bounds are derived
+beside the tests, from paged_common's where nothing is said."""
+import math
+
+import pytest
+
+from paged_common import D, Cache, check_attention, half_step
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / math.sqrt(D)
+
+
+@pytest.fixture(scope="module")
+def J():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from tensor_decomposition_b200 import build
+    build.build()
+    from tensor_decomposition_b200 import jolt
+    return jolt
+
+
+def _t(name):
+    import torch
+    return torch.bfloat16 if name == "bf16" else torch.float16
+
+
+def _reported(J, pages, **kw):
+    """What jolt_pages_status says, or nothing."""
+    try:
+        J.jolt_pages_status(pages, **kw)
+    except J.JoltError as e:
+        assert e.status == 1
+        return str(e)
+    return ""
+
+
+def test_append_of_tokens_that_two_sequences_claim(J):
+    """Offsets that fall make the sequences around them overlap. Each token is then appended for one of them, the
+    last, at the place that this one has for it: never by one's table and another's position, whose table entry may
+    lie behind the sequence's pages and name a page of someone else."""
+    import torch
+    S, n, page = 301, 40, 16
+    kv = [n + 16 * (s % 7) for s in range(S)]
+    own = [(t + page - 1) // page for t in kv]
+    cols = max(own)
+    table = torch.zeros((S, cols), dtype=torch.int32)
+    at = 0
+    for s in range(S):
+        table[s, :own[s]] = torch.arange(at, at + own[s])
+        table[s, own[s]:] = sum(own)                      # not among the sequence's pages: a page of someone else
+        at += own[s]
+    K = torch.zeros((at + 1, 1, page, D), dtype=torch.bfloat16, device="cuda")
+    V = torch.zeros_like(K)
+    pages = J.jolt_pages_create(K, V)
+    starts = [0 if s % 2 == 0 else n for s in range(S + 1)]       # 0 40 0 40 ...: every other sequence falls
+    batch = J.jolt_batch(torch.tensor(starts, dtype=torch.int32, device="cuda"),
+                         torch.tensor(kv, dtype=torch.int32, device="cuda"), table.cuda(), n, n)
+    last = S - 1
+    assert starts[last] == 0 and starts[S] == n
+    pos = torch.arange(kv[last] - n, kv[last])
+    want_p, want_r = table[last][pos // page].long().cuda(), (pos % page).cuda()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for _ in range(200):
+        x = torch.randn((n, 2, D), generator=g, device="cuda").to(torch.bfloat16)
+        K.zero_(), V.zero_()
+        J.jolt_paged_append(pages, batch, x[:, :1], x[:, 1:])
+        _reported(J, pages)
+        for X, new in ((K, x[:, 0]), (V, x[:, 1])):
+            assert torch.equal(X[want_p, 0, want_r], new)
+            X[want_p, 0, want_r] = 0
+            assert not X.any(), X.flatten(1).any(1).nonzero()[:4].tolist()

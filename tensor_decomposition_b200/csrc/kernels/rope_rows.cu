@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_rope_rows(const RowsArgs a)
     __syncthreads();
     for (int s = tid; s < a.b.num_seqs; s += kThreads) {
       const int q0 = a.b.q_start[s], q1 = a.b.q_start[s + 1];
-      if (q0 >= t0 + nt || q1 <= t0) continue;
+      // (the first CTA looks at all of them, so that one whose bounds fit no tile is reported too)
+      if (blockIdx.x != 0 && (q0 >= t0 + nt || q1 <= t0)) continue;
       const SeqView sv = seq_view(a.b, s);
       if (sv.n == 0) continue;
       // offsets that fall let several sequences claim a token: the last has it, and its place comes from that one alone

@@ -71,3 +71,26 @@ def test_append_of_tokens_that_two_sequences_claim(J):
             assert torch.equal(X[want_p, 0, want_r], new)
             X[want_p, 0, want_r] = 0
             assert not X.any(), X.flatten(1).any(1).nonzero()[:4].tolist()
+
+
+@pytest.mark.parametrize("starts,kv,total", [
+    ([0, 3, 1, 4], [9, 9, 9], 4),            # an offset that falls between two tokens
+    ([0, 4, 9], [9, 9], 4),                  # a sequence wholly behind the batch's rows
+    ([0, 4, -3], [9, 9], 4),
+    ([0, 4, 4], [9, -5], 4),                 # a length below zero, or beyond the table, of a sequence without tokens
+    ([0, 4, 4], [9, 17], 4),
+])
+def test_append_reports_what_attention_reports(J, starts, kv, total):
+    import torch
+    K = torch.zeros((8, 2, 16, D), dtype=torch.bfloat16, device="cuda")
+    V = torch.zeros_like(K)
+    pages = J.jolt_pages_create(K, V)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = J.jolt_batch(torch.tensor(starts, **i32), torch.tensor(kv, **i32), torch.arange(len(kv), **i32)[:, None].contiguous(),
+                         total, total)
+    x = torch.ones((total, 2, D), dtype=torch.bfloat16, device="cuda")
+    J.jolt_paged_append(pages, batch, x, x)
+    assert "q_start or kv_len" in _reported(J, pages)
+    assert not _reported(J, pages)
+    J.jolt_paged_attention(pages, batch, x, torch.empty_like(x), SCALE)
+    assert "q_start or kv_len" in _reported(J, pages)

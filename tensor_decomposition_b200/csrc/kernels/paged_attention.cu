@@ -155,11 +155,19 @@ cudaError_t combine(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& 
   return launch_early(k_attn_combine_blocks<T>, dim3(p.grid, (p.most + 31) / 32), dim3(32 * kBlockWarps), 0, 1, s, a, w);
 }
 
+__global__ void k_take_status(int32_t* word, int32_t* out) { *out = atomicExch(word, 0); }
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 size_t o_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * kD * sizeof(float)); }
 size_t ml_bytes(const AttnPlan& p) { return up256((size_t)p.grid * 2 * p.rows * sizeof(float2)); }
 
 }  // namespace
+
+cudaError_t take_status(int32_t* word, int32_t* out, cudaStream_t s) {
+  k_take_status<<<1, 1, 0, s>>>(word, out);
+  note_launch();
+  return cudaGetLastError();
+}
 
 // Up to 8 rows of a chunk reading one KV head run in the kernel for few rows; 9 to 32 do where there are few
 // items and short caches, whose fewer steps to the first output count (32 items of 16 rows: 8.7, 9.3, 14.3, 32.7

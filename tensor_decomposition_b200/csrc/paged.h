@@ -75,6 +75,9 @@ __device__ __forceinline__ int page_of(const BatchView& b, int s, int pos) {
   return p;
 }
 
+// *out = *word; *word = 0, in one step.
+cudaError_t take_status(int32_t* word, int32_t* out, cudaStream_t s);
+
 // Allow a kernel its dynamic shared memory, once a device (`done`: the kernel's own flags).
 struct SmemFlags {
   std::atomic<bool> on[64] = {};

@@ -235,8 +235,14 @@ JOLT_API jolt_status jolt_pages_status(jolt_pages_t p, void* cuda_stream) {
   if (jolt_status st = check_device("jolt_pages_status", p)) return st;
   cudaStream_t s = (cudaStream_t)cuda_stream;
   int32_t w = 0;
-  cudaError_t e = cudaMemcpyAsync(&w, p->d_status, sizeof(w), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(p->d_status, 0, sizeof(w), s);
+  void* got = nullptr;
+  cudaError_t e = host_pool_malloc(&got, sizeof(w), s);
+  if (e == cudaSuccess) {   // read and cleared in one: kernels on other streams may be reporting
+    e = take_status(p->d_status, static_cast<int32_t*>(got), s);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&w, got, sizeof(w), cudaMemcpyDeviceToHost, s);
+    const cudaError_t e2 = cudaFreeAsync(got, s);
+    if (e == cudaSuccess) e = e2;
+  }
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail("jolt_pages_status", e);
   if (w & PST_TIMEOUT) return host_fail(JOLT_ERR_TIMEOUT, "a bounded device wait of paged attention gave up");

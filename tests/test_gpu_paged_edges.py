@@ -94,3 +94,27 @@ def test_append_reports_what_attention_reports(J, starts, kv, total):
     assert not _reported(J, pages)
     J.jolt_paged_attention(pages, batch, x, torch.empty_like(x), SCALE)
     assert "q_start or kv_len" in _reported(J, pages)
+
+
+def test_no_report_is_lost_to_another_stream(J):
+    """A batch is found wrong on one stream while the reports are fetched on another: each is seen once."""
+    import torch
+    c = Cache([40], [1], 1, 16, torch.bfloat16, poison=False)
+    pages, batch = c.handles(J)
+    c.kv_len.fill_(-1)
+    x = c.randn(1, 1, D)
+    work, ask = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    lost = 0
+    for i in range(4000):
+        with torch.cuda.stream(work):
+            torch.cuda._sleep(500 * (i % 64))            # up to 16 us: the report falls anywhere into the fetching
+            J.jolt_paged_append(pages, batch, x, x)
+        done = work.record_event()
+        seen = 0
+        while not done.query():
+            seen += bool(_reported(J, pages, cuda_stream=ask))
+        seen += bool(_reported(J, pages, cuda_stream=ask))
+        lost += seen == 0
+        assert seen <= 1
+    assert lost == 0

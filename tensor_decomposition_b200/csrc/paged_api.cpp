@@ -1,6 +1,7 @@
 // Host side of the growing cache (include/jolt.h): page sets, argument checks and launches.
 #include <algorithm>
 #include <atomic>
+#include <cstdio>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -245,11 +246,15 @@ JOLT_API jolt_status jolt_pages_status(jolt_pages_t p, void* cuda_stream) {
   }
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail("jolt_pages_status", e);
-  if (w & PST_TIMEOUT) return host_fail(JOLT_ERR_TIMEOUT, "a bounded device wait of paged attention gave up");
-  if (w & PST_BAD_BATCH)
-    return host_fail(JOLT_ERR_INVALID_ARG, "a sequence's q_start or kv_len does not fit its batch (the sequence was skipped)");
-  if (w & PST_BAD_PAGE)
-    return host_fail(JOLT_ERR_INVALID_ARG, "a page table names a page outside the set (it was not followed)");
+  if (w) {
+    const char* found[3] = {w & PST_TIMEOUT ? "a bounded device wait of paged attention gave up; " : "",
+                            w & PST_BAD_BATCH ? "a sequence's q_start or kv_len does not fit its batch (the sequence was skipped); " : "",
+                            w & PST_BAD_PAGE ? "a page table names a page outside the set (it was not followed); " : ""};
+    char all[256];
+    const int n = snprintf(all, sizeof(all), "%s%s%s", found[0], found[1], found[2]);
+    all[n - 2] = 0;   // the last separator
+    return host_fail(w & PST_TIMEOUT ? JOLT_ERR_TIMEOUT : JOLT_ERR_INVALID_ARG, "%s", all);
+  }
   return JOLT_OK;
 }
 

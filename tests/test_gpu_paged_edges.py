@@ -118,3 +118,15 @@ def test_no_report_is_lost_to_another_stream(J):
         lost += seen == 0
         assert seen <= 1
     assert lost == 0
+
+
+def test_a_report_names_all_that_was_found(J):
+    import torch
+    c = Cache([40, 40], [1, 1], 1, 16, torch.bfloat16, poison=False)
+    pages, batch = c.handles(J)
+    c.kv_len[0] = -1
+    c.table[1] = -3
+    x = c.randn(2, 1, D)
+    J.jolt_paged_append(pages, batch, x, x)
+    said = _reported(J, pages)
+    assert "q_start or kv_len" in said and "page table" in said

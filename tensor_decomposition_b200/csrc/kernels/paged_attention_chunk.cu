@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.pre_lse) {
           const float pl = a.pre_lse[row] * kLog2e, mn = fmaxf(m, pl);
           inv = rescale(m, mn);
-          w = rescale(pl, mn);
+          w = pl == -INFINITY ? 0.0f : ex2(pl - mn);   // one that is no number stays so, also without keys
           l = fmaf(l, inv, w);
           m = mn;
         }

@@ -130,3 +130,25 @@ def test_a_report_names_all_that_was_found(J):
     J.jolt_paged_append(pages, batch, x, x)
     said = _reported(J, pages)
     assert "q_start or kv_len" in said and "page table" in said
+
+
+@pytest.mark.parametrize("kv,chunks", [([0, 40], [1, 1]), ([0, 40], [5, 5]), ([0, 40], [40, 40]), ([0, 400], [300, 300]),
+                                       ([0, 9000], [1, 1])])
+def test_a_prefix_that_is_no_number_shows(J, kv, chunks):
+    """A log-sum-exp of a prefix that is no number makes its row none, also a row that has no keys."""
+    import torch
+    c = Cache(kv, chunks, 2, 16, torch.bfloat16, seed=3)
+    Q, out = c.randn(c.total, 8, D), torch.zeros((c.total, 8, D), dtype=c.dtype, device="cuda")
+    L = torch.zeros((c.total, 8), device="cuda")
+    po, pl = c.randn(c.total, 8, D, dtype=torch.float32), c.randn(c.total, 8, dtype=torch.float32)
+    rows = [0, c.starts[1] - 1, c.starts[1], c.total - 1]
+    pl[rows, 3] = math.nan
+    pages, batch = c.handles(J)
+    J.jolt_paged_attention(pages, batch, Q, out, SCALE, lse=L, prefix_out=po, prefix_lse=pl)
+    J.jolt_pages_status(pages)
+    assert torch.isnan(out[rows, 3].float()).all() and torch.isnan(L[rows, 3]).all()
+    pl[rows, 3] = 0.5
+    good, G = torch.zeros_like(out), torch.zeros_like(L)
+    J.jolt_paged_attention(pages, batch, Q, good, SCALE, lse=G, prefix_out=po, prefix_lse=pl)
+    out[rows, 3], L[rows, 3] = good[rows, 3], G[rows, 3]
+    assert torch.equal(out, good) and torch.equal(L, G)

@@ -321,7 +321,7 @@ JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* bat
  *   jolt_attention: for token i of a chunk of n and query head j reading KV head j / (q_heads / heads),
  *       out = sum_t e^(s_t) V[t] / sum_t e^(s_t),  s_t = scale * Q . K[t],
  *   over t <= kv_len - n + i (causal) or all t < kv_len (causal = 0). The chunk's own keys have to be
- *   appended before. prefix_out, prefix_lse: the attention of the same queries over another part of
+ *   appended before. scale: any finite number. prefix_out, prefix_lse: the attention of the same queries over another part of
  *   the context and the log of its sum of exponentials (both or neither): joined as a term
  *   e^(prefix_lse) of value prefix_out. A row without keys gets out = 0 and lse = -inf.
  *   Where a row's keys are divided between CTAs depends on all lengths of the batch, so a row's last

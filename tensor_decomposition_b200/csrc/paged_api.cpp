@@ -1,6 +1,7 @@
 // Host side of the growing cache (include/jolt.h): page sets, argument checks and launches.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <mutex>
 #include <new>
@@ -332,6 +333,7 @@ JOLT_API jolt_status jolt_paged_attention(jolt_pages_t pages, const jolt_batch* 
                      pages->shape.heads);
   if ((int64_t)batch->total_q * q.q_heads > INT32_MAX - 1024)
     return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 query rows", what);
+  if (!std::isfinite(q.scale)) return host_fail(JOLT_ERR_INVALID_ARG, "%s: the scale is no finite number", what);
   if (!q.prefix_out != !q.prefix_lse)
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: prefix_out and prefix_lse come together", what);
   if (batch->total_q == 0 || batch->num_seqs == 0) return JOLT_OK;

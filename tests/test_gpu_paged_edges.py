@@ -152,3 +152,17 @@ def test_a_prefix_that_is_no_number_shows(J, kv, chunks):
     J.jolt_paged_attention(pages, batch, Q, good, SCALE, lse=G, prefix_out=po, prefix_lse=pl)
     out[rows, 3], L[rows, 3] = good[rows, 3], G[rows, 3]
     assert torch.equal(out, good) and torch.equal(L, G)
+
+
+@pytest.mark.parametrize("chunks", [[1, 1], [40, 9]])
+def test_a_scale_that_is_no_finite_number_is_refused(J, chunks):
+    import torch
+    c = Cache([100, 60], chunks, 2, 16, torch.bfloat16, seed=1)
+    Q = c.randn(c.total, 8, D)
+    pages, batch = c.handles(J)
+    before = J.jolt_launch_count()
+    for scale in (math.nan, math.inf, -math.inf):
+        with pytest.raises(J.JoltError) as e:
+            J.jolt_paged_attention(pages, batch, Q, torch.empty_like(Q), scale)
+        assert e.value.status == 1 and "scale" in str(e.value)
+    assert J.jolt_launch_count() == before

@@ -185,7 +185,7 @@ JOLT_API jolt_status jolt_decode(jolt_stream_t stream, void* K_out, void* V_out,
  * Q: device bf16 [layers][q_heads][n_queries][head_dim]; out: device float32, same shape. The
  *   stream must hold K and V (bf16). Enqueued on `cuda_stream`; takes scratch from the library's
  *   memory pool. Errors: INVALID_ARG (null pointers, q_heads not a multiple of the KV heads, no V),
- *   UNSUPPORTED (float32 streams).
+ *   UNSUPPORTED (float32 streams; more than 65535 / layers groups of four query rows a KV head).
  */
 JOLT_API jolt_status jolt_attention(jolt_stream_t stream, const void* Q, int32_t q_heads, int32_t n_queries,
                                     float scale, float* out, void* cuda_stream);
@@ -196,7 +196,8 @@ JOLT_API jolt_status jolt_attention(jolt_stream_t stream, const void* Q, int32_t
  *   context is a compressed stream followed by tokens in pages attends to both with one call each.
  * Q: device bf16 [n_queries][q_heads][head_dim] of layer `layer`; out: device float32, same shape;
  *   lse: device float32 [n_queries][q_heads]. Otherwise as jolt_attention: the queries are bf16 beside
- *   pages of F16 too, and have to be rounded for it there.
+ *   pages of F16 too, and have to be rounded for it there, and any number of them is taken, some at a
+ *   time in 128 MB of scratch (more only where one query row's share of a long stream needs it).
  */
 JOLT_API jolt_status jolt_attention_lse(jolt_stream_t stream, int32_t layer, const void* Q, int32_t q_heads,
                                         int32_t n_queries, float scale, float* out, float* lse, void* cuda_stream);

@@ -1493,20 +1493,41 @@ static jolt_status stream_attention(const char* what, jolt_stream_t st, const vo
     return fail(JOLT_ERR_INVALID_ARG, "%s: q_heads must be a positive multiple of the %d KV heads", what, st->H);
   cudaStream_t s = (cudaStream_t)cuda_stream;
   AttnArgs a;
-  a.L = layers; a.H = st->H; a.T = st->T; a.D = st->D; a.Hq = q_heads; a.n = n_queries; a.R = std::max(st->R, 1);
+  a.L = layers; a.H = st->H; a.T = st->T; a.D = st->D; a.Hq = q_heads; a.R = std::max(st->R, 1);
   a.layer0 = layer0; a.token_major = token_major;
   a.scale = scale; a.meta = st->d_meta; a.body = st->d_body; a.Pi = st->d_Pi;
-  a.Q = reinterpret_cast<const __nv_bfloat16*>(Q); a.out = out; a.lse = lse;
-  a.nchunk = attn_chunks(st->T); a.ngroups = attn_groups(q_heads, st->H, n_queries);
-  const size_t nqv = (size_t)a.L * q_heads * n_queries;
-  const size_t floats = nqv * (kD + a.R) + (size_t)a.L * a.H * a.nchunk * a.ngroups * attn_part_floats(a.R);
+  a.nchunk = attn_chunks(st->T);
+  // Queries token by token are taken some at a time, so that the scratch, which grows with them, and the groups of
+  // queries, a dimension of the grid, stay bounded (a row's arithmetic is the same in any group).
+  auto scratch_of = [&](int n) {
+    const size_t nqv = (size_t)layers * q_heads * n;
+    return (nqv * (kD + a.R) + (size_t)layers * a.H * a.nchunk * attn_groups(q_heads, a.H, n) * attn_part_floats(a.R)) * sizeof(float);
+  };
+  constexpr size_t kScratch = 128 << 20;
+  constexpr int64_t kGroups = 65535;
+  const int64_t per_head = q_heads / a.H;
+  int step = n_queries;
+  if (token_major)
+    step = std::max(1, (int)std::min({(int64_t)n_queries, 4 * kGroups / per_head, (int64_t)(64 * kScratch / scratch_of(64))}));
+  if ((per_head * step + 3) / 4 * layers > kGroups)
+    return fail(JOLT_ERR_UNSUPPORTED, "%s: %d queries of %d heads over %d KV heads and %d layers in one call", what, n_queries,
+                q_heads, a.H, layers);
   float* scratch = nullptr;
   PROF("attention", s);
-  CK(pool_malloc(&scratch, floats * sizeof(float), s));
-  a.qpi = scratch;
-  a.qhat = scratch + nqv * kD;
-  a.part = a.qhat + nqv * a.R;
-  cudaError_t e = attention(a, s);
+  CK(pool_malloc(&scratch, scratch_of(step), s));
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < n_queries && e == cudaSuccess; i += step) {
+    a.n = std::min(step, n_queries - i);
+    const int64_t row = (int64_t)i * q_heads, nqv = (int64_t)layers * q_heads * a.n;
+    a.Q = reinterpret_cast<const __nv_bfloat16*>(Q) + row * kD;
+    a.out = out + row * kD;
+    a.lse = lse ? lse + row : nullptr;
+    a.ngroups = attn_groups(q_heads, a.H, a.n);
+    a.qpi = scratch;
+    a.qhat = a.qpi + nqv * kD;
+    a.part = a.qhat + nqv * a.R;
+    e = attention(a, s);
+  }
   cudaError_t e2 = cudaFreeAsync(scratch, s);
   if (e == cudaSuccess) e = e2;
   if (e != cudaSuccess) return fail(JOLT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));

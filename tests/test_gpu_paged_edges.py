@@ -166,3 +166,43 @@ def test_a_scale_that_is_no_finite_number_is_refused(J, chunks):
             J.jolt_paged_attention(pages, batch, Q, torch.empty_like(Q), scale)
         assert e.value.status == 1 and "scale" in str(e.value)
     assert J.jolt_launch_count() == before
+
+
+def _stream(J, tokens, heads):
+    import synth
+    from gpu_common import gpu_encode
+    cfg = synth.config(1, layers=2, tokens=tokens, heads=heads, seed=1709, groups=2)
+    K, V = synth.gen_cache_numpy(cfg)
+    return gpu_encode(cfg, K, V, synth.bf16_bytes(cfg) // 2, "sketch")[1]
+
+
+def test_attention_over_a_stream_of_many_queries(J):
+    """As many queries as a grid's dimension does not hold groups of, in bounded scratch; each row as in a call of few."""
+    import torch
+    st = _stream(J, 300, 1)
+    n, hq = 65536 + 77, 4
+    g = torch.Generator(device="cuda").manual_seed(4)
+    Q = torch.randn((n, hq, D), generator=g, device="cuda").to(torch.bfloat16)
+    out, L = torch.full((n, hq, D), math.nan, device="cuda"), torch.full((n, hq), math.nan, device="cuda")
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    J.jolt_attention_lse(st, 1, Q, out, L, SCALE)
+    torch.cuda.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] <= 400 << 20
+    for at in (0, 5, 1023, 30000, n - 9):
+        o, l = torch.empty((9, hq, D), device="cuda"), torch.empty((9, hq), device="cuda")
+        J.jolt_attention_lse(st, 1, Q[at:at + 9], o, l, SCALE)
+        assert torch.equal(o, out[at:at + 9]) and torch.equal(l, L[at:at + 9])
+    assert torch.isfinite(out).all() and torch.isfinite(L).all()
+
+
+def test_attention_over_a_stream_beyond_its_grid_is_refused(J):
+    """All layers at once, more groups of queries than the grid's third dimension holds: refused before any launch."""
+    import torch
+    st = _stream(J, 300, 1)
+    Q = torch.zeros((2, 4, 32768, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(Q.shape, device="cuda")
+    before = J.jolt_launch_count()
+    with pytest.raises(J.JoltError) as e:
+        J.jolt_attention(st, Q, out, SCALE)
+    assert e.value.status == 9 and J.jolt_launch_count() == before

@@ -461,6 +461,8 @@ def jolt_qk_norm_rope(Q, Q_out, K=None, K_out=None, positions=None, inv_freq=Non
         raise ValueError("Q must be [tokens][q_heads][128]")
     if inv_freq is not None and positions is None:
         raise ValueError("inv_freq without positions")
+    if (K is None) != (K_out is None):
+        raise ValueError("K and K_out come together")
     t, dev, (n, hq, _) = Q.dtype, Q.get_device(), Q.shape
     _here(dev, torch)
     dt = _row_dtype(Q, torch)

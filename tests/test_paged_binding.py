@@ -86,3 +86,14 @@ def test_attention_over_a_stream_takes_its_types_and_sizes_alone(J):
         with pytest.raises(ValueError):
             J.m.jolt_attention(st, **{**whole, **bad}, scale=0.1)
     assert len(J.calls) == 2
+
+
+def test_keys_and_their_output_come_together(J):
+    bf16 = J.torch.bfloat16
+    Q, K = FakeTensor((5, 8, 128), bf16), FakeTensor((5, 2, 128), bf16)
+    J.m.jolt_qk_norm_rope(Q, Q, K, K)
+    assert J.calls == ["jolt_qk_norm_rope"]
+    for kw in (dict(K=K), dict(K_out=K)):
+        with pytest.raises(ValueError):
+            J.m.jolt_qk_norm_rope(Q, Q, **kw)
+    assert len(J.calls) == 1

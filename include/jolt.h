@@ -271,8 +271,8 @@ JOLT_API void jolt_pages_destroy(jolt_pages_t pages);
  *   (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a), j = i + rope_dim / 2, or pairs
  *   (2 i, 2 i + 1) when interleaved. float32 inside, rounded once.
  * Q, K: device [tokens][heads][128] of `dtype`, element strides as given (multiples of 8; rows
- *   contiguous and 16-byte aligned); K may be NULL with k_heads 0. Q_out, K_out: the same, or the
- *   inputs themselves. q_weight, k_weight: device [128] of `dtype`, or NULL. positions: device int32
+ *   contiguous and 16-byte aligned); K may be NULL with k_heads 0. Q_out, K_out: the same, with rows
+ *   that do not overlap, or the inputs themselves. q_weight, k_weight: device [128] of `dtype`, or NULL. positions: device int32
  *   [tokens]; inv_freq: device float32 [rope_dim / 2], rope_dim a multiple of 16 up to 128; both
  *   NULL for no rotation.
  */

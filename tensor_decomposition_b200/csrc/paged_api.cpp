@@ -3,6 +3,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -92,6 +93,20 @@ jolt_status check_rows(const char* what, const char* name, const void* p, int64_
   if (ts > INT32_MAX || ts < -INT32_MAX || hs > INT32_MAX || hs < -INT32_MAX)
     return host_fail(JOLT_ERR_UNSUPPORTED, "%s: strides of %s beyond 2^31 elements", what, name);
   return JOLT_OK;
+}
+
+// Whether rows of an output lie over one another, of 128 elements at ts t + hs h. Mostly one dimension lies within
+// the other's stride; else each distance of heads is held against the nearest of tokens.
+bool rows_overlap(int64_t ts, int64_t hs, int64_t tokens, int64_t heads) {
+  ts = std::abs(ts);
+  hs = std::abs(hs);
+  if ((tokens > 1 && ts < kD) || (heads > 1 && hs < kD)) return true;
+  if (tokens == 1 || heads == 1 || ts >= hs * (heads - 1) + kD || hs >= ts * (tokens - 1) + kD) return false;
+  for (int64_t h = 1; h < heads; ++h) {
+    const int64_t t = h * hs / ts, left = h * hs - t * ts;   // signs of the strides: the rows' set is the same mirrored
+    if ((t < tokens && left < kD) || (t + 1 < tokens && ts - left < kD)) return true;
+  }
+  return false;
 }
 
 jolt_status check_rope(const char* what, const int32_t* positions, bool positions_needed, const float* inv_freq,
@@ -275,6 +290,9 @@ JOLT_API jolt_status jolt_qk_norm_rope(const jolt_norm_rope* args, void* cuda_st
   if (st != JOLT_OK) return st;
   if (((int64_t)n.q_heads + n.k_heads) * n.tokens > INT32_MAX)
     return host_fail(JOLT_ERR_UNSUPPORTED, "%s: more than 2^31 rows", what);
+  if (rows_overlap(n.qo_token_stride, n.qo_head_stride, n.tokens, n.q_heads) ||
+      (n.k_heads > 0 && rows_overlap(n.ko_token_stride, n.ko_head_stride, n.tokens, n.k_heads)))
+    return host_fail(JOLT_ERR_INVALID_ARG, "%s: rows of an output overlap", what);
   if (!aligned16(n.q_weight) || !aligned16(n.k_weight))
     return host_fail(JOLT_ERR_INVALID_ARG, "%s: weights must be 16-byte aligned", what);
   RowsIn q = rows_in(n.Q, n.q_token_stride, n.q_head_stride, n.q_heads, n.q_weight), k;

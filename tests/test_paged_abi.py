@@ -122,3 +122,25 @@ def test_pages_whose_head_stride_is_beyond_32_bits(J, untouched):
     h = ctypes.c_void_p()
     sh = J.PageShape(1, 1, 1 << 24, 128, 0)
     assert J._lib.jolt_pages_create(ctypes.byref(sh), p, p, None, ctypes.byref(h)) == 9 and not h.value
+
+
+def test_output_rows_that_overlap_are_refused(J, untouched):
+    """Rows written over one another (an expanded output, a token stride shorter than a token) leave results that
+    depend on their order. Layouts that look odd but keep their rows apart are none of them: those get as far as the
+    next check, of the weights' alignment."""
+    keep, p = _buf()
+
+    def call(tokens, hq, qts, qhs, hk=0, kts=0, khs=0):
+        return J._lib.jolt_qk_norm_rope(J._NORM_ROPE.pack(p, 128, 128, p + 2, p, qts, qhs, p if hk else 0, 128, 128, 0,
+                                                          p if hk else 0, kts, khs, 0, 0, 0, tokens, hq, hk, 0, 0, 1e-6), None)
+
+    def said():
+        return J._lib.jolt_last_error().decode()
+
+    for a in ((2, 1, 0, 128), (1, 2, 256, 0), (2, 2, 128, 128), (3, 4, 504, 128), (2, 2, 256, 120), (9, 5, 128, 1024),
+              (4, 3, 256, 384), (2, 1, -64, 128), (7, 2, 128, -640)):
+        assert call(*a) == 1 and "overlap" in said(), a
+        assert call(a[0], 1, 128, 0, a[1], a[2], a[3]) == 1 and "overlap" in said(), a
+    for a in ((1, 1, 0, 0), (2, 2, 256, 128), (5, 3, 128, 640), (3, 2, 256, 384), (3, 2, -256, 128), (2, 3, 384, 256),
+              (5, 40, 40 * 128 + 8, 128)):
+        assert call(*a) == 1 and "weights" in said(), (a, said())

@@ -13,11 +13,13 @@
 // other. Weights overwrite their scores in Tensor Memory and are the second product's A operand
 // from there, so only keys, values and queries pass through shared memory.
 // The weights are rounded to the type of the values (the tensor pipe takes no wider ones); their sum
-// is not. A maximum that grows by less than 8 (in units of log 2) is not followed: weights up to 2^8
+// is not. A maximum that grows by less than 8 (in units of log 2; 6 in fp16) is not followed: weights up to 2^8
 // are as exact, and most rescalings of the output fall away.
 // Measured (32 query heads on 8): 2048 tokens over 32768 keys 1.00 PFLOP/s in a sustained run, where the
 // card is at its power limit, up to 1.18 in a short one; a prompt of 8192 tokens 1.00; items of one or two
 // tiles are bound by the chain of an item (queries, scores, weights, output), 10 us.
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "paged_attention.cuh"
 #include "sm100.cuh"
@@ -39,7 +41,15 @@ constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;   // 256 x 200 + 128 x 104 = 384 x 168
 constexpr int kSmem = (2 + kStages) * kTileBytes;
 constexpr int kItem = 3;                     // what an item costs besides its tiles, in tiles
-constexpr float kFollow = 8.0f;
+// A maximum that grows by no more than kFollow (in units of log 2) is not followed, and weights are 2^kLift times as
+// large as beside a maximum of 1: fp16 has nothing below 2^-24, and what lies so far below the largest counts where
+// the keys are many, so there the largest weight is moved up to 2^15 and each is held to 2^-34 of it, whole down to
+// 2^-23 (unmoved, all below 2^-25 was lost: keys 17.4 lower in the exponent). A prompt of 4096 tokens in fp16:
+// 150.9 us, 149.1 with 8 and 2^7, 156.5 with 4 and 2^11.
+template <typename T>
+constexpr float kFollow = std::is_same_v<T, __half> ? 6.0f : 8.0f;
+template <typename T>
+constexpr float kLift = std::is_same_v<T, __half> ? 9.0f : 0.0f;
 
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
@@ -648,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mn = max3(m, max3(mx[0], mx[1], mx[2]) * scale2, mx[3] * scale2);
         if (j == t0) {
           m = mn;
-        } else if (__any_sync(0xffffffffu, r < R && mn - m > kFollow)) {   // lanes behind the rows hold anything
+        } else if (__any_sync(0xffffffffu, r < R && mn - m > kFollow<T>)) {   // lanes behind the rows hold anything
           const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
           m = mn;
           l *= f;
@@ -663,9 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(tO + 16 * c, o);
           }
         }
-        const float sub = m == -INFINITY ? 0.0f : -m;
+        const float sub = m == -INFINITY ? 0.0f : kLift<T> - m;
         weights<T>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
+      m -= kLift<T>;   // what sum and output are relative to
       const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g.d + (rc - tok * g.d);
       if (a.pre_lse && r < R) {   // what the end needs of the prefix, while the last products are made
         prefetch_l2(a.pre_out + row * kD, kD * 4);

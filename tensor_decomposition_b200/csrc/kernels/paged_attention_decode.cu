@@ -34,6 +34,10 @@ constexpr int kTile = kKeys * kD * 2;     // bytes of a slice's keys (or values)
 constexpr int kMinUnits = 1;
 constexpr int kTeamCtas = 8;
 constexpr int kThreads = 32 * kSlices;
+// Weights are 2^kLift times as large as beside a maximum of 1: fp16 holds nothing below 2^-24, neither a weight nor
+// the remainder of one, and the largest may be 2^15.
+template <typename T>
+constexpr float kLift = std::is_same_v<T, __half> ? 15.0f : 0.0f;
 // kT: blocks of 16 query rows, 0 for up to 8 rows. CTAs per SM and stages of a ring: what registers and
 // shared memory allow.
 template <int kT>
@@ -208,7 +212,7 @@ struct Blocks16 {
             }
           }
         }
-        const float sub[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0], m[t][1] == -INFINITY ? 0.0f : m[t][1]};
+        const float sub[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0] - kLift<T>, m[t][1] == -INFINITY ? 0.0f : m[t][1] - kLift<T>};
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -245,6 +249,7 @@ struct Blocks16 {
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        m[t][k] -= kLift<T>;   // what sum and output are relative to
         l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 1);
         l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 2);
         if (pair == 0) ml[16 * t + quad + 8 * k] = make_float2(m[t][k], l[t][k]);
@@ -345,7 +350,7 @@ struct Block8 {
         }
       }
     }
-    const float sub[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+    const float sub[2] = {m[0] == -INFINITY ? 0.0f : m[0] - kLift<T>, m[1] == -INFINITY ? 0.0f : m[1] - kLift<T>};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       s[e] = ex2(s[e] - sub[e & 1]);
@@ -372,6 +377,7 @@ struct Block8 {
     const int quad = lane >> 2, pair = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      m[e] -= kLift<T>;   // what sum and output are relative to
 #pragma unroll
       for (int w = 4; w < 32; w <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], w);
       if (quad == 0) ml[2 * pair + e] = make_float2(m[e], l[e]);

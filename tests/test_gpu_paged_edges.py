@@ -206,3 +206,46 @@ def test_attention_over_a_stream_beyond_its_grid_is_refused(J):
     with pytest.raises(J.JoltError) as e:
         J.jolt_attention(st, Q, out, SCALE)
     assert e.value.status == 9 and J.jolt_launch_count() == before
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("below", [16, 18, 20])
+@pytest.mark.parametrize("seqs,n,g", [(2, 1, 4), (600, 1, 4), (600, 3, 4), (300, 5, 4), (300, 100, 1), (300, 200, 1)])
+def test_many_keys_far_below_one(J, dtype, below, seqs, n, g):
+    """One key whose value is 0, and 32767 others `below` lower in the exponent: they make the output, each with a
+    weight that 16 bits would not hold beside 1.
+
+    The bound: a score is 8 below / 8 in one product, exact, but for its scale in units of log 2 (2 roundings of
+    2^-24 of a number up to 29, each moving a weight by 2 ln 2 times as much: 2^-17); the weights' and the output's
+    rounding (2 half steps), sums in 32 bits over 2^15 keys in blocks (2^-15 with each of 2^11 accumulations off by a
+    last place); and what is below the type's smallest numbers, half of fp16's, 2^-25, beside a largest
+    weight of 2^9 at least: 2^-34 a key."""
+    import torch
+    t, kv, page = _t(dtype), 32768, 64
+    K = torch.zeros((kv // page, 1, page, D), dtype=t, device="cuda")
+    V = torch.zeros_like(K)
+    v = torch.linspace(-1, 1, D, device="cuda").to(t)
+    V[:] = v
+    V[0, 0, 0] = 0
+    K[0, 0, 0, 5] = below
+    pages = J.jolt_pages_create(K, V)
+    table = torch.arange(kv // page, dtype=torch.int32, device="cuda").expand(seqs, -1).contiguous()   # all share them
+    Q = torch.zeros((seqs * n, g, D), dtype=t, device="cuda")
+    Q[..., 5] = 8
+    out = torch.full_like(Q, math.nan)
+    L = torch.full((seqs * n, g), math.nan, device="cuda")
+    batch = J.jolt_batch(n * torch.arange(seqs + 1, dtype=torch.int32, device="cuda"),
+                         torch.full((seqs,), kv, dtype=torch.int32, device="cuda"), table, seqs * n, n)
+    J.jolt_paged_attention(pages, batch, Q, out, 0.125, lse=L)
+    J.jolt_pages_status(pages)
+    many = (kv - n + torch.arange(n, device="cuda")).double().repeat(seqs)[:, None, None]     # keys but the first
+    w = many * math.exp(-below)
+    ref = w / (1 + w) * v.double()
+    h = half_step(t)
+    tol = (2 * h + 2.0 ** -15 + 2.0 ** -17) * ref.abs() + torch.finfo(t).tiny * h
+    if t == torch.float16:
+        tol += 2.0 ** -34 * kv * v.double().abs()
+    err = (out.double() - ref).abs()
+    assert (err <= tol).all(), (float((err / tol).max()), int((err > tol).sum()))
+    ref_l = torch.log(math.exp(below) + many[..., 0])
+    assert ((L.double() - ref_l).abs() <= 2.0 ** -15 + 2.0 ** -22 * below).all(), float((L.double() - ref_l).abs().max())

@@ -326,7 +326,9 @@ JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* bat
  *   the context and the log of its sum of exponentials (both or neither): joined as a term
  *   e^(prefix_lse) of value prefix_out. A row without keys gets out = 0 and lse = -inf.
  *   Where a row's keys are divided between CTAs depends on all lengths of the batch, so a row's last
- *   places may too; the same call gives the same bits.
+ *   places may too; the same call gives the same bits. Scores, weights and sums are float32 and the output
+ *   is rounded once, but for calls whose chunks may have more than 128 rows a KV head (max_q tokens, total_q
+ *   at most, times q_heads / heads): there the weights e^(s_t) meet the values rounded to their type.
  * Q: device [total_q][q_heads][128] of the set's dtype, element strides as above. out: device
  *   [total_q][q_heads][128] of that dtype; lse: device float32 [total_q][q_heads], the log of the
  *   sum of exponentials, prefix included, or NULL. prefix_out, prefix_lse: device float32

@@ -173,7 +173,7 @@ cudaError_t take_status(int32_t* word, int32_t* out, cudaStream_t s) {
 // items and short caches, whose fewer steps to the first output count (32 items of 16 rows: 8.7, 9.3, 14.3, 32.7
 // and 98 us for 128, 512, 2048, 8192 and 32768 keys, in the other kernel 15.2, 16.7, 18.7, 35.7 and 93; of 20
 // rows: 12.1, 15.6, 23.7, 47, 120 and 15.3, 17.0, 18.8, 37, 95; 128 items of 16 rows: 17.5, 26.7, 43, 102, 338
-// and 16.6, 18.1, 35, 93, 326). Where clusters of 8 CTAs, one for each item, all run at once (33 and more
+// and 16.6, 18.1, 35, 93, 326). Both round the output alone up to 128 rows, so the choice is one of time. Where clusters of 8 CTAs, one for each item, all run at once (33 and more
 // do not: 9.0 us instead of 5.9) and their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0
 // instead of 7.7 us at 1024 keys, 11.9 and 10.9 at 4096, 19.3 and 13.5 at 8192; 32 items: 26 instead of 32
 // at 8192).

@@ -12,8 +12,8 @@
 // the query rows. While one half's scores are turned into weights, the tensor pipe works for the
 // other. Weights overwrite their scores in Tensor Memory and are the second product's A operand
 // from there, so only keys, values and queries pass through shared memory.
-// The weights are rounded to the type of the values (the tensor pipe takes no wider ones); their sum
-// is not. A maximum that grows by less than 8 (in units of log 2; 6 in fp16) is not followed: weights up to 2^8
+// The weights are rounded to the type of the values (the tensor pipe takes no wider ones; up to 128 rows
+// what the rounding left follows as a second operand, kFew); their sum is not. A maximum that grows by less than 8 (in units of log 2; 6 in fp16) is not followed: weights up to 2^8
 // are as exact, and most rescalings of the output fall away.
 // Measured (32 query heads on 8): 2048 tokens over 32768 keys 1.00 PFLOP/s in a sustained run, where the
 // card is at its power limit, up to 1.18 in a short one; a prompt of 8192 tokens 1.00; items of one or two
@@ -155,6 +155,13 @@ __device__ __forceinline__ uint32_t pack2(__half, float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint64_t wide2(__nv_bfloat16, uint32_t v) {
+  return pair_of(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t wide2(__half, uint32_t v) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return pair_of(f.x, f.y);
+}
 template <typename T>
 __device__ __forceinline__ constexpr uint32_t idesc();
 template <>
@@ -172,12 +179,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 // The weights 2^(s scale2 + sub) of a row, rounded to the type, written to Tensor Memory (tP); their
-// sum goes to l unrounded. The first half is announced while the second is made. (Making 1 or 2 of 8
+// sum goes to l unrounded. kRest: what the rounding left, rounded, behind them (kRestAt). The first half is
+// announced while the second is made. (Making 1 or 2 of 8
 // exponentials by a polynomial on the multiply-add units, to spare the special function unit, gave 0 and
 // -8 % on a chunk of 2048 tokens over 32768 keys. Leaving out those of 32 keys that no row of the warp sees,
 // by a branch, made items of one or two tiles 5 % faster and prompts 4 % slower.)
-template <typename T>
-__device__ __forceinline__ void weights(const float (&s)[kHalf], float scale2, float sub, float& l, uint32_t tP,
+constexpr uint32_t kRestAt = kHalf / 2;      // columns
+template <typename T, bool kRest>
+__device__ __forceinline__ void weights(float (&s)[kHalf], float scale2, float sub, float& l, uint32_t tP,
                                         uint64_t* lo, uint64_t* hi, int lane) {
   const uint64_t sc = pair_of(scale2, scale2), sb = pair_of(sub, sub);
   uint64_t sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
@@ -193,8 +202,15 @@ __device__ __forceinline__ void weights(const float (&s)[kHalf], float scale2, f
       y = ex2(y);
       sum[i & 1] = add2(sum[i & 1], pair_of(x, y));
       w[i] = pack2(T(), x, y);
+      if (kRest)   // in the place of the scores
+        unpair(fma2(wide2(T(), w[i]), pair_of(-1.0f, -1.0f), pair_of(x, y)), s[32 * c + 2 * i], s[32 * c + 2 * i + 1]);
     }
     tmem_st16(tP + 16 * c, w);
+    if (kRest) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = pack2(T(), s[32 * c + 2 * i], s[32 * c + 2 * i + 1]);
+      tmem_st16(tP + kRestAt + 16 * c, w);
+    }
     if (c & 1) {
       tmem_st_wait();
       tc_fence_before();
@@ -270,7 +286,11 @@ __device__ __noinline__ void drain(uint64_t* bar) {
   mbar_wait(bar, 0, 1u << 20);
 }
 
-template <typename T>
+// kFew: no item has more than half a block of rows. Their weights' remainders enter the second product too, as
+// in the kernel for fewer rows, so that only the output is rounded: these calls wait for memory or an item's chain and not
+// for the tensor pipe (16 sequences over up to 4096 keys: 41.8 us with them and without for 2 to 5 drafted tokens, 65.6 and
+// 64.2 for 32). As a branch of one kernel it cost prompts 4 to 10 %, and items of whole blocks a third.
+template <typename T, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_chunk(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws, int box) {
   extern __shared__ __align__(1024) uint8_t sm[];   // what is static takes the rest, 3 KB
@@ -418,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
             }
             umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + 8 * k, B + k * (2048 >> 4), id_pv, !first || k != 0);
+            if (kFew) umma_ts(tmem + (2 + t) * kHalf, tmem + t * kHalf + kRestAt + 8 * k, B + k * (2048 >> 4), id_pv, 1);
           }
           ++tiles[t];
           return true;
@@ -429,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         do {
           const int nt = p.t1 - p.t0;
-          if (solo(p, g)) {
+          if (kFew || solo(p, g)) {
             // the halves take the tiles in turn, each ahead of the other by its softmax
             const int lead = min(nt, 2);
             if (!(ok = query(0))) break;
@@ -494,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       do {
         const int t0 = p.t0, nt = p.t1 - t0, len = p.v.len, upto = p.upto, h = p.h, seq = p.s;
-        const bool alone = solo(p, g);
+        const bool alone = kFew || solo(p, g);
         const int seen = causal ? len - p.v.n + g.quot(p.m * kBlockRows) : len - 1;   // the last key that all rows see
         // (the ring holds the tiles of three pieces at most, and the softmax is at most two behind those)
         bool* hid = &hid_s[pieces++ & 7];
@@ -611,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A wait that gives up does not end this role: a pair's barriers need both of its warps, and the other
     // waits give up at once then. The result is reported as void.
     do {
-      const bool alone = solo(p, g), began = p.t0 == 0, ends = p.t1 == p.T;
+      const bool alone = kFew || solo(p, g), began = p.t0 == 0, ends = p.t1 == p.T;
       const int R = p.v.n * g.d, r0 = p.m * kBlockRows + (alone ? 0 : t * kHalf);
       if (tid == 0 && began && !ends)   // the share's last piece
         ws.list[blockIdx.x] = Split{p.s, p.h, p.m, owner_of(range_s[0] + (p.T - p.t1) - 1, range_s[1], range_s[2]), 1,
@@ -674,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float sub = m == -INFINITY ? 0.0f : kLift<T> - m;
-        weights<T>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
+        weights<T, kFew>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
       m -= kLift<T>;   // what sum and output are relative to
       const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g.d + (rc - tok * g.d);
@@ -791,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kSoftmaxWarps) tmem_dealloc(tmem, 512);
 }
 
-template <typename T>
+template <typename T, bool kFew>
 cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
   int box = kHalf;
   while (a.b.page_size % box) box /= 2;      // 16 at least
@@ -799,15 +820,17 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
   maps.K = a.maps[0];
   maps.V = a.maps[1];
   static SmemFlags allowed;
-  cudaError_t e = allow_smem(k_attn_chunk<T>, kSmem, a.device, allowed);
+  cudaError_t e = allow_smem(k_attn_chunk<T, kFew>, kSmem, a.device, allowed);
   if (e != cudaSuccess) return e;
-  return launch_early(k_attn_chunk<T>, dim3(p.grid), dim3(kThreads), kSmem, 1, s, a, maps, w, box);
+  return launch_early(k_attn_chunk<T, kFew>, dim3(p.grid), dim3(kThreads), kSmem, 1, s, a, maps, w, box);
 }
 
 }  // namespace
 
 cudaError_t attn_chunk(const PagedAttnArgs& a, const AttnPlan& p, const pattn::Workspace& w, cudaStream_t s) {
-  return a.dtype == JOLT_BF16 ? launch<__nv_bfloat16>(a, p, w, s) : launch<__half>(a, p, w, s);
+  const bool b = a.dtype == JOLT_BF16;
+  if (p.most <= kHalf) return b ? launch<__nv_bfloat16, true>(a, p, w, s) : launch<__half, true>(a, p, w, s);
+  return b ? launch<__nv_bfloat16, false>(a, p, w, s) : launch<__half, false>(a, p, w, s);
 }
 
 }  // namespace jolt

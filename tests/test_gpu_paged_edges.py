@@ -249,3 +249,48 @@ def test_many_keys_far_below_one(J, dtype, below, seqs, n, g):
     assert (err <= tol).all(), (float((err / tol).max()), int((err > tol).sum()))
     ref_l = torch.log(math.exp(below) + many[..., 0])
     assert ((L.double() - ref_l).abs() <= 2.0 ** -15 + 2.0 ** -22 * below).all(), float((L.double() - ref_l).abs().max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kv,chunks,heads,g", [
+    ([300, 77, 200], [1, 1, 1], 2, 4),           # up to 8 rows, clusters
+    ([300, 77, 200] * 20, [2, 1, 2] * 20, 2, 4),  # in shares
+    ([300, 77, 200], [3, 4, 2], 2, 4),           # up to 16 rows
+    ([300, 77, 200], [5, 8, 6], 1, 4),           # up to 32
+    ([300, 77, 200] * 20, [3, 4, 2] * 20, 2, 4),  # the same of many sequences
+    ([300, 77, 200] * 20, [5, 8, 6] * 20, 2, 4),
+    ([300, 150, 200], [100, 128, 127], 2, 1),    # up to 128
+    ([300, 150, 200] * 30, [100, 128, 33] * 30, 2, 1),
+])
+def test_up_to_128_rows_round_the_output_alone(J, dtype, kv, chunks, heads, g):
+    """Up to 128 rows that read one KV head of a sequence: their weights are not rounded to the type, whatever else
+    is in the batch, so that the output's rounding is all that is left.
+
+    Queries and keys are small whole numbers and the scale is a power of two, so scores are exact. What remains, of
+    A = sum_j w_j |v_j|: their scale in units of log 2 (2 roundings of 2^-24 of up to 64, times 2 ln 2: 2^-16), the
+    weights' remainder, rounded to the type (h^2), and the sums: up to 2 x 300 / 16 accumulations, off by a last place
+    each (2^-17). Without the remainder it would be h, 2^-8 in bf16."""
+    import torch
+    t = _t(dtype)
+    c = Cache(kv, chunks, heads, 16, t, seed=len(kv))
+    c.K.copy_(torch.where(torch.isnan(c.K), c.K, torch.randint(-2, 3, c.K.shape, generator=c.g, device="cuda").to(t)))
+    Q = torch.randint(-2, 3, (c.total, heads * g, D), generator=c.g, device="cuda").to(t)
+    out, L = torch.full_like(Q, math.nan), torch.full((c.total, heads * g), math.nan, device="cuda")
+    pages, batch = c.handles(J)
+    J.jolt_paged_attention(pages, batch, Q, out, 0.125, lse=L)
+    J.jolt_pages_status(pages)
+    check_attention(c, Q, out, L, 0.125, True)
+    h = half_step(t)
+    for s in range(len(kv)):
+        n, r = c.n[s], slice(c.starts[s], c.starts[s + 1])
+        for k in range(heads):
+            K, V = c.rows(s, k, c.K).double(), c.rows(s, k, c.V).double()
+            x = Q[r, k * g:k * g + g].double()
+            z = (x @ K.T * 0.125).masked_fill(torch.arange(kv[s], device="cuda") > (kv[s] - n + torch.arange(n, device="cuda"))[:, None, None],
+                                              -math.inf)
+            assert z[z > -math.inf].abs().max() * math.log2(math.e) < 64
+            w = torch.softmax(z, -1)
+            ref, A = w @ V, w @ V.abs()
+            tol = h * ref.abs() + (1 + h) * (h * h + 2.0 ** -16 + 2.0 ** -17) * A + torch.finfo(t).tiny
+            err = (out[r, k * g:k * g + g].double() - ref).abs()
+            assert (err <= tol).all(), (s, k, float((err / tol).max()))

@@ -4,8 +4,8 @@
 // with a part (out0, lse0) attended elsewhere, which counts as one more key of score lse0 and
 // value out0. Two kernels do the work, one for few rows a KV head (paged_attention_decode.cu), bound
 // by HBM, one for many (paged_attention_chunk.cu), bound by the tensor pipe; both divide it into
-// equal shares a CTA, whatever the lengths are. This file chooses, and combines the parts of what a
-// share's end has cut.
+// equal shares a CTA, whatever the lengths are (but for small calls of few rows, which clusters take item by
+// item). This file chooses, and combines the parts of what a share's end has cut.
 #include "paged_attention.cuh"
 
 namespace jolt {
@@ -170,24 +170,26 @@ cudaError_t take_status(int32_t* word, int32_t* out, cudaStream_t s) {
 }
 
 // Up to 8 rows of a chunk reading one KV head run in the kernel for few rows; 9 to 32 do where there are few
-// items and short caches, whose fewer steps to the first output count (32 items of 16 rows: 8.7, 9.3, 14.3, 32.7
-// and 98 us for 128, 512, 2048, 8192 and 32768 keys, in the other kernel 15.2, 16.7, 18.7, 35.7 and 93; of 20
-// rows: 12.1, 15.6, 23.7, 47, 120 and 15.3, 17.0, 18.8, 37, 95; 128 items of 16 rows: 17.5, 26.7, 43, 102, 338
-// and 16.6, 18.1, 35, 93, 326). Both round the output alone up to 128 rows, so the choice is one of time. Where clusters of 8 CTAs, one for each item, all run at once (33 and more
-// do not: 9.0 us instead of 5.9) and their CTAs get few keys or fill the GPU, they combine by themselves (8 items: 6.0
-// instead of 7.7 us at 1024 keys, 11.9 and 10.9 at 4096, 19.3 and 13.5 at 8192; 32 items: 26 instead of 32
-// at 8192).
-constexpr int kFewItems = 32, kFewTokens16 = 8192, kFewTokens32 = 512;
-constexpr int kTeamTokens = 4096, kTeamItems = 32;
+// items and short caches, whose fewer steps to the first output count (32 items of 16 rows: 8.1, 8.9, 13.6, 19.6
+// and 31.2 us for 128, 512, 2048, 4096 and 6000 keys, in the other kernel 15.3, 16.5, 18.5, 21.5 and 25.8; of 20
+// rows: 11.5, 14.9, 22.8 for 128, 512, 2048 and 15.4, 16.9, 18.8; 128 items of 16 rows: 16.9, 25.9, 42, 99 for 128,
+// 512, 2048, 8192 and 16.2, 18.1, 35, 93). Both round the output alone up to 128 rows, so the choice is one of time.
+// Clusters of 8 CTAs, one for each item, combine by themselves where they all run at once (33 and more do not: 9.0 us
+// instead of 5.9) and the table holds few keys (8 items: 5.9 instead of 7.4 us at 1024 keys, 11.8 and 12.2 at 4096, 19.4
+// and 14.4 at 8192; one item: 5.9 and 7.7, 11.7 and 9.6, 19.3 and 12.0; 32 items: 7.7 and 10.8, 15.0 and 16.3, 26.4 and
+// 29.6). An item's eight CTAs have it whatever the others' lengths are, so longer tables are not for them, where one
+// sequence may have nearly all the keys (32 items of 131072, 100, 100 and 100 keys: 271 us, in shares 94; 8192, 100, 100
+// and 100: 22 and 15). 9 to 16 rows are in the kernel for few rows where they are in clusters.
+constexpr int kTeamTokens = 4096, kTeamItems = 32, kFewTokens32 = 512;
 AttnPlan paged_attention_plan(const PagedAttnArgs& a, int sms) {
   AttnPlan p;
   const int64_t tokens = (int64_t)a.b.max_pages * a.b.page_size, rows = (int64_t)std::min(a.b.max_q, a.b.total_q) * (a.Hq / a.b.heads);
   const int64_t items = (int64_t)a.b.heads * a.b.num_seqs;
-  p.decode = rows <= 8 || (rows <= 32 && items <= kFewItems && tokens <= (rows <= 16 ? kFewTokens16 : kFewTokens32));
+  p.decode = rows <= 8 || (rows <= 32 && items <= kTeamItems && tokens <= (rows <= 16 ? kTeamTokens : kFewTokens32));
   p.rows = !p.decode ? 256 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   p.most = (int)std::max<int64_t>(1, std::min<int64_t>(rows, p.rows));
   const int fit = p.rows <= 16 ? kTeamItems : kTeamItems / 2;   // two CTAs an SM, or one
-  if (p.decode && items <= fit && (tokens <= kTeamTokens || items >= fit - fit / 8)) {
+  if (p.decode && items <= fit && tokens <= kTeamTokens) {
     p.team = 1;
     p.grid = (int)items * 8;
     return p;

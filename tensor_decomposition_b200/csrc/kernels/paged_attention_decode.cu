@@ -661,7 +661,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<kT>)
 
 template <typename T, int kT>
 cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w, cudaStream_t s) {
-  static SmemFlags allowed, allowed_team;
+  [[maybe_unused]] static SmemFlags allowed;
+  static SmemFlags allowed_team;
   Maps maps;
   maps.K = a.maps[2];
   maps.V = a.maps[3];
@@ -671,9 +672,13 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnPlan& p, const Workspace& w
     if (e != cudaSuccess) return e;
     return launch_early(k_attn_decode<T, kT, true>, dim3(p.grid), dim3(kThreads), kTeamSmem<kT>, kTeamCtas, s, a, maps, w);
   }
-  e = allow_smem(k_attn_decode<T, kT, false>, kSmem<kT>, a.device, allowed);
-  if (e != cudaSuccess) return e;
-  return launch_early(k_attn_decode<T, kT, false>, dim3(p.grid), dim3(kThreads), kSmem<kT>, 1, s, a, maps, w);
+  if constexpr (kT == 1) {   // 9 to 16 rows: clusters only
+    return cudaErrorInvalidValue;
+  } else {
+    e = allow_smem(k_attn_decode<T, kT, false>, kSmem<kT>, a.device, allowed);
+    if (e != cudaSuccess) return e;
+    return launch_early(k_attn_decode<T, kT, false>, dim3(p.grid), dim3(kThreads), kSmem<kT>, 1, s, a, maps, w);
+  }
 }
 
 }  // namespace

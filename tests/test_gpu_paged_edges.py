@@ -294,3 +294,22 @@ def test_up_to_128_rows_round_the_output_alone(J, dtype, kv, chunks, heads, g):
             tol = h * ref.abs() + (1 + h) * (h * h + 2.0 ** -16 + 2.0 ** -17) * A + torch.finfo(t).tiny
             err = (out[r, k * g:k * g + g].double() - ref).abs()
             assert (err <= tol).all(), (s, k, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_one_long_sequence_among_few(J, n):
+    """Four sequences of eight KV heads, one of them long: its keys are divided over the whole GPU and their parts combined
+    by a second launch, where a cluster an item would leave it to an eighth of the CTAs; small tables stay with clusters."""
+    import torch
+    for long, launches in ((16384 - n, 2), (8000, 2), (4000, 1)):
+        if n > 1 and long > 8192:
+            continue
+        c = Cache([long, 100, 7, 60], [n] * 4, 8, 16, torch.bfloat16, seed=n)
+        Q = c.randn(c.total, 32, D)
+        out, L = torch.full_like(Q, math.nan), torch.full((c.total, 32), math.nan, device="cuda")
+        pages, batch = c.handles(J)
+        before = J.jolt_launch_count()
+        J.jolt_paged_attention(pages, batch, Q, out, SCALE, lse=L)
+        assert J.jolt_launch_count() - before == launches
+        J.jolt_pages_status(pages)
+        check_attention(c, Q, out, L, SCALE, True)

@@ -313,3 +313,17 @@ def test_one_long_sequence_among_few(J, n):
         assert J.jolt_launch_count() - before == launches
         J.jolt_pages_status(pages)
         check_attention(c, Q, out, L, SCALE, True)
+
+
+def test_a_stream_from_the_host_knows_its_layers(J):
+    import torch
+    st = _stream(J, 300, 1)
+    back = J.jolt_stream_from_host(J.jolt_stream_to_host(st))
+    Q = torch.randn((2, 4, 3, D), device="cuda").to(torch.bfloat16)
+    a, b = torch.zeros(Q.shape, device="cuda"), torch.ones(Q.shape, device="cuda")
+    J.jolt_attention(st, Q, a, SCALE)
+    J.jolt_attention(back, Q, b, SCALE)
+    assert torch.equal(a, b)
+    for s in (st, back):
+        with pytest.raises(ValueError):
+            J.jolt_attention(s, Q[:1], a[:1], SCALE)

@@ -50,6 +50,16 @@ template <typename T>
 constexpr float kFollow = std::is_same_v<T, __half> ? 6.0f : 8.0f;
 template <typename T>
 constexpr float kLift = std::is_same_v<T, __half> ? 9.0f : 0.0f;
+// What the weights are relative to beside the maximum m, and a score in units of log 2 as a maximum. Both are rounded
+// up where there is a lift: with scores of 2^24 and more a last place is a whole unit, and no weight may pass 2^15 for it.
+template <typename T>
+__device__ __forceinline__ float base_of(float m) {
+  return kLift<T> == 0.0f ? m : __fsub_ru(m, kLift<T>);
+}
+template <typename T>
+__device__ __forceinline__ float top_of(float s, float scale2) {
+  return kLift<T> == 0.0f ? s * scale2 : __fmul_ru(s, scale2);
+}
 
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
@@ -676,11 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[kHalf - 4 + k]);
-        const float mn = max3(m, max3(mx[0], mx[1], mx[2]) * scale2, mx[3] * scale2);
+        const float mn = max3(m, top_of<T>(max3(mx[0], mx[1], mx[2]), scale2), top_of<T>(mx[3], scale2));
         if (j == t0) {
           m = mn;
         } else if (__any_sync(0xffffffffu, r < R && mn - m > kFollow<T>)) {   // lanes behind the rows hold anything
-          const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+          const float f = mn == -INFINITY ? 1.0f : ex2(base_of<T>(m) - base_of<T>(mn));
           m = mn;
           l *= f;
           // the scores being complete, so is every earlier product: the output is at rest
@@ -694,10 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(tO + 16 * c, o);
           }
         }
-        const float sub = m == -INFINITY ? 0.0f : kLift<T> - m;
+        const float sub = m == -INFINITY ? 0.0f : -base_of<T>(m);
         weights<T, kFew>(s, scale2, sub, l, tS, &bar.p_lo[t], &bar.p_hi[t], lane);
       }
-      m -= kLift<T>;   // what sum and output are relative to
+      m = base_of<T>(m);   // what sum and output are relative to
       const int64_t row = (int64_t)(p.v.q0 + tok) * a.Hq + p.h * g.d + (rc - tok * g.d);
       if (a.pre_lse && r < R) {   // what the end needs of the prefix, while the last products are made
         prefetch_l2(a.pre_out + row * kD, kD * 4);

@@ -38,6 +38,12 @@ constexpr int kThreads = 32 * kSlices;
 // the remainder of one, and the largest may be 2^15.
 template <typename T>
 constexpr float kLift = std::is_same_v<T, __half> ? 15.0f : 0.0f;
+// What the weights are relative to beside the maximum m; rounded up, since with scores of 2^24 and more a last place
+// is a whole unit, and no weight may pass 2^15 for it.
+template <typename T>
+__device__ __forceinline__ float base_of(float m) {
+  return kLift<T> == 0.0f ? m : __fsub_ru(m, kLift<T>);
+}
 // kT: blocks of 16 query rows, 0 for up to 8 rows. CTAs per SM and stages of a ring: what registers and
 // shared memory allow.
 template <int kT>
@@ -202,7 +208,7 @@ struct Blocks16 {
         if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1])) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float f = mn[k] == -INFINITY ? 1.0f : ex2(m[t][k] - mn[k]);
+            const float f = mn[k] == -INFINITY ? 1.0f : ex2(base_of<T>(m[t][k]) - base_of<T>(mn[k]));
             m[t][k] = mn[k];
             l[t][k] *= f;
 #pragma unroll
@@ -212,7 +218,7 @@ struct Blocks16 {
             }
           }
         }
-        const float sub[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0] - kLift<T>, m[t][1] == -INFINITY ? 0.0f : m[t][1] - kLift<T>};
+        const float sub[2] = {m[t][0] == -INFINITY ? 0.0f : base_of<T>(m[t][0]), m[t][1] == -INFINITY ? 0.0f : base_of<T>(m[t][1])};
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -249,7 +255,7 @@ struct Blocks16 {
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[t][k] -= kLift<T>;   // what sum and output are relative to
+        m[t][k] = base_of<T>(m[t][k]);   // what sum and output are relative to
         l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 1);
         l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], 2);
         if (pair == 0) ml[16 * t + quad + 8 * k] = make_float2(m[t][k], l[t][k]);
@@ -340,7 +346,7 @@ struct Block8 {
     if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float f = mn[e] == -INFINITY ? 1.0f : ex2(m[e] - mn[e]);
+        const float f = mn[e] == -INFINITY ? 1.0f : ex2(base_of<T>(m[e]) - base_of<T>(mn[e]));
         m[e] = mn[e];
         l[e] *= f;
 #pragma unroll
@@ -350,7 +356,7 @@ struct Block8 {
         }
       }
     }
-    const float sub[2] = {m[0] == -INFINITY ? 0.0f : m[0] - kLift<T>, m[1] == -INFINITY ? 0.0f : m[1] - kLift<T>};
+    const float sub[2] = {m[0] == -INFINITY ? 0.0f : base_of<T>(m[0]), m[1] == -INFINITY ? 0.0f : base_of<T>(m[1])};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       s[e] = ex2(s[e] - sub[e & 1]);
@@ -377,7 +383,7 @@ struct Block8 {
     const int quad = lane >> 2, pair = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m[e] -= kLift<T>;   // what sum and output are relative to
+      m[e] = base_of<T>(m[e]);   // what sum and output are relative to
 #pragma unroll
       for (int w = 4; w < 32; w <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], w);
       if (quad == 0) ml[2 * pair + e] = make_float2(m[e], l[e]);

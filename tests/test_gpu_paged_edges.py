@@ -327,3 +327,40 @@ def test_a_stream_from_the_host_knows_its_layers(J):
     for s in (st, back):
         with pytest.raises(ValueError):
             J.jolt_attention(s, Q[:1], a[:1], SCALE)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [0.0025, 0.0884, 0.3536, -0.0884])
+@pytest.mark.parametrize("seqs,n,g", [(2, 1, 4), (300, 1, 4), (2, 3, 4), (40, 5, 4), (2, 200, 1), (160, 200, 1)])
+def test_scores_of_millions(J, dtype, scale, seqs, n, g):
+    """Scores whose last places are whole units of the exponent, rising by less than a weight's range from tile to tile:
+    no weight may leave the type's range for it, so each output stays between the values and near those of the
+    largest scores: a score is exact, 2^24 to 2^26 in units of log 2, and its rounding moves a weight by 2^4 at most, so
+    keys 24 and more below the row's largest have less than 900 2^-16 of it together."""
+    import torch
+    t, kv, page = _t(dtype), 900, 64
+    big = 1024.0                                   # 127 products of 2^20, exact
+    K = torch.full((15, 1, page, D), big, device="cuda").to(t)
+    j = torch.arange(15 * page, device="cuda").reshape(15, page)
+    rise = (j // 32).float() if scale > 0 else (30 - j // 32).float()
+    K[:, 0, :, 127] = (8 * rise if dtype == "f16" else rise).to(t)      # bf16 holds whole numbers up to 256
+    V = torch.randn((15, 1, page, D), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(t)
+    Q = torch.full((seqs * n, g, D), big, device="cuda").to(t)
+    Q[..., 127] = 8 if dtype == "bf16" else 1
+    pages = J.jolt_pages_create(K, V)
+    table = torch.arange(15, dtype=torch.int32, device="cuda").expand(seqs, -1).contiguous()
+    batch = J.jolt_batch(n * torch.arange(seqs + 1, dtype=torch.int32, device="cuda"),
+                         torch.full((seqs,), kv, dtype=torch.int32, device="cuda"), table, seqs * n, n)
+    out, L = torch.full_like(Q, math.nan), torch.full((seqs * n, g), math.nan, device="cuda")
+    J.jolt_paged_attention(pages, batch, Q, out, scale, lse=L)
+    J.jolt_pages_status(pages)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(L).all()
+    v = V.reshape(-1, D)[:kv].double()
+    z = (K.reshape(-1, D)[:kv].double() @ Q[0, 0].double()) * scale * math.log2(math.e)
+    for i in {0, n - 1, n // 2}:
+        see = kv - n + i + 1
+        near = z[:see] > z[:see].max() - 24
+        lo, hi = v[:see][near].amin(0), v[:see][near].amax(0)
+        slack = half_step(t) * 4 + 2.0 ** -5
+        o = out.reshape(seqs, n, g, D)[:, i].double()
+        assert (o >= lo - slack).all() and (o <= hi + slack).all(), (i, float((lo - o).max()), float((o - hi).max()))

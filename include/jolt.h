@@ -242,7 +242,8 @@ typedef struct {
   int32_t num_seqs;            /* sequences */
   int32_t total_q;             /* rows of the batch's tensors, padded rows included */
   int32_t max_q;               /* the longest chunk that may occur */
-  int32_t max_pages;           /* columns of page_table */
+  int32_t max_pages;           /* columns of page_table; few-token calls over small caches are fastest
+                                  where they hold 4096 tokens at most */
   const int32_t* q_start;      /* device [num_seqs + 1] */
   const int32_t* kv_len;       /* device [num_seqs], the chunk's tokens included */
   const int32_t* page_table;   /* device [num_seqs][max_pages] */

@@ -15,7 +15,7 @@
 // The weights are rounded to the type of the values (the tensor pipe takes no wider ones; up to 128 rows
 // what the rounding left follows as a second operand, kFew); their sum is not. A maximum that grows by less than 8 (in units of log 2; 6 in fp16) is not followed: weights up to 2^8
 // are as exact, and most rescalings of the output fall away.
-// Measured (32 query heads on 8): 2048 tokens over 32768 keys 1.00 PFLOP/s in a sustained run, where the
+// Measured (32 query heads on 8): 2048 tokens over 32768 keys 0.97 PFLOP/s in a sustained run, where the
 // card is at its power limit, up to 1.18 in a short one; a prompt of 8192 tokens 1.00; items of one or two
 // tiles are bound by the chain of an item (queries, scores, weights, output), 10 us.
 #include <type_traits>
@@ -298,8 +298,8 @@ __device__ __noinline__ void drain(uint64_t* bar) {
 
 // kFew: no item has more than half a block of rows. Their weights' remainders enter the second product too, as
 // in the kernel for fewer rows, so that only the output is rounded: these calls wait for memory or an item's chain and not
-// for the tensor pipe (16 sequences over up to 4096 keys: 41.8 us with them and without for 2 to 5 drafted tokens, 65.6 and
-// 64.2 for 32). As a branch of one kernel it cost prompts 4 to 10 %, and items of whole blocks a third.
+// for the tensor pipe (16 sequences over up to 4096 keys: 42.8 us with them and 40.8 without for 2 to 5 drafted tokens, 65.6
+// and 64.2 for 32). As a branch of one kernel it cost prompts 4 to 10 %, and items of whole blocks a third.
 template <typename T, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_chunk(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ Maps maps, const Workspace ws, int box) {

@@ -14,8 +14,8 @@
 // warp has two blocks of 16, whose queries it reads from shared memory each time (their fragments would
 // not fit the registers beside two outputs). A warp for each block on a common ring, with a barrier a
 // unit, ran at half the speed.
-// Measured: 64 sequences of up to 8192 keys (8 KV heads, 4 rows each, 1.14 GB) 181 us, 6.3 TB/s; one
-// sequence of 131072 keys 88 us, 6.1 TB/s; one of 1024 keys 6.2 us, a chain of latencies.
+// Measured: 64 sequences of up to 8192 keys (8 KV heads, 4 rows each, 1.14 GB) 184 us, 6.2 TB/s; one
+// sequence of 131072 keys 89 us, 6.0 TB/s; one of 1024 keys 6.2 us in a graph, a chain of latencies.
 #include <cooperative_groups.h>
 
 #include <type_traits>

@@ -9,7 +9,7 @@
 // Each row is read and written once, which bounds the kernel for long inputs (HBM); short inputs
 // are bound by latency. A CTA takes a tile of tokens, up to 64 rows, 8 lanes a row (two 16-byte runs each) and
 // up to four rows a lane in flight at once: with one token a CTA the append of 16 rows a token ran at 1.4
-// TB/s, so it runs at 4.3 (tokens of 80 rows, a CTA each, at 5.5). The tile's sines are computed once (a thread each, while the rows are on their
+// TB/s, so it runs at 4.4 (tokens of 80 rows, a CTA each, at 5.0, in a short run 5.5). The tile's sines are computed once (a thread each, while the rows are on their
 // way) and used by all heads from shared memory; the append's page lookup is one parallel pass over the
 // batch's offsets instead of a search. (Persistent CTAs with a ring of asynchronous copies, and tiles of
 // two to four times the rows, were 8 to 25 % slower.)
@@ -28,7 +28,8 @@ constexpr int kLanes = 8;               // of a row: 16 features each
 constexpr int kSlots = kThreads / kLanes;   // rows at a time
 // Rows a slot keeps in flight. Where a tile has more rows than the slots hold at once (a token of more than 64
 // rows), the next row is loaded as soon as one is taken up, and three do; else all are loaded first and used
-// (16384 tokens of 80 rows: 121 us that way and 132 the other; 64 tokens of 40 rows: 4.4 and 3.3 us).
+// (16384 tokens of 80 rows: 121 us that way and 132 the other in a short run, 134 that way in a sustained one; 64
+// tokens of 40 rows: 4.4 and 3.3 us).
 template <bool kLong>
 constexpr int kBatch = kLong ? 3 : 4;
 constexpr int kRows = kSlots * kBatch<false>;   // of a tile, unless one token has more

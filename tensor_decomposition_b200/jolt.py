@@ -325,7 +325,7 @@ def _attention_tensors(Q, out, lse=None):
 
 def jolt_attention(stream: Stream, Q, out, scale: float, cuda_stream=None):
     """Q: bf16 CUDA tensor [layers][q_heads][n][head_dim]; out: float32 CUDA tensor of the same shape."""
-    if Q.dim() != 4 or tuple(out.shape) != tuple(Q.shape) or Q.shape[0] != stream.layers:
+    if Q.dim() != 4 or tuple(out.shape) != tuple(Q.shape) or stream.layers not in (None, Q.shape[0]):
         raise ValueError("Q and out must be [layers][q_heads][n][head_dim] of the same shape")
     _attention_tensors(Q, out)
     _check(_lib.jolt_attention(stream.handle, _dptr(Q), int(Q.shape[1]), int(Q.shape[2]), float(scale), _dptr(out),
@@ -344,7 +344,8 @@ def jolt_attention_lse(stream: Stream, layer: int, Q, out, lse, scale: float, cu
 
 # ------------------------------------------------------------------ the growing cache
 class Pages:
-    """A page set (jolt_pages_create): keeps the page tensors alive."""
+    """A page set (jolt_pages_create): keeps the page tensors alive. To be dropped after its calls have finished: what
+    they report goes to the set that has its place then."""
 
     def __init__(self, handle, K_pages, V_pages):
         self.handle, self.K, self.V = handle.value, K_pages, V_pages

@@ -97,3 +97,10 @@ def test_keys_and_their_output_come_together(J):
         with pytest.raises(ValueError):
             J.m.jolt_qk_norm_rope(Q, Q, **kw)
     assert len(J.calls) == 1
+
+
+def test_a_stream_of_unknown_layers_is_taken(J):
+    """A stream object made around a handle from elsewhere: its layers are the caller's to know."""
+    T, bf16, f32 = FakeTensor, J.torch.bfloat16, J.torch.float32
+    J.m.jolt_attention(J.m.Stream(None), T((3, 8, 5, 128), bf16), T((3, 8, 5, 128), f32), 0.1)
+    assert J.calls == ["jolt_attention"]

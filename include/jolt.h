@@ -330,6 +330,8 @@ JOLT_API jolt_status jolt_paged_append(jolt_pages_t pages, const jolt_batch* bat
  *   places may too; the same call gives the same bits. Scores, weights and sums are float32 and the output
  *   is rounded once, but for calls whose chunks may have more than 128 rows a KV head (max_q tokens, total_q
  *   at most, times q_heads / heads): there the weights e^(s_t) meet the values rounded to their type.
+ *   Scores of a row's largest keys are taken to be below 10^7 (F16) and 10^8 (BF16) in absolute value; beyond, where
+ *   their last places are whole units of the exponent and more, a row may come out as no numbers or 0.
  * Q: device [total_q][q_heads][128] of the set's dtype, element strides as above. out: device
  *   [total_q][q_heads][128] of that dtype; lse: device float32 [total_q][q_heads], the log of the
  *   sum of exponentials, prefix included, or NULL. prefix_out, prefix_lse: device float32
